@@ -6,7 +6,10 @@ finished tiles into per-destination slice buffers with ready flags; reducer
 workgroups sum this rank's slice with the peer partials as tiles are flagged.
 
 The C ABI is ``include/gemm_rs.h`` (``libgemm_rs.so``); ``gemm_rs`` is its
-ctypes binding.
+ctypes binding.  The operators around that layer (4-bit weights for decode, the
+norms, gate and residual after it with their gradients, 8-bit checkpoints and the
+weight gradient) are in ``layer`` (``include/gemm_rs_layer.h``,
+``libgemm_rs_layer.so``).
 """
 from .gemm_rs import (  # noqa: F401
     GemmRS, GemmRSError, gemm_rs_config, gemm_rs_info, make_config,

@@ -1,0 +1,133 @@
+// checkpoint.hip -- C entry points of the 8-bit checkpoint and the weight gradient
+// (gemm_rs_layer.h), and the error messages.
+#include "host.hpp"
+
+#include "checkpoint.hpp"
+
+using namespace gemm_rs_layer;
+
+extern "C" {
+
+const char* gemm_rs_layer_strerror(int code)
+{
+    switch (code) {
+    case GEMM_RS_OK: return "ok";
+    case GEMM_RS_ERR_INVALID_ARG: return "invalid argument";
+    case GEMM_RS_ERR_UNSUPPORTED_SHAPE: return "unsupported shape";
+    case GEMM_RS_ERR_MISALIGNED: return "misaligned buffer";
+    case GEMM_RS_ERR_NO_DEVICE: return "the current device is not a gfx950";
+    case GEMM_RS_ERR_HIP: return g_hip_msg[0] ? g_hip_msg : "HIP error";
+    case GEMM_RS_ERR_SCRATCH: return "workspace missing or too small";
+    default: return "unknown error";
+    }
+}
+
+static int ckpt_check(int32_t dtype, int64_t M, int64_t K, const void* x, int64_t stride, const void* q,
+                      const void* exps)
+{
+    if (dtype < GEMM_RS_DTYPE_BF16 || dtype > GEMM_RS_DTYPE_F32 || M < 0 || K < 1) return GEMM_RS_ERR_INVALID_ARG;
+    if (M >= kMaxRows || K > (1 << 24) || ceil_div(M * (ceil_div(K, 32) * 2), kCkptThreads) > 0x7FFFFFFF)
+        return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return GEMM_RS_OK;
+    Checker k;
+    k.need(x, elem_bytes(dtype));
+    k.stride(stride, K);
+    k.need(q, 16);
+    k.need(exps, 1);
+    return k.code;
+}
+
+static CkptArgs ckpt_args(int64_t M, int64_t K, int64_t stride)
+{
+    CkptArgs a = {};
+    a.rows = M;
+    a.stride = stride;
+    a.K = (int)K;
+    a.chunks = (int)ceil_div(K, 32) * 2;
+    return a;
+}
+
+int gemm_rs_ckpt_pack(int32_t dtype, int64_t M, int64_t K, const void* x, int64_t x_stride, void* q, void* exps,
+                      void* stream)
+{
+    int rc = ckpt_check(dtype, M, K, x, x_stride, q, exps);
+    if (rc != GEMM_RS_OK || M == 0) return rc;
+    if ((rc = check_device()) != GEMM_RS_OK) return rc;
+    CkptArgs a = ckpt_args(M, K, x_stride);
+    a.x = x;
+    a.q = static_cast<int8_t*>(q);
+    a.e = static_cast<int8_t*>(exps);
+    void (*kern)(CkptArgs) = dtype == GEMM_RS_DTYPE_BF16  ? ckpt_pack_kernel<__bf16>
+                             : dtype == GEMM_RS_DTYPE_F16 ? ckpt_pack_kernel<_Float16>
+                                                          : ckpt_pack_kernel<float>;
+    return launch(kern, dim3((unsigned)ceil_div(M * a.chunks, kCkptThreads)), kCkptThreads, a, stream, "gemm_rs_ckpt_pack");
+}
+
+int gemm_rs_ckpt_unpack(int32_t dtype, int64_t M, int64_t K, const void* q, const void* exps, void* x,
+                        int64_t x_stride, void* stream)
+{
+    int rc = ckpt_check(dtype, M, K, x, x_stride, q, exps);
+    if (rc != GEMM_RS_OK || M == 0) return rc;
+    if ((rc = check_device()) != GEMM_RS_OK) return rc;
+    CkptArgs a = ckpt_args(M, K, x_stride);
+    a.out = x;
+    a.q = static_cast<int8_t*>(const_cast<void*>(q));
+    a.e = static_cast<int8_t*>(const_cast<void*>(exps));
+    void (*kern)(CkptArgs) = dtype == GEMM_RS_DTYPE_BF16  ? ckpt_unpack_kernel<__bf16>
+                             : dtype == GEMM_RS_DTYPE_F16 ? ckpt_unpack_kernel<_Float16>
+                                                          : ckpt_unpack_kernel<float>;
+    return launch(kern, dim3((unsigned)ceil_div(M * a.chunks, kCkptThreads)), kCkptThreads, a, stream,
+                  "gemm_rs_ckpt_unpack");
+}
+
+static int wgrad_check(const gemm_rs_wgrad_args* g)
+{
+    if (!g || (g->dtype != GEMM_RS_DTYPE_BF16 && g->dtype != GEMM_RS_DTYPE_F16) ||
+        (g->out_dtype != g->dtype && g->out_dtype != GEMM_RS_DTYPE_F32) || g->M < 0 || g->N < 1 || g->K < 1)
+        return GEMM_RS_ERR_INVALID_ARG;
+    if (g->M >= kMaxRows || g->N > (1 << 24) || g->K > (1 << 24) || ceil_div(g->N, kWgTile) > 65535)
+        return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    return GEMM_RS_OK;
+}
+
+size_t gemm_rs_ckpt_wgrad_workspace(const gemm_rs_wgrad_args* g) { return 0; }
+
+int gemm_rs_ckpt_wgrad(const gemm_rs_wgrad_args* g, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int rc = wgrad_check(g);
+    if (rc != GEMM_RS_OK) return rc;
+    Checker k;
+    if (g->M > 0) {
+        k.need(g->dy, 2);
+        k.stride(g->dy_stride, g->N);
+        k.need(g->q, 16);
+        k.need(g->exps, 1);
+    }
+    k.maybe(g->add, 4);
+    if (g->add) k.stride(g->add_stride, g->K);
+    k.need(g->dw, elem_bytes(g->out_dtype));
+    k.stride(g->dw_stride, g->K);
+    if (g->add && g->add == g->dw && (g->out_dtype != GEMM_RS_DTYPE_F32 || g->add_stride != g->dw_stride))
+        k.fail(GEMM_RS_ERR_INVALID_ARG);
+    if (k.code != GEMM_RS_OK) return k.code;
+    if ((rc = check_device()) != GEMM_RS_OK) return rc;
+    WgradArgs a = {};
+    a.dy = g->dy;
+    a.q = static_cast<const int8_t*>(g->q);
+    a.e = static_cast<const int8_t*>(g->exps);
+    a.add = g->add;
+    a.dw = g->dw;
+    a.M = g->M;
+    a.dy_stride = g->dy_stride;
+    a.add_stride = g->add_stride;
+    a.dw_stride = g->dw_stride;
+    a.N = (int)g->N;
+    a.K = (int)g->K;
+    a.Kp = (int)ceil_div(g->K, 32) * 32;
+    a.out_f32 = g->out_dtype == GEMM_RS_DTYPE_F32;
+    const dim3 grid((unsigned)ceil_div(g->K, kWgTile), (unsigned)ceil_div(g->N, kWgTile));
+    return launch(g->dtype == GEMM_RS_DTYPE_BF16 ? wgrad_kernel<__bf16> : wgrad_kernel<_Float16>, grid, kWgThreads, a,
+                  stream, "gemm_rs_ckpt_wgrad");
+}
+
+}  // extern "C"

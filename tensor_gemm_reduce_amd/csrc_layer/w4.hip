@@ -1,0 +1,125 @@
+// w4.hip -- C entry points of the product with 4-bit weights (gemm_rs_layer.h).
+#include "host.hpp"
+
+#include "w4.hpp"
+
+using namespace gemm_rs_layer;
+
+namespace {
+
+W4Layout w4_layout(const gemm_rs_w4_config& c)
+{
+    W4Layout l;
+    l.N = c.N;
+    l.K = c.K;
+    l.group = c.group;
+    l.tiles = (int)ceil_div(c.N, kW4Tile);
+    l.blocks = (int)ceil_div(c.K, kW4Block);
+    l.groups = (int)ceil_div(c.K, c.group);
+    l.subs = c.group >= c.K || c.group % 128 == 0 ? 1 : c.group % 64 == 0 ? 2 : 4;
+    const int64_t tb = (int64_t)l.tiles * l.blocks;
+    l.scale_at = tb * 1024;
+    l.zero_at = l.scale_at + tb * kW4Tile * l.subs * 2;
+    l.bytes = l.zero_at + (c.zero_points ? tb * kW4Tile * l.subs : 0);
+    return l;
+}
+
+template <class T, int NT, int MF>
+int w4_launch(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
+{
+    constexpr int kWaves = 8;
+    const dim3 grid((unsigned)ceil_div(a.l.tiles, NT), (unsigned)ceil_div(a.M, 16 * MF));
+    auto go = [&](void (*k)(W4Args)) { return launch(k, grid, 64 * kWaves, a, stream, "gemm_rs_w4_linear"); };
+    if (c.zero_points) {
+        switch (a.l.subs) {
+        case 1: return go(w4_kernel<T, kWaves, NT, MF, 1, true>);
+        case 2: return go(w4_kernel<T, kWaves, NT, MF, 2, true>);
+        default: return go(w4_kernel<T, kWaves, NT, MF, 4, true>);
+        }
+    }
+    switch (a.l.subs) {
+    case 1: return go(w4_kernel<T, kWaves, NT, MF, 1, false>);
+    case 2: return go(w4_kernel<T, kWaves, NT, MF, 2, false>);
+    default: return go(w4_kernel<T, kWaves, NT, MF, 4, false>);
+    }
+}
+
+template <class T>
+int w4_run(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
+{
+    if (a.M <= 16) return w4_launch<T, 1, 1>(c, a, stream);
+    if (a.M <= 32) return w4_launch<T, 1, 2>(c, a, stream);
+    return w4_launch<T, 1, 4>(c, a, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_rs_w4_validate(const gemm_rs_w4_config* c)
+{
+    if (!c || c->N < 0 || c->K < 0 || c->group <= 0 || (c->zero_points != 0 && c->zero_points != 1) ||
+        (c->dtype != GEMM_RS_DTYPE_BF16 && c->dtype != GEMM_RS_DTYPE_F16))
+        return GEMM_RS_ERR_INVALID_ARG;
+    // tiles are counted in 32 bits by the launch grid, inputs by the kernels
+    if (c->K < 2 || c->K % 2 != 0 || c->K > (1 << 24) || c->N < 1 || c->N > (1 << 24) ||
+        ceil_div(c->N, kW4Tile) * ceil_div(c->K, kW4Block) > 0x7FFFFFFF)
+        return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (c->group % 32 != 0 && c->group != c->K) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    return GEMM_RS_OK;
+}
+
+size_t gemm_rs_w4_packed_bytes(const gemm_rs_w4_config* c)
+{
+    return gemm_rs_w4_validate(c) == GEMM_RS_OK ? (size_t)w4_layout(*c).bytes : 0;
+}
+
+int gemm_rs_w4_pack(const gemm_rs_w4_config* c, const void* q, const void* scales, const void* zeros, void* packed,
+                    void* stream)
+{
+    int rc = gemm_rs_w4_validate(c);
+    if (rc != GEMM_RS_OK) return rc;
+    Checker k;
+    k.need(q, 1);
+    k.need(scales, 2);
+    k.need(packed, 16);
+    if ((zeros != nullptr) != (c->zero_points != 0)) k.fail(GEMM_RS_ERR_INVALID_ARG);
+    if (k.code != GEMM_RS_OK) return k.code;
+    if ((rc = check_device()) != GEMM_RS_OK) return rc;
+    W4PackArgs a;
+    a.l = w4_layout(*c);
+    a.q = static_cast<const uint8_t*>(q);
+    a.scales = static_cast<const uint16_t*>(scales);
+    a.zeros = static_cast<const uint8_t*>(zeros);
+    a.packed = static_cast<char*>(packed);
+    return launch(w4_pack_kernel, dim3((unsigned)((int64_t)a.l.tiles * a.l.blocks)), 64, a, stream, "gemm_rs_w4_pack");
+}
+
+int gemm_rs_w4_linear(const gemm_rs_w4_config* c, const void* packed, int64_t M, const void* x, int64_t x_stride,
+                      void* y, int64_t y_stride, void* stream)
+{
+    int rc = gemm_rs_w4_validate(c);
+    if (rc != GEMM_RS_OK) return rc;
+    if (M < 0) return GEMM_RS_ERR_INVALID_ARG;
+    if (M > (1 << 20)) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return GEMM_RS_OK;
+    Checker k;
+    k.need(packed, 16);
+    k.need(x, 2);
+    k.need(y, 2);
+    k.stride(x_stride, c->K);
+    k.stride(y_stride, c->N);
+    if (k.code != GEMM_RS_OK) return k.code;
+    if ((rc = check_device()) != GEMM_RS_OK) return rc;
+    W4Args a;
+    a.l = w4_layout(*c);
+    a.packed = static_cast<const char*>(packed);
+    a.x = x;
+    a.y = y;
+    a.M = M;
+    a.x_stride = x_stride;
+    a.y_stride = y_stride;
+    return c->dtype == GEMM_RS_DTYPE_BF16 ? w4_run<__bf16>(*c, a, stream) : w4_run<_Float16>(*c, a, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,519 @@
+"""ctypes binding of libgemm_rs_layer.so (include/gemm_rs_layer.h): the operators
+around the row-parallel layer.
+
+  w4_pack, w4_linear                  4-bit weights for a few tokens (decode)
+  block_norm, block_norm_backward     slice sum, norms, gate and residual
+  ckpt_pack, ckpt_unpack, ckpt_wgrad  activations kept in 8 bits, weight gradient
+
+Argument checks and marshalling only: every step runs in the HIP kernels of the
+library.  Tensors live on the current device; rows may be strided, elements of a
+row are adjacent.  Work is enqueued on ``stream`` (a torch stream or a raw
+handle; default: torch's current stream) and calls return at once; outputs
+and workspaces come from torch's allocator on that stream.
+
+If the library is missing this module raises ImportError on first use: there is
+no fallback path.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import torch
+
+from . import build as _build
+from .gemm_rs import ERR_INVALID_ARG, OK  # noqa: F401
+
+# ---- constants mirrored from include/gemm_rs_layer.h --------------------------
+DTYPE_BF16 = 0
+DTYPE_F16 = 1
+DTYPE_F32 = 2
+GATE_NONE = 0
+GATE_CHANNEL = 1
+GATE_TOKEN = 2
+GATE_FULL = 3
+NORM_MAX_PARTS = 8
+NORM_MAX_WIDTH = 32768
+CKPT_BLOCK = 32
+CKPT_NAN = 127
+
+EXPORTS = ("gemm_rs_layer_strerror", "gemm_rs_w4_validate", "gemm_rs_w4_packed_bytes", "gemm_rs_w4_pack",
+           "gemm_rs_w4_linear", "gemm_rs_norm_validate", "gemm_rs_block_norm", "gemm_rs_block_norm_workspace",
+           "gemm_rs_block_norm_backward", "gemm_rs_ckpt_pack", "gemm_rs_ckpt_unpack",
+           "gemm_rs_ckpt_wgrad_workspace", "gemm_rs_ckpt_wgrad")
+
+_CODES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+
+_vp, _i32, _i64, _f32, _size = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t)
+
+
+class gemm_rs_w4_config(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("N", "K", "group", "dtype", "zero_points")]
+
+
+class gemm_rs_norm_config(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("width", "dtype", "residual_dtype", "parts", "gate", "post_norm", "pre_norm")] + [
+        (n, _f32) for n in ("eps", "block_scale", "residual_scale")]
+
+
+class gemm_rs_norm_args(ctypes.Structure):
+    _fields_ = [("parts", _vp * NORM_MAX_PARTS), ("part_stride", _i64), ("residual", _vp), ("residual_stride", _i64),
+                ("post_weight", _vp), ("gate", _vp), ("gate_stride", _i64), ("pre_weight", _vp), ("h", _vp),
+                ("h_stride", _i64), ("z", _vp), ("z_stride", _i64), ("y", _vp), ("y_stride", _i64), ("rstd", _vp)]
+
+
+class gemm_rs_norm_grad_args(ctypes.Structure):
+    _fields_ = [("dz", _vp), ("dz_stride", _i64), ("dh", _vp), ("dh_stride", _i64), ("h", _vp), ("h_stride", _i64),
+                ("y", _vp), ("y_stride", _i64), ("rstd", _vp), ("post_weight", _vp), ("gate", _vp),
+                ("pre_weight", _vp), ("gate_stride", _i64), ("dresidual", _vp), ("dresidual_stride", _i64),
+                ("dy", _vp), ("dy_stride", _i64), ("dpre_weight", _vp), ("dpost_weight", _vp), ("dgate", _vp),
+                ("dgate_stride", _i64)]
+
+
+class gemm_rs_wgrad_args(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("out_dtype", _i32), ("M", _i64), ("N", _i64), ("K", _i64), ("dy", _vp),
+                ("dy_stride", _i64), ("q", _vp), ("exps", _vp), ("add", _vp), ("add_stride", _i64), ("dw", _vp),
+                ("dw_stride", _i64)]
+
+
+_LIB = None
+
+
+def library_path() -> str:
+    return _build.layer_library_path()
+
+
+def lib():
+    global _LIB
+    if _LIB is None:
+        path = library_path()
+        if not os.path.exists(path):
+            raise ImportError(
+                f"{path} is missing: build it with `python -m tensor_gemm_reduce_amd.build` "
+                "(there is no fallback implementation)")
+        L = ctypes.CDLL(path)
+        P = ctypes.POINTER
+        w4, norm, wg = P(gemm_rs_w4_config), P(gemm_rs_norm_config), P(gemm_rs_wgrad_args)
+        L.gemm_rs_layer_strerror.argtypes = [ctypes.c_int]
+        L.gemm_rs_layer_strerror.restype = ctypes.c_char_p
+        L.gemm_rs_w4_validate.argtypes = [w4]
+        L.gemm_rs_w4_packed_bytes.argtypes = [w4]
+        L.gemm_rs_w4_pack.argtypes = [w4, _vp, _vp, _vp, _vp, _vp]
+        L.gemm_rs_w4_linear.argtypes = [w4, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+        L.gemm_rs_norm_validate.argtypes = [norm]
+        L.gemm_rs_block_norm.argtypes = [norm, _i64, P(gemm_rs_norm_args), _vp]
+        L.gemm_rs_block_norm_workspace.argtypes = [norm, _i64]
+        L.gemm_rs_block_norm_backward.argtypes = [norm, _i64, P(gemm_rs_norm_grad_args), _vp, _size, _vp]
+        L.gemm_rs_ckpt_pack.argtypes = [_i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp]
+        L.gemm_rs_ckpt_unpack.argtypes = [_i32, _i64, _i64, _vp, _vp, _vp, _i64, _vp]
+        L.gemm_rs_ckpt_wgrad_workspace.argtypes = [wg]
+        L.gemm_rs_ckpt_wgrad.argtypes = [wg, _vp, _size, _vp]
+        for name in EXPORTS[1:]:
+            getattr(L, name).restype = _size if name.endswith(("_bytes", "_workspace")) else ctypes.c_int
+        _LIB = L
+    return _LIB
+
+
+class GemmRSLayerError(RuntimeError):
+    def __init__(self, code: int, what: str):
+        self.code = code
+        super().__init__(f"{what}: {lib().gemm_rs_layer_strerror(code).decode()} ({code})")
+
+
+def _check(code: int, what: str) -> None:
+    if code != OK:
+        raise GemmRSLayerError(code, what)
+
+
+# ---- argument checks ------------------------------------------------------------
+
+def _rows(t, name, shape, dtype):
+    """Checks a [rows][width] tensor with adjacent row elements; returns its row stride."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    rows, width = shape
+    s0, s1 = t.stride()
+    if not t.is_cuda or (s1 != 1 and width != 1) or (s0 < width and rows > 1):
+        raise ValueError(f"{name}: must be a device tensor whose rows hold their elements side by side")
+    return s0 if rows > 1 else max(s0, width)
+
+
+def _flat(t, name, shape, dtype):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: must be a contiguous device tensor")
+
+
+def _two(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected two dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {first.device}, but the current device is {torch.cuda.current_device()}")
+
+
+def _current(device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _elsewhere(stream, device):
+    """None, or the torch stream to switch to for a call whose `stream` is not the current one."""
+    if stream is None:
+        return None
+    raw = stream if isinstance(stream, int) else stream.cuda_stream
+    if raw == _current(device):
+        return None
+    return torch.cuda.ExternalStream(raw, device=device) if isinstance(stream, int) else stream
+
+
+def _on_stream(call, stream, inputs, *args, **kw):
+    """Runs call(...) with `stream` as torch's current stream, so that its outputs and
+    workspace belong to that stream, and tells the allocator that the inputs are used there."""
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+    return out
+
+
+# ---- 4-bit weights -----------------------------------------------------------------
+
+class W4Weight:
+    """Weights of w4_linear as w4_pack laid them out: w[n][k] = scale[n][k // group] (q[n][k] - zero[n][k // group])."""
+
+    __slots__ = ("packed", "cfg", "ref", "N", "K", "group", "dtype")
+
+    def __init__(self, packed, cfg, dtype):
+        self.packed, self.cfg, self.dtype = packed, cfg, dtype
+        self.ref = ctypes.byref(cfg)
+        self.N, self.K, self.group = cfg.N, cfg.K, cfg.group
+
+
+def w4_pack(q, scales, zeros=None, *, group, stream=None) -> W4Weight:
+    """Lays 4-bit weights out for w4_linear, once.
+
+    q: uint8 [N][K / 2], input k of a row in byte k // 2, even k in the low half;
+    scales: bf16 or f16 [N][ceil(K / group)], also the type of x and y;
+    zeros: uint8 of the scales' shape (0 .. 15), or None for 8 everywhere.
+    group: a multiple of 32, or K.
+    """
+    N, half = _two(q, "q")
+    if scales.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"scales: expected bfloat16 or float16, got {scales.dtype}")
+    cfg = gemm_rs_w4_config(N, 2 * half, group, _CODES[scales.dtype], int(zeros is not None))
+    L = lib()
+    _check(L.gemm_rs_w4_validate(ctypes.byref(cfg)), "gemm_rs_w4_validate")
+    shape = (N, -(-cfg.K // group))
+    _flat(q, "q", (N, half), torch.uint8)
+    _flat(scales, "scales", shape, scales.dtype)
+    if zeros is not None:
+        _flat(zeros, "zeros", shape, torch.uint8)
+    _same_device(q, scales, zeros)
+    other = _elsewhere(stream, q.device)
+    if other is not None:
+        return _on_stream(w4_pack, other, (q, scales, zeros), q, scales, zeros, group=group)
+    packed = torch.empty(L.gemm_rs_w4_packed_bytes(ctypes.byref(cfg)), dtype=torch.uint8, device=q.device)
+    _check(L.gemm_rs_w4_pack(ctypes.byref(cfg), q.data_ptr(), scales.data_ptr(),
+                             None if zeros is None else zeros.data_ptr(), packed.data_ptr(), _current(q.device)),
+           "gemm_rs_w4_pack")
+    return W4Weight(packed, cfg, scales.dtype)
+
+
+def w4_linear(x, weight: W4Weight, out=None, *, stream=None):
+    """y = x w^T for x [M][K] (any M; made for few rows), FP32 accumulation, rounded once to x's type."""
+    M, _ = _two(x, "x")
+    xs = _rows(x, "x", (M, weight.K), weight.dtype)
+    if out is not None:
+        ys = _rows(out, "out", (M, weight.N), weight.dtype)
+    _same_device(x, weight.packed, out)
+    other = _elsewhere(stream, x.device)
+    if other is not None:
+        return _on_stream(w4_linear, other, (x, weight.packed, out), x, weight, out)
+    if out is None:
+        out, ys = x.new_empty((M, weight.N)), weight.N
+    _check(lib().gemm_rs_w4_linear(weight.ref, weight.packed.data_ptr(), M, x.data_ptr(), xs, out.data_ptr(), ys,
+                                   _current(x.device)), "gemm_rs_w4_linear")
+    return out
+
+
+# ---- block norm -----------------------------------------------------------------------
+
+class BlockNorm:
+    """Outputs of block_norm: h, z (None without a pre weight), and with save=True y and rstd."""
+
+    __slots__ = ("h", "z", "y", "rstd")
+
+    def __init__(self, h, z, y, rstd):
+        self.h, self.z, self.y, self.rstd = h, z, y, rstd
+
+
+class BlockNormGrads:
+    """Gradients from block_norm_backward; None for what the forward pass did not have."""
+
+    __slots__ = ("residual", "y", "pre_weight", "post_weight", "gate")
+
+    def __init__(self, residual, y, pre_weight, post_weight, gate):
+        self.residual, self.y, self.pre_weight, self.post_weight, self.gate = residual, y, pre_weight, post_weight, gate
+
+
+def _gate(gate, S, N, dtype):
+    """(kind, row stride) of a gate: [N] for every row, [S][1] per row or [S][N]."""
+    if gate is None:
+        return GATE_NONE, 0
+    if gate.dim() == 1:
+        _flat(gate, "gate", (N,), dtype)
+        return GATE_CHANNEL, 0
+    if gate.shape == (S, 1) and N != 1:
+        _flat(gate, "gate", (S, 1), dtype)
+        return GATE_TOKEN, 0
+    return GATE_FULL, _rows(gate, "gate", (S, N), dtype)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def block_norm(parts, residual=None, *, pre_weight=None, post_weight=None, gate=None, block_scale=1.0,
+               residual_scale=1.0, eps=1e-5, save=False, h=None, z=None, stream=None) -> BlockNorm:
+    """What follows the row-parallel layer, in one pass over each row (FP32, one rounding per output):
+
+      y = sum of the parts;  u = y / rms(y) * post_weight (y itself without a post weight)
+      h = residual_scale * residual + block_scale * gate * u
+      z = h / rms(h) * pre_weight (no z without a pre weight),  rms(t) = sqrt(mean(t^2) + eps)
+
+    parts: a [S][N] tensor, a list of 1 .. 8 of them, or a [P][S][N] tensor: the ranks' partials in the order they
+    are added.  residual and h: parts' type or float32 (h has the residual's type; parts' without one).
+    gate: [N], [S][1] or [S][N].  h may be the residual itself, to update it in place.
+    save=True also returns y and rstd ([2][S] float32: 1 / rms(y), 1 / rms(h)) for block_norm_backward.
+    """
+    if isinstance(parts, torch.Tensor):
+        parts = list(parts.unbind(0)) if parts.dim() == 3 else [parts]
+    if not 1 <= len(parts) <= NORM_MAX_PARTS:
+        raise ValueError(f"parts: 1 to {NORM_MAX_PARTS}, got {len(parts)}")
+    first = parts[0]
+    S, N = shape = _two(first, "parts[0]")
+    dtype = first.dtype
+    if dtype not in _CODES:
+        raise TypeError(f"parts: expected bfloat16, float16 or float32, got {dtype}")
+    a = gemm_rs_norm_args()
+    for i, p in enumerate(parts):
+        stride = _rows(p, f"parts[{i}]", shape, dtype)
+        if i == 0:
+            a.part_stride = stride
+        elif stride != a.part_stride:
+            raise ValueError(f"parts[{i}]: row stride {stride} != {a.part_stride} of parts[0]")
+        a.parts[i] = p.data_ptr()
+    rdtype = dtype
+    if residual is not None:
+        rdtype = residual.dtype
+        if rdtype is not dtype and rdtype is not torch.float32:
+            raise TypeError(f"residual: expected {dtype} or float32, got {rdtype}")
+        a.residual, a.residual_stride = residual.data_ptr(), _rows(residual, "residual", shape, rdtype)
+    elif h is not None:
+        rdtype = h.dtype if h.dtype is torch.float32 else dtype
+    kind, a.gate_stride = _gate(gate, S, N, dtype)
+    a.gate = _ptr(gate)
+    for t, name in ((pre_weight, "pre_weight"), (post_weight, "post_weight")):
+        if t is not None:
+            _flat(t, name, (N,), dtype)
+            setattr(a, name, t.data_ptr())
+    if z is not None and pre_weight is None:
+        raise ValueError("z: needs a pre_weight")
+    _same_device(first, *parts, residual, gate, pre_weight, post_weight, h, z)
+    other = _elsewhere(stream, first.device)
+    if other is not None:
+        return _on_stream(block_norm, other, (*parts, residual, gate, pre_weight, post_weight, h, z), parts, residual,
+                          pre_weight=pre_weight, post_weight=post_weight, gate=gate, block_scale=block_scale,
+                          residual_scale=residual_scale, eps=eps, save=save, h=h, z=z)
+    new = first.new_empty
+    if h is None:
+        h = new(shape, dtype=rdtype)
+    a.h, a.h_stride = h.data_ptr(), _rows(h, "h", shape, rdtype)
+    if pre_weight is not None:
+        if z is None:
+            z = new(shape)
+        a.z, a.z_stride = z.data_ptr(), _rows(z, "z", shape, dtype)
+    y = rstd = None
+    if save:
+        y, rstd = new(shape), new((2, S), dtype=torch.float32)
+        a.y, a.y_stride, a.rstd = y.data_ptr(), N, rstd.data_ptr()
+    cfg = gemm_rs_norm_config(N, _CODES[dtype], _CODES[rdtype], len(parts), kind, int(post_weight is not None),
+                              int(pre_weight is not None), eps, block_scale, residual_scale)
+    _check(lib().gemm_rs_block_norm(ctypes.byref(cfg), S, ctypes.byref(a), _current(first.device)), "gemm_rs_block_norm")
+    return BlockNorm(h, z, y, rstd)
+
+
+def block_norm_backward(dz, dh, h, y, rstd, *, pre_weight=None, post_weight=None, gate=None, block_scale=1.0,
+                        residual_scale=1.0, stream=None) -> BlockNormGrads:
+    """Gradients of block_norm's inputs from dz (None without a pre weight) and dh (None: zero).
+
+    h, y, rstd: what block_norm(save=True) returned; h is only read with a pre weight, y only with a post weight or a
+    gate (either may then be None).  Every part's gradient is .y.  Weight and [N]-gate gradients are float32, sums over
+    rows in a fixed order; .residual has the residual's type.
+    """
+    like = dz if dz is not None else y
+    if like is None:
+        raise ValueError("dz or y is needed")
+    S, N = shape = _two(like, "dz" if dz is not None else "y")
+    dtype = like.dtype
+    if dtype not in _CODES:
+        raise TypeError(f"dz, y: expected bfloat16, float16 or float32, got {dtype}")
+    stream_of = dh if dh is not None else h
+    rdtype = dtype if stream_of is None else stream_of.dtype
+    if rdtype is not dtype and rdtype is not torch.float32:
+        raise TypeError(f"dh, h: expected {dtype} or float32, got {rdtype}")
+    a = gemm_rs_norm_grad_args()
+    kind, a.gate_stride = _gate(gate, S, N, dtype)
+    a.gate = _ptr(gate)
+    if pre_weight is not None:
+        if dz is None or h is None:
+            raise ValueError("a pre_weight needs dz and h")
+        _flat(pre_weight, "pre_weight", (N,), dtype)
+        a.pre_weight = pre_weight.data_ptr()
+        a.dz, a.dz_stride = dz.data_ptr(), _rows(dz, "dz", shape, dtype)
+        a.h, a.h_stride = h.data_ptr(), _rows(h, "h", shape, rdtype)
+    if post_weight is not None:
+        _flat(post_weight, "post_weight", (N,), dtype)
+        a.post_weight = post_weight.data_ptr()
+    if post_weight is not None or gate is not None:
+        if y is None:
+            raise ValueError("a post_weight or a gate needs y")
+        a.y, a.y_stride = y.data_ptr(), _rows(y, "y", shape, dtype)
+    if pre_weight is not None or post_weight is not None:
+        if rstd is None:
+            raise ValueError("a pre_weight or post_weight needs rstd")
+        _flat(rstd, "rstd", (2, S), torch.float32)
+        a.rstd = rstd.data_ptr()
+    if dh is not None:
+        a.dh, a.dh_stride = dh.data_ptr(), _rows(dh, "dh", shape, rdtype)
+    _same_device(like, dz, dh, h, y, rstd, pre_weight, post_weight, gate)
+    other = _elsewhere(stream, like.device)
+    if other is not None:
+        return _on_stream(block_norm_backward, other, (dz, dh, h, y, rstd, pre_weight, post_weight, gate), dz, dh, h, y,
+                          rstd, pre_weight=pre_weight, post_weight=post_weight, gate=gate, block_scale=block_scale,
+                          residual_scale=residual_scale)
+    new = like.new_empty
+    dres, dy = new(shape, dtype=rdtype), new(shape)
+    a.dresidual, a.dresidual_stride, a.dy, a.dy_stride = dres.data_ptr(), N, dy.data_ptr(), N
+    dpre = new(N, dtype=torch.float32) if pre_weight is not None else None
+    dpost = new(N, dtype=torch.float32) if post_weight is not None else None
+    dgate = None
+    if kind == GATE_CHANNEL:
+        dgate = new(N, dtype=torch.float32)
+    elif kind != GATE_NONE:
+        dgate = new(gate.shape)
+        a.dgate_stride = N
+    a.dpre_weight, a.dpost_weight, a.dgate = _ptr(dpre), _ptr(dpost), _ptr(dgate)
+    cfg = gemm_rs_norm_config(N, _CODES[dtype], _CODES[rdtype], 1, kind, int(post_weight is not None),
+                              int(pre_weight is not None), 0.0, block_scale, residual_scale)
+    L, ref = lib(), ctypes.byref(cfg)
+    size = L.gemm_rs_block_norm_workspace(ref, S)
+    ws = new(size, dtype=torch.uint8)
+    _check(L.gemm_rs_block_norm_backward(ref, S, ctypes.byref(a), ws.data_ptr(), size, _current(like.device)),
+           "gemm_rs_block_norm_backward")
+    return BlockNormGrads(dres, dy, dpre, dpost, dgate)
+
+
+# ---- 8-bit checkpoints -----------------------------------------------------------------
+
+class Checkpoint:
+    """An activation [M][K] kept in 8 bits: q int8 [M][K rounded up to 32], exps int8 [M][that / 32], and the type it
+    had.  A block of 32 columns stands for q 2^exp (exp 127: the block held an infinity or a NaN, and stands for NaN)."""
+
+    __slots__ = ("q", "exps", "K", "dtype")
+
+    def __init__(self, q, exps, K, dtype):
+        blocks = -(-K // CKPT_BLOCK)
+        M, _ = _two(q, "q")
+        if dtype not in _CODES:
+            raise TypeError(f"dtype: expected bfloat16, float16 or float32, got {dtype}")
+        _flat(q, "q", (M, blocks * CKPT_BLOCK), torch.int8)
+        _flat(exps, "exps", (M, blocks), torch.int8)
+        self.q, self.exps, self.K, self.dtype = q, exps, K, dtype
+
+
+def ckpt_pack(x, *, stream=None) -> Checkpoint:
+    """Keeps x [M][K] (bfloat16, float16 or float32) in 8 bits: round(x 2^-e) with e = floor(log2(max |x|)) - 6 for
+    every 32 columns of a row."""
+    M, K = _two(x, "x")
+    if x.dtype not in _CODES:
+        raise TypeError(f"x: expected bfloat16, float16 or float32, got {x.dtype}")
+    if K < 1:
+        raise ValueError("x: needs at least one column")
+    xs = _rows(x, "x", (M, K), x.dtype)
+    _same_device(x)
+    other = _elsewhere(stream, x.device)
+    if other is not None:
+        return _on_stream(ckpt_pack, other, (x,), x)
+    blocks = -(-K // CKPT_BLOCK)
+    q = x.new_empty((M, blocks * CKPT_BLOCK), dtype=torch.int8)
+    exps = x.new_empty((M, blocks), dtype=torch.int8)
+    _check(lib().gemm_rs_ckpt_pack(_CODES[x.dtype], M, K, x.data_ptr(), xs, q.data_ptr(), exps.data_ptr(),
+                                   _current(x.device)), "gemm_rs_ckpt_pack")
+    return Checkpoint(q, exps, K, x.dtype)
+
+
+def ckpt_unpack(kept: Checkpoint, out=None, *, stream=None):
+    """The values a checkpoint stands for, in the type it was made from."""
+    shape = (kept.q.shape[0], kept.K)
+    if out is not None:
+        stride = _rows(out, "out", shape, kept.dtype)
+    _same_device(kept.q, kept.exps, out)
+    other = _elsewhere(stream, kept.q.device)
+    if other is not None:
+        return _on_stream(ckpt_unpack, other, (kept.q, kept.exps, out), kept, out)
+    if out is None:
+        out, stride = kept.q.new_empty(shape, dtype=kept.dtype), kept.K
+    _check(lib().gemm_rs_ckpt_unpack(_CODES[kept.dtype], shape[0], kept.K, kept.q.data_ptr(), kept.exps.data_ptr(),
+                                     out.data_ptr(), stride, _current(out.device)), "gemm_rs_ckpt_unpack")
+    return out
+
+
+def ckpt_wgrad(dy, kept: Checkpoint, *, add=None, out=None, dtype=torch.float32, stream=None):
+    """The weight gradient dw [N][K] = dy^T x^ (+ add) of a linear layer whose input was kept as `kept`.
+
+    dy: [M][N] bfloat16 or float16 (float16 needs a checkpoint of a float16 activation).  add: float32 [N][K] or None.
+    dtype: float32 or dy's (out's, if given).  out may be `add` (float32): gradients accumulated in place.
+    """
+    M, N = _two(dy, "dy")
+    if dy.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"dy: expected bfloat16 or float16, got {dy.dtype}")
+    if dy.dtype is torch.float16 and kept.dtype is not torch.float16:
+        raise TypeError(f"dy: float16 with a checkpoint of {kept.dtype}")
+    if kept.q.shape[0] != M:
+        raise ValueError(f"dy has {M} rows, the checkpoint {kept.q.shape[0]}")
+    K = kept.K
+    if out is not None:
+        dtype = out.dtype
+    if dtype is not torch.float32 and dtype is not dy.dtype:
+        raise TypeError(f"dtype: expected float32 or {dy.dtype}, got {dtype}")
+    a = gemm_rs_wgrad_args(_CODES[dy.dtype], _CODES[dtype], M, N, K, dy.data_ptr(), _rows(dy, "dy", (M, N), dy.dtype),
+                           kept.q.data_ptr(), kept.exps.data_ptr())
+    if add is not None:
+        a.add, a.add_stride = add.data_ptr(), _rows(add, "add", (N, K), torch.float32)
+    if out is not None:
+        a.dw, a.dw_stride = out.data_ptr(), _rows(out, "out", (N, K), dtype)
+    _same_device(dy, kept.q, kept.exps, add, out)
+    other = _elsewhere(stream, dy.device)
+    if other is not None:
+        return _on_stream(ckpt_wgrad, other, (dy, kept.q, kept.exps, add, out), dy, kept, add=add, out=out, dtype=dtype)
+    if out is None:
+        out = dy.new_empty((N, K), dtype=dtype)
+        a.dw, a.dw_stride = out.data_ptr(), K
+    L, ref = lib(), ctypes.byref(a)
+    size = L.gemm_rs_ckpt_wgrad_workspace(ref)
+    ws = dy.new_empty(size, dtype=torch.uint8)
+    _check(L.gemm_rs_ckpt_wgrad(ref, ws.data_ptr(), size, _current(dy.device)), "gemm_rs_ckpt_wgrad")
+    return out
