@@ -6,6 +6,64 @@
 
 using namespace gemm_rs_layer;
 
+namespace {
+
+// dy in whole 4-byte words (buffer loads check bounds by the word), and 64 of its rows
+// within a buffer resource's 2^31 bytes.
+bool wgrad_fast(const gemm_rs_wgrad_args& g)
+{
+    return g.M > 0 && aligned(g.dy, 4) && g.dy_stride % 2 == 0 && g.N % 2 == 0 && g.dy_stride < (1 << 23);
+}
+
+constexpr int kCus = 256;         // compute units of an MI355X
+constexpr int kWgMinSteps = 4;    // a share is at least this many steps of 64 tokens
+
+WgradPlan wgrad_plan(const gemm_rs_wgrad_args& g, int& big)
+{
+    auto tiles = [&](int t) { return ceil_div(g.N, t) * ceil_div(g.K, t); };
+    big = tiles(256) >= kCus / 2;
+    const int edge = big ? 256 : 128, slots = big ? kCus : 2 * kCus;
+    WgradPlan p = {};
+    p.tiles_n = (int)ceil_div(g.N, edge);
+    p.tiles_k = (int)ceil_div(g.K, edge);
+    p.steps = ceil_div(g.M, kWgRows);
+    const int64_t all = (int64_t)p.tiles_n * p.tiles_k, rest = all % slots;
+    p.full = (int)(all - rest);
+    int64_t shares = rest * p.steps / kWgMinSteps;
+    shares = shares < slots ? shares : slots;
+    if (shares <= rest) {  // nothing to gain from cutting them
+        p.full = (int)all;
+        shares = 0;
+    }
+    p.shares = (int)shares;
+    p.grid = (int)(p.full >= slots || shares >= slots ? slots : p.full > shares ? p.full : shares);
+    return p;
+}
+
+template <class A, class B>
+int launch2(void (*kernel)(A, B), dim3 grid, int lds, const A& a, const B& b, void* stream)
+{
+    void* p[] = {const_cast<A*>(&a), const_cast<B*>(&b)};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kWgThreads), p, lds,
+                                         static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? GEMM_RS_OK : hip_fail(e, "gemm_rs_ckpt_wgrad");
+}
+
+template <class T, int WN, int WK>
+int wgrad_run(const WgradArgs& a, const WgradPlan& p, void* stream)
+{
+    constexpr int kLds = WgradTile<WN, WK>::kLds;
+    static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(wgrad_kernel<T, WN, WK>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (allowed != hipSuccess) return hip_fail(allowed, "hipFuncSetAttribute");
+    int rc = launch2(wgrad_kernel<T, WN, WK>, dim3((unsigned)p.grid), kLds, a, p, stream);
+    if (rc != GEMM_RS_OK || p.shares == 0) return rc;
+    const int64_t rest = (int64_t)p.tiles_n * p.tiles_k - p.full;
+    return launch2(wgrad_join_kernel<T, WN, WK>, dim3((unsigned)rest, WN), 0, a, p, stream);
+}
+
+}  // namespace
+
 extern "C" {
 
 const char* gemm_rs_layer_strerror(int code)
@@ -85,12 +143,17 @@ static int wgrad_check(const gemm_rs_wgrad_args* g)
     if (!g || (g->dtype != GEMM_RS_DTYPE_BF16 && g->dtype != GEMM_RS_DTYPE_F16) ||
         (g->out_dtype != g->dtype && g->out_dtype != GEMM_RS_DTYPE_F32) || g->M < 0 || g->N < 1 || g->K < 1)
         return GEMM_RS_ERR_INVALID_ARG;
-    if (g->M >= kMaxRows || g->N > (1 << 24) || g->K > (1 << 24) || ceil_div(g->N, kWgTile) > 65535)
-        return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (g->M >= kMaxRows || g->N > (1 << 22) || g->K > (1 << 22)) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     return GEMM_RS_OK;
 }
 
-size_t gemm_rs_ckpt_wgrad_workspace(const gemm_rs_wgrad_args* g) { return 0; }
+size_t gemm_rs_ckpt_wgrad_workspace(const gemm_rs_wgrad_args* g)
+{
+    if (wgrad_check(g) != GEMM_RS_OK || !wgrad_fast(*g)) return 0;
+    int big;
+    const WgradPlan p = wgrad_plan(*g, big);
+    return (size_t)p.shares * 2 * (big ? WgradTile<4, 4>::kFloats : WgradTile<2, 2>::kFloats) * sizeof(float);
+}
 
 int gemm_rs_ckpt_wgrad(const gemm_rs_wgrad_args* g, void* workspace, size_t workspace_bytes, void* stream)
 {
@@ -109,6 +172,11 @@ int gemm_rs_ckpt_wgrad(const gemm_rs_wgrad_args* g, void* workspace, size_t work
     k.stride(g->dw_stride, g->K);
     if (g->add && g->add == g->dw && (g->out_dtype != GEMM_RS_DTYPE_F32 || g->add_stride != g->dw_stride))
         k.fail(GEMM_RS_ERR_INVALID_ARG);
+    const size_t ws = gemm_rs_ckpt_wgrad_workspace(g);
+    if (ws > 0) {
+        if (workspace_bytes < ws || !workspace) k.fail(GEMM_RS_ERR_SCRATCH);
+        else k.need(workspace, 16);
+    }
     if (k.code != GEMM_RS_OK) return k.code;
     if ((rc = check_device()) != GEMM_RS_OK) return rc;
     WgradArgs a = {};
@@ -125,9 +193,17 @@ int gemm_rs_ckpt_wgrad(const gemm_rs_wgrad_args* g, void* workspace, size_t work
     a.K = (int)g->K;
     a.Kp = (int)ceil_div(g->K, 32) * 32;
     a.out_f32 = g->out_dtype == GEMM_RS_DTYPE_F32;
-    const dim3 grid((unsigned)ceil_div(g->K, kWgTile), (unsigned)ceil_div(g->N, kWgTile));
-    return launch(g->dtype == GEMM_RS_DTYPE_BF16 ? wgrad_kernel<__bf16> : wgrad_kernel<_Float16>, grid, kWgThreads, a,
-                  stream, "gemm_rs_ckpt_wgrad");
+    const bool bf16 = g->dtype == GEMM_RS_DTYPE_BF16;
+    if (!wgrad_fast(*g)) {
+        const dim3 grid((unsigned)ceil_div(g->K, kWgTile), (unsigned)ceil_div(g->N, kWgTile));
+        return launch(bf16 ? wgrad_any_kernel<__bf16> : wgrad_any_kernel<_Float16>, grid, kWgThreads, a, stream,
+                      "gemm_rs_ckpt_wgrad");
+    }
+    int big;
+    WgradPlan p = wgrad_plan(*g, big);
+    p.pieces = static_cast<float*>(workspace);
+    if (bf16) return big ? wgrad_run<__bf16, 4, 4>(a, p, stream) : wgrad_run<__bf16, 2, 2>(a, p, stream);
+    return big ? wgrad_run<_Float16, 4, 4>(a, p, stream) : wgrad_run<_Float16, 2, 2>(a, p, stream);
 }
 
 }  // extern "C"

@@ -155,19 +155,67 @@ __device__ __forceinline__ F read_column8(const char* p, int pitch)
     return __builtin_bit_cast(F, v);
 }
 
-// dw = dy^T x^: 128 x 128 outputs per workgroup, four waves of 64 x 64, 32 tokens
-// a step.  Both operands are token-major in memory, the MFMA wants eight tokens of
+// A lane of a 32 x 32 block of accumulators holds row n (lane % 32), and per group of
+// four accumulators four consecutive columns k.  Results leave through LDS so that
+// 32 WK / 4 lanes store one row's columns side by side: `area` is the wave's own,
+// 32 rows x 32 WK floats, 16-byte chunk c of row r at c ^ r.
+template <class T, int WK>
+__device__ __forceinline__ void wgrad_store_rows(const WgradArgs& a, char* area, int n0, int k0, const f32x16 (&acc)[WK])
+{
+    constexpr int kPer = 8 * WK, kRows = 64 / kPer;  // lanes per row, rows per instruction
+    typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+    typedef T t4 __attribute__((ext_vector_type(4), aligned(2)));
+    const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
+    __asm__ __volatile__("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < WK; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<f32x4*>(area + (r * kPer + ((8 * j + 2 * g + half) ^ (r & (kPer - 1)))) * 16) =
+                f32x4{acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
+    // the LDS operations of a wave complete in order
+    __asm__ __volatile__("" ::: "memory");
+    const int c = lane % kPer, k = k0 + 4 * c;
+#pragma unroll 4
+    for (int i = 0; i < 32 / kRows; ++i) {
+        const int row = i * kRows + lane / kPer, n = n0 + row;
+        f32x4 v = *reinterpret_cast<const f32x4*>(area + (row * kPer + (c ^ (row & (kPer - 1)))) * 16);
+        if (n >= a.N || k >= a.K) continue;
+        if (k + 4 <= a.K) {
+            if (a.add) v += *reinterpret_cast<const f4*>(a.add + n * a.add_stride + k);
+            if (a.out_f32)
+                *reinterpret_cast<f4*>(static_cast<float*>(a.dw) + n * a.dw_stride + k) = v;
+            else
+                *reinterpret_cast<t4*>(static_cast<T*>(a.dw) + n * a.dw_stride + k) = t4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                if (k + e >= a.K) break;
+                float x = v[e];
+                if (a.add) x += a.add[n * a.add_stride + k + e];
+                if (a.out_f32) static_cast<float*>(a.dw)[n * a.dw_stride + k + e] = x;
+                else static_cast<T*>(a.dw)[n * a.dw_stride + k + e] = (T)x;
+            }
+        }
+    }
+    __asm__ __volatile__("" ::: "memory");
+}
+
+constexpr int kWgThreads = 256;
+
+// dw = dy^T x^ for any alignment and stride of dy (wgrad_kernel below takes words): 128 x 128 outputs per workgroup, four waves of 64 x 64, 32 tokens a step.  Both operands are token-major in memory, the MFMA wants eight tokens of
 // a column in a lane: the tiles go into LDS as they are and are read transposed.
 // The checkpoint is expanded to T between its load and LDS.
-constexpr int kWgTile = 128, kWgStep = 32, kWgThreads = 256;
+constexpr int kWgTile = 128, kWgStep = 32;
 constexpr int kWgPitch = kWgTile * 2 + 64;  // rows 16 banks apart: the four rows of a transposed read differ
 
 template <class T>
-__global__ __launch_bounds__(kWgThreads) void wgrad_kernel(const WgradArgs a)
+__global__ __launch_bounds__(kWgThreads) void wgrad_any_kernel(const WgradArgs a)
 {
     typedef typename Mfma<T>::frag frag;
-    __shared__ __attribute__((aligned(16))) char lds_y[kWgStep * kWgPitch];
-    __shared__ __attribute__((aligned(16))) char lds_x[kWgStep * kWgPitch];
+    __shared__ __attribute__((aligned(16))) char lds[32 * 1024];
+    static_assert(2 * kWgStep * kWgPitch <= (int)sizeof(lds), "stage");
+    char *const lds_y = lds, *const lds_x = lds + kWgStep * kWgPitch;
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int n0 = blockIdx.y * kWgTile, k0 = blockIdx.x * kWgTile;
     const int wn = (wave >> 1) * 64, wk = (wave & 1) * 64;
@@ -219,25 +267,441 @@ __global__ __launch_bounds__(kWgThreads) void wgrad_kernel(const WgradArgs a)
                 for (int j = 0; j < 2; ++j) acc[i][j] = Mfma<T>::run(fx[j], fy[i], acc[i][j]);
         }
     }
-    // a lane holds row n, four consecutive k per group of four accumulators
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int n = n0 + wn + i * 32 + (lane & 31);
-        if (n >= a.N) continue;
+    for (int i = 0; i < 2; ++i) wgrad_store_rows<T, 2>(a, lds + wave * 8192, n0 + wn + i * 32, k0 + wk, acc[i]);
+}
+
+// The same for dy in whole words (wgrad_fast): 2 x 2 waves of 32 WN x 32 WK outputs,
+// 64 tokens a step, two stages in LDS.
+//   - The MFMA wants eight tokens of a column in a lane, memory has a token's columns
+//     side by side.  A thread loads 8 tokens x 8 columns of each operand and turns them
+//     in registers: dy by half a byte permute per element, the checkpoint for nothing,
+//     since its values are converted one by one and paired as they are rounded.  LDS
+//     then holds, for every column, 64 tokens in eight 16-byte chunks, and both sides
+//     use 16-byte accesses.  (Staging token-major and reading with the transposing
+//     LDS loads moves the same bytes in twice the reads, 8 bytes each.)
+//   - Chunk c of column r lies at chunk c ^ ((r ^ r / 8) & 7): eight (sixteen)
+//     consecutive columns, as a fragment read takes them, and eight columns 8 apart,
+//     as the threads write them, lie in different banks.
+//   - A workgroup's work is a list of tiles, then a share of the tiles that do not
+//     fill the device a last time: those are cut along the tokens into equal shares
+//     (wgrad_join_kernel adds the pieces in token order).
+struct WgradPlan {
+    int tiles_n, tiles_k;
+    int full;          // tiles computed whole, tile t by workgroup t % grid
+    int grid;          // workgroups
+    int shares;        // workgroups that take a share of the other tiles (0: there are none)
+    int64_t steps;     // of 64 tokens
+    float* pieces;     // [2 shares] partial tiles
+};
+
+// Tile t in the order of computation: groups of eight tile rows, column by column, so
+// that the 32 tiles an XCD works on at a time share rows of dy and columns of x^.
+__device__ __host__ inline void wgrad_tile(const WgradPlan& p, int t, int& tn, int& tk)
+{
+    const int per = 8 * p.tiles_k, g = t / per, left = p.tiles_n - 8 * g, rows = left < 8 ? left : 8, r = t - g * per;
+    tn = 8 * g + r % rows;
+    tk = r / rows;
+}
+
+// The steps of the cut tiles are numbered through; share s begins at this one.
+__device__ __host__ inline int64_t wgrad_share(const WgradPlan& p, int64_t s)
+{
+    const int64_t rest = (int64_t)p.tiles_n * p.tiles_k - p.full;
+    return rest * p.steps * s / p.shares;
+}
+
+constexpr int kWgRows = 64;   // tokens per step
+constexpr int kWgCol = 128;   // LDS bytes of a column's tokens
+
+// LDS offset of chunk c (8 tokens) of column r
+__device__ __forceinline__ int wgrad_at(int r, int c) { return r * kWgCol + ((c ^ r ^ (r >> 3)) & 7) * 16; }
+
+// A thread's share of a step: 8 tokens x 8 columns of dy and of the checkpoint.
+struct WgradRegs {
+    u32x4 y[8];
+    u32x2 x[8];
+    int e[2];  // scales of tokens 2 (lane % 4) and the next: four lanes share a block of 32 columns
+};
+
+template <class T>
+struct WgradLoader {
+    const WgradArgs& a;
+    uint32_t yoff, xoff, eoff, ypitch;
+    int eper;
+    int64_t end;  // first step past the range
+    __amdgpu_buffer_rsrc_t ry, rq, re;
+
+    // tg: which eight of the step's tokens; n, k: the first of the eight columns of dy and x
+    __device__ __forceinline__ WgradLoader(const WgradArgs& args, int tg, int n, int k, int64_t stop) : a(args), end(stop)
+    {
+        ypitch = (uint32_t)a.dy_stride * 2u;
+        eper = a.Kp / 32;
+        yoff = n < a.N ? (uint32_t)(8 * tg) * ypitch + (uint32_t)n * 2u : kOob;
+        xoff = k < a.Kp ? (uint32_t)(8 * tg) * (uint32_t)a.Kp + (uint32_t)k : kOob;
+        eoff = k < a.Kp ? (uint32_t)(8 * tg + 2 * (threadIdx.x & 3)) * (uint32_t)eper + (uint32_t)(k / 32) : kOob;
+    }
+    // Resources that begin at the step's first token and end with the last one's row: tokens past M and
+    // columns past the row read as zero.
+    __device__ __forceinline__ void at(int64_t step)
+    {
+        const int64_t m = step * kWgRows, left = step < end ? a.M - m : 0;
+        const int rows = (int)(left < kWgRows ? left : kWgRows);
+        ry = __builtin_amdgcn_make_buffer_rsrc((void*)(static_cast<const T*>(a.dy) + m * a.dy_stride), 0,
+                                               rows > 0 ? ((rows - 1) * (int)a.dy_stride + a.N) * 2 : 0, kRsrcFlags);
+        rq = __builtin_amdgcn_make_buffer_rsrc((void*)(a.q + m * a.Kp), 0, rows * a.Kp, kRsrcFlags);
+        re = __builtin_amdgcn_make_buffer_rsrc((void*)(a.e + m * eper), 0, rows * eper, kRsrcFlags);
+    }
+    __device__ __forceinline__ void load_y(WgradRegs& r, int i) const
+    {
+        r.y[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ry, yoff + (uint32_t)i * ypitch, 0, 0));
+    }
+    __device__ __forceinline__ void load_x(WgradRegs& r, int i) const
+    {
+        r.x[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rq, xoff + (uint32_t)(i * a.Kp), 0, 0));
+    }
+    __device__ __forceinline__ void load_e(WgradRegs& r, int i) const
+    {
+        r.e[i] = (int8_t)__builtin_amdgcn_raw_buffer_load_b8(re, eoff + (uint32_t)(i * eper), 0, 0);
+    }
+};
+
+// The eight tokens' scales from the four lanes that hold two each.
+__device__ __forceinline__ void wgrad_scales(const WgradRegs& r, float (&sc)[8])
+{
+    const int s[2] = {(int)__float_as_uint(block_scale(r.e[0])), (int)__float_as_uint(block_scale(r.e[1]))};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+    for (int q = 0; q < 2; ++q) {
+        sc[0 + q] = __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp(s[q], 0x00, 0xF, 0xF, true));
+        sc[2 + q] = __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp(s[q], 0x55, 0xF, 0xF, true));
+        sc[4 + q] = __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp(s[q], 0xAA, 0xF, 0xF, true));
+        sc[6 + q] = __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp(s[q], 0xFF, 0xF, 0xF, true));
+    }
+}
+
+// Tokens 2 p and 2 p + 1 of column j of the checkpoint as a pair of T.
+template <class T>
+__device__ __forceinline__ uint32_t wgrad_pair_x(const WgradRegs& r, const float (&sc)[8], int j, int p)
+{
+    typedef T t2 __attribute__((ext_vector_type(2)));
+    const t2 v = {(T)(byte_value(r.x[2 * p][j / 4], j % 4) * sc[2 * p]),
+                  (T)(byte_value(r.x[2 * p + 1][j / 4], j % 4) * sc[2 * p + 1])};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// Tokens 2 p and 2 p + 1 of column j of dy.
+__device__ __forceinline__ uint32_t wgrad_pair_y(const WgradRegs& r, int j, int p)
+{
+    return __builtin_amdgcn_perm(r.y[2 * p + 1][j / 2], r.y[2 * p][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+}
+
+template <int WN, int WK>
+struct WgradTile {
+    static constexpr int kBN = 64 * WN, kBK = 64 * WK;
+    static constexpr int kBlocks = WN * WK;           // 32 x 32 blocks of a wave
+    static constexpr int kFloats = kBN * kBK;         // of a partial tile
+    static constexpr int kStage = (kBN + kBK) * kWgCol;
+    static constexpr int kLds = 2 * kStage;
+};
+
+// One tile over the steps s0 .. s1 - 1, tiles of 128 x 128: two workgroups share a CU
+// and cover each other's waits.  Waves 0 and 1 load and turn dy, waves 2 and 3 the
+// checkpoint, a step ahead.
+template <class T>
+__device__ __forceinline__ void wgrad_run_tile(const WgradArgs& a, char* lds, int tn, int tk, int64_t s0, int64_t s1,
+                                               f32x16 (&acc)[2][2])
+{
+    typedef WgradTile<2, 2> Tile;
+    typedef typename Mfma<T>::frag frag;
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+    const int tg = (threadIdx.x >> 4) & 7, cg = threadIdx.x & 15;
+    WgradLoader<T> ld(a, tg, tn * Tile::kBN + 8 * cg, tk * Tile::kBK + 8 * cg, s1);
+    WgradRegs r;
+    auto load = [&](int64_t step) {
+        ld.at(step);
+        if (wave < 2) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int k = k0 + wk + j * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
-                if (k >= a.K) continue;
-                float v = acc[i][j][r];
-                if (a.add) v += a.add[n * a.add_stride + k];
-                if (a.out_f32)
-                    static_cast<float*>(a.dw)[n * a.dw_stride + k] = v;
-                else
-                    static_cast<T*>(a.dw)[n * a.dw_stride + k] = (T)v;
+            for (int i = 0; i < 8; ++i) ld.load_y(r, i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ld.load_x(r, i);
+            ld.load_e(r, 0);
+            ld.load_e(r, 1);
+        }
+    };
+    auto put = [&](char* stage) {
+        if (wave < 2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<u32x4*>(stage + wgrad_at(8 * cg + j, tg)) =
+                    u32x4{wgrad_pair_y(r, j, 0), wgrad_pair_y(r, j, 1), wgrad_pair_y(r, j, 2), wgrad_pair_y(r, j, 3)};
+        } else {
+            float sc[8];
+            wgrad_scales(r, sc);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<u32x4*>(stage + Tile::kBN * kWgCol + wgrad_at(8 * cg + j, tg)) =
+                    u32x4{wgrad_pair_x<T>(r, sc, j, 0), wgrad_pair_x<T>(r, sc, j, 1), wgrad_pair_x<T>(r, sc, j, 2),
+                          wgrad_pair_x<T>(r, sc, j, 3)};
+        }
+    };
+    load(s0);
+    put(lds);
+    load(s0 + 1);
+    __syncthreads();
+    for (int64_t s = s0; s < s1; ++s) {
+        const int cur = (int)(s - s0) & 1;
+        const char* stage = lds + cur * Tile::kStage;
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) {
+            frag fy[2], fx[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = 2 * sub + (lane >> 5);
+                fy[i] = *reinterpret_cast<const frag*>(stage + wgrad_at((wave >> 1) * 64 + i * 32 + (lane & 31), c));
+                fx[i] = *reinterpret_cast<const frag*>(stage + Tile::kBN * kWgCol +
+                                                       wgrad_at((wave & 1) * 64 + i * 32 + (lane & 31), c));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = Mfma<T>::run(fx[j], fy[i], acc[i][j]);
+        }
+        if (s + 1 < s1) put(lds + (cur ^ 1) * Tile::kStage);
+        if (s + 2 < s1) load(s + 2);
+        __syncthreads();
+    }
+}
+
+// The same for tiles of 256 x 256: one workgroup per CU, one wave per SIMD, whose 256
+// accumulators leave no second wave to cover a wait.  Every other instruction of a
+// step therefore has a place after one of its 64 MFMAs, and fences keep it there:
+//   MFMA 16 u ..     (u = 0, 1, 2) the fragment reads of the next 16 tokens,
+//   MFMA 0 .. 31     the next step's checkpoint, a column every four MFMAs,
+//   MFMA 32 .. 47    the next step's dy, two columns every four,
+//   MFMA 0 .. 35     the loads of the step after that, into the other set of
+//                    registers: they have more than a step (2048 cycles) to arrive,
+//   before MFMA 48   the barrier: the next step is written, and the buffer that the
+//                    step after will be written to has been read,
+//   MFMA 48 ..       the fragment reads of the next step's first 16 tokens.
+template <class T>
+struct WgradBig {
+    typedef WgradTile<4, 4> Tile;
+    typedef typename Mfma<T>::frag frag;
+
+    const WgradArgs& a;
+    char* const lds;
+    f32x16 (&acc)[4][4];
+    WgradLoader<T> ld;
+    // LDS offsets in each of the two stages: this thread's first column of eight (column
+    // j's chunk lies at offset ^ 16 j), and this lane's column of the first fragment
+    // (x then dy) with the first chunk, where 16 tokens on or a block on changes the
+    // chunk by an exclusive or of 32 sub and 64 block.  Kept to these few registers: the
+    // step hides their constancy, or every sum would get a register of its own.
+    uint32_t put[2], get_y[2], get_x[2];
+    WgradRegs r[2];
+    frag fy[2][4], fx[2][4];
+
+    __device__ __forceinline__ WgradBig(const WgradArgs& args, char* l, int tn, int tk, int64_t s1, f32x16 (&c)[4][4])
+        : a(args), lds(l), acc(c),
+          ld(args, threadIdx.x >> 5, tn * Tile::kBN + 8 * (threadIdx.x & 31), tk * Tile::kBK + 8 * (threadIdx.x & 31), s1)
+    {
+        const int tg = threadIdx.x >> 5, cg = threadIdx.x & 31, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            put[p] = p * Tile::kStage + wgrad_at(8 * cg, tg);
+            get_y[p] = p * Tile::kStage + wgrad_at((wave >> 1) * 128 + (lane & 31), lane >> 5);
+            get_x[p] = p * Tile::kStage + wgrad_at((wave & 1) * 128 + (lane & 31), lane >> 5);
+        }
+    }
+    __device__ __forceinline__ void hide()
+    {
+        __asm__ __volatile__("" : "+v"(put[0]), "+v"(put[1]), "+v"(get_y[0]), "+v"(get_y[1]), "+v"(get_x[0]),
+                             "+v"(get_x[1]), "+v"(ld.yoff), "+v"(ld.xoff), "+v"(ld.eoff));
+    }
+    __device__ __forceinline__ void load(WgradRegs& g, int i) const  // 0 .. 17
+    {
+        if (i < 2) ld.load_e(g, i);
+        else if (i < 10) ld.load_x(g, i - 2);
+        else ld.load_y(g, i - 10);
+    }
+    template <int P>
+    __device__ __forceinline__ void write(int j, bool x, const u32x4& v) const
+    {
+        *reinterpret_cast<u32x4*>(lds + (put[P] ^ (16u * j)) + j * kWgCol + (x ? Tile::kBN * kWgCol : 0)) = v;
+    }
+    template <int P>
+    __device__ __forceinline__ void read(int sub, int i, frag (&gy)[4], frag (&gx)[4]) const
+    {
+        const int b = i & 3;
+        const uint32_t flip = 32u * sub ^ 64u * (b & 1);
+        if (i < 4)
+            gy[b] = *reinterpret_cast<const frag*>(lds + (get_y[P] ^ flip) + b * 32 * kWgCol);
+        else
+            gx[b] = *reinterpret_cast<const frag*>(lds + (get_x[P] ^ flip) + b * 32 * kWgCol + Tile::kBN * kWgCol);
+    }
+
+    template <int P>
+    __device__ __forceinline__ void step(int64_t s)
+    {
+        hide();
+        WgradRegs& g = r[P ^ 1];
+        ld.at(s + 2);
+        float sc[8];
+        wgrad_scales(g, sc);
+        u32x4 w0, w1;
+#pragma unroll
+        for (int m = 0; m < 64; ++m) {
+            const int u = m / 16, i = (m % 16) / 4, j = m % 4;
+            if (m == 48) {
+                __asm__ __volatile__("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            acc[i][j] = Mfma<T>::run(fx[u & 1][j], fy[u & 1][i], acc[i][j]);
+            if (m % 2 == 0) {
+                const int f = (m % 16) / 2;  // x fragments first: the next MFMA needs all four and one of dy's
+                if (u < 3) read<P>(u + 1, f ^ 4, fy[(u + 1) & 1], fx[(u + 1) & 1]);
+                else read<P ^ 1>(0, f ^ 4, fy[0], fx[0]);
+            } else if (m < 36) {
+                load(r[P], m / 2);
+            }
+            if (m < 32) {
+                w0[j] = wgrad_pair_x<T>(g, sc, m / 4, j);
+                if (j == 3) write<P ^ 1>(m / 4, true, w0);
+            } else if (m < 48) {
+                const int col = 2 * ((m - 32) / 4);
+                w0[j] = wgrad_pair_y(g, col, j);
+                w1[j] = wgrad_pair_y(g, col + 1, j);
+                if (j == 3) {
+                    write<P ^ 1>(col, false, w0);
+                    write<P ^ 1>(col + 1, false, w1);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    __device__ __forceinline__ void run(int64_t s0, int64_t s1)
+    {
+        ld.at(s0);
+#pragma unroll
+        for (int i = 0; i < 18; ++i) load(r[0], i);
+        ld.at(s0 + 1);
+#pragma unroll
+        for (int i = 0; i < 18; ++i) load(r[1], i);
+        float sc[8];
+        wgrad_scales(r[0], sc);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            u32x4 x, y;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                x[p] = wgrad_pair_x<T>(r[0], sc, j, p);
+                y[p] = wgrad_pair_y(r[0], j, p);
+            }
+            write<0>(j, false, y);
+            write<0>(j, true, x);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) read<0>(0, i, fy[0], fx[0]);
+        // in twos: a step past the range multiplies the zeros its loads gave
+        for (int64_t s = s0; s < s1; s += 2) {
+            step<0>(s);
+            step<1>(s + 1);
+        }
+        __syncthreads();
+    }
+};
+
+template <class T>
+__device__ __forceinline__ void wgrad_run_tile(const WgradArgs& a, char* lds, int tn, int tk, int64_t s0, int64_t s1,
+                                               f32x16 (&acc)[4][4])
+{
+    WgradBig<T>(a, lds, tn, tk, s1, acc).run(s0, s1);
+}
+
+template <class T, int WN, int WK>
+__global__ __launch_bounds__(kWgThreads, WN == 4 ? 1 : 2) void wgrad_kernel(const WgradArgs a, const WgradPlan p)
+{
+    typedef WgradTile<WN, WK> Tile;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    const int wave = uni(threadIdx.x >> 6);
+    // workgroups are dealt to the 8 XCDs in turn: those of one XCD take neighbouring tiles
+    const int per = p.grid / 8, me = p.grid % 8 == 0 ? (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8) : (int)blockIdx.x;
+    f32x16 acc[WN][WK];
+    auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < WN; ++i)
+#pragma unroll
+            for (int j = 0; j < WK; ++j) acc[i][j] = f32x16{};
+    };
+    for (int t = me; t < p.full; t += p.grid) {
+        int tn, tk;
+        wgrad_tile(p, t, tn, tk);
+        clear();
+        wgrad_run_tile<T>(a, lds, tn, tk, 0, p.steps, acc);
+#pragma unroll
+        for (int i = 0; i < WN; ++i)
+            wgrad_store_rows<T, WK>(a, lds + wave * (32 * 32 * WK * 4), tn * Tile::kBN + (wave >> 1) * 32 * WN + 32 * i,
+                                    tk * Tile::kBK + (wave & 1) * 32 * WK, acc[i]);
+        __syncthreads();
+    }
+    if (me >= p.shares) return;
+    const int64_t end = wgrad_share(p, me + 1);
+    int slot = 0;
+    for (int64_t at = wgrad_share(p, me); at < end; ++slot) {
+        const int64_t t = at / p.steps, stop = (t + 1) * p.steps < end ? (t + 1) * p.steps : end;
+        int tn, tk;
+        wgrad_tile(p, p.full + (int)t, tn, tk);
+        clear();
+        wgrad_run_tile<T>(a, lds, tn, tk, at - t * p.steps, stop - t * p.steps, acc);
+        // in the order of the registers: [block][four accumulators][thread]
+        f32x4* out = reinterpret_cast<f32x4*>(p.pieces + (int64_t)(2 * me + slot) * Tile::kFloats) + threadIdx.x;
+#pragma unroll
+        for (int b = 0; b < Tile::kBlocks; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x16& v = acc[b / WK][b % WK];
+                out[(b * 4 + g) * kWgThreads] = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+            }
+        at = stop;
+    }
+}
+
+// Adds the pieces of the cut tiles in token order: one workgroup per tile and row of
+// blocks of each wave.
+template <class T, int WN, int WK>
+__global__ __launch_bounds__(kWgThreads) void wgrad_join_kernel(const WgradArgs a, const WgradPlan p)
+{
+    typedef WgradTile<WN, WK> Tile;
+    constexpr int kArea = 32 * 32 * WK * 4;
+    __shared__ __attribute__((aligned(16))) char lds[4 * kArea];
+    const int t = blockIdx.x, row = blockIdx.y, wave = uni(threadIdx.x >> 6);
+    const int64_t first = t * p.steps, last = first + p.steps, rest = (int64_t)p.tiles_n * p.tiles_k - p.full;
+    // the share that holds the tile's first step: the last one that begins at or before it
+    int64_t s = first * p.shares / (rest * p.steps);
+    while (s + 1 < p.shares && wgrad_share(p, s + 1) <= first) ++s;
+    f32x16 acc[WK];
+#pragma unroll
+    for (int j = 0; j < WK; ++j) acc[j] = f32x16{};
+    for (; s < p.shares && wgrad_share(p, s) < last; ++s) {
+        const int slot = wgrad_share(p, s) < first ? 1 : 0;
+        const f32x4* in = reinterpret_cast<const f32x4*>(p.pieces + (2 * s + slot) * Tile::kFloats) + threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < WK; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 v = in[((row * WK + j) * 4 + g) * kWgThreads];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][4 * g + e] += v[e];
             }
     }
+    int tn, tk;
+    wgrad_tile(p, p.full + t, tn, tk);
+    wgrad_store_rows<T, WK>(a, lds + wave * kArea, tn * Tile::kBN + (wave >> 1) * 32 * WN + 32 * row,
+                            tk * Tile::kBK + (wave & 1) * 32 * WK, acc);
 }
 
 }  // namespace gemm_rs_layer
