@@ -15,7 +15,6 @@ bool wgrad_fast(const gemm_rs_wgrad_args& g)
     return g.M > 0 && aligned(g.dy, 4) && g.dy_stride % 2 == 0 && g.N % 2 == 0 && g.dy_stride < (1 << 23);
 }
 
-constexpr int kCus = 256;         // compute units of an MI355X
 constexpr int kWgMinSteps = 4;    // a share is at least this many steps of 64 tokens
 
 WgradPlan wgrad_plan(const gemm_rs_wgrad_args& g, int& big)

@@ -78,5 +78,6 @@ struct Checker {
 };
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;
+constexpr int kCus = 256;  // compute units of an MI355X
 
 }  // namespace gemm_rs_layer

@@ -1,4 +1,6 @@
 // w4.hip -- C entry points of the product with 4-bit weights (gemm_rs_layer.h).
+#include <type_traits>
+
 #include "host.hpp"
 
 #include "w4.hpp"
@@ -24,32 +26,54 @@ W4Layout w4_layout(const gemm_rs_w4_config& c)
     return l;
 }
 
-template <class T, int NT, int MF>
-int w4_launch(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
+// f(SUBS, ZEROS) for the layout, as compile-time constants
+template <class F>
+int w4_forms(const W4Layout& l, bool zeros, F f)
 {
-    constexpr int kWaves = 8;
-    const dim3 grid((unsigned)ceil_div(a.l.tiles, NT), (unsigned)ceil_div(a.M, 16 * MF));
-    auto go = [&](void (*k)(W4Args)) { return launch(k, grid, 64 * kWaves, a, stream, "gemm_rs_w4_linear"); };
-    if (c.zero_points) {
-        switch (a.l.subs) {
-        case 1: return go(w4_kernel<T, kWaves, NT, MF, 1, true>);
-        case 2: return go(w4_kernel<T, kWaves, NT, MF, 2, true>);
-        default: return go(w4_kernel<T, kWaves, NT, MF, 4, true>);
+    auto subs = [&](auto z) {
+        switch (l.subs) {
+        case 1: return f(std::integral_constant<int, 1>(), z);
+        case 2: return f(std::integral_constant<int, 2>(), z);
+        default: return f(std::integral_constant<int, 4>(), z);
         }
-    }
-    switch (a.l.subs) {
-    case 1: return go(w4_kernel<T, kWaves, NT, MF, 1, false>);
-    case 2: return go(w4_kernel<T, kWaves, NT, MF, 2, false>);
-    default: return go(w4_kernel<T, kWaves, NT, MF, 4, false>);
-    }
+    };
+    return zeros ? subs(std::true_type()) : subs(std::false_type());
 }
 
+template <class T, int WAVES, int NT, int MF, bool FEW, int WA, int XA>
+int w4_launch(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
+{
+    const dim3 grid((unsigned)ceil_div(a.l.tiles, NT), (unsigned)ceil_div(a.M, 16 * MF));
+    return w4_forms(a.l, c.zero_points, [&](auto subs, auto zeros) {
+        return launch(w4_kernel<T, WAVES, NT, MF, FEW, WA, XA, decltype(subs)::value, decltype(zeros)::value>, grid, 64 * WAVES, a,
+                      stream, "gemm_rs_w4_linear");
+    });
+}
+
+template <class T, int NT>
+int w4_tile_launch(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
+{
+    const dim3 grid((unsigned)ceil_div(a.M, kW4Rows), (unsigned)ceil_div(a.l.tiles, 4 * NT));
+    return w4_forms(a.l, c.zero_points, [&](auto subs, auto zeros) {
+        return launch(w4_tile_kernel<T, NT, decltype(subs)::value, decltype(zeros)::value>, grid, 256, a, stream,
+                      "gemm_rs_w4_linear");
+    });
+}
+
+// Few rows: the kernel whose waves split K; 4, 16, 32 rows or 64 at a time.  Many: the
+// kernel whose workgroups keep 64 rows in LDS, once there is one for every second
+// CU (fewer leave too much of the chip idle, since each runs all of K).  Measured, us
+// (few / many): 7168 x 8192 at 128 rows (112 workgroups) 60 / 77, at 200 (224) 105 / 77;
+// 1280 x 8192 at 300 rows (50) 31 / 78, at 1000 (160) 90 / 75.
 template <class T>
 int w4_run(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
 {
-    if (a.M <= 16) return w4_launch<T, 1, 1>(c, a, stream);
-    if (a.M <= 32) return w4_launch<T, 1, 2>(c, a, stream);
-    return w4_launch<T, 1, 4>(c, a, stream);
+    if (a.M <= 4) return w4_launch<T, 8, 1, 1, true, 4, 4>(c, a, stream);
+    if (a.M <= 16) return w4_launch<T, 8, 2, 1, false, 4, 4>(c, a, stream);
+    if (a.M <= 32) return w4_launch<T, 8, 2, 2, false, 2, 1>(c, a, stream);
+    const int64_t many = ceil_div(a.M, kW4Rows) * ceil_div(a.l.tiles, 4 * 2);
+    if (a.M <= 64 || many < kCus / 2) return w4_launch<T, 4, 2, 4, false, 2, 1>(c, a, stream);
+    return w4_tile_launch<T, 2>(c, a, stream);
 }
 
 }  // namespace

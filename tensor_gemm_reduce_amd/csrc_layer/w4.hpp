@@ -6,10 +6,11 @@
 // reading them at full rate.
 //   - A nibble becomes a 16-bit float by two bit operations per pair: placed in the
 //     mantissa of 16.0 it reads as 16 + q exactly.
-//   - The MFMA multiplies x by 16 + q, a second one by the constant -(16 + z), both
-//     into the group's FP32 accumulator, so no vector instruction subtracts the zero
-//     point and nothing is rounded before the scale.
-//   - The group's accumulator times its scale (FP32) is added to the result's.
+//   - The MFMA multiplies x by 16 + q; the group's FP32 accumulator starts at
+//     -(16 + z) times the sum of the group's inputs, which an MFMA with a constant
+//     gives for every column at once.  No weight is rounded, and none has its zero
+//     point subtracted by itself.
+//   - The group's accumulator times its scale is added to the result's (FP32).
 #pragma once
 
 #include "common.hpp"
@@ -109,12 +110,24 @@ __device__ __forceinline__ typename W4Type<T>::frag w4_expand(uint32_t w)
     return __builtin_bit_cast(typename W4Type<T>::frag, v);
 }
 
-// -(16 + z) in all eight places.
+// A value in all eight places.
 template <class T>
-__device__ __forceinline__ typename W4Type<T>::frag w4_offset(uint32_t z)
+__device__ __forceinline__ typename W4Type<T>::frag w4_constant(float v)
 {
-    uint32_t v = ((z | (z << 16)) << W4Type<T>::kShift) | W4Type<T>::kMagic | 0x80008000u;
-    return __builtin_bit_cast(typename W4Type<T>::frag, (u32x4{v, v, v, v}));
+    typename W4Type<T>::frag f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (T)v;
+    return f;
+}
+
+// Within 16 lanes, lane i takes lane i + N's register (zero past the end).
+template <int N>
+__device__ __forceinline__ i32x4 lanes_down(const i32x4& v)
+{
+    i32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_update_dpp(0, v[i], 0x100 + N, 0xF, 0xF, true);
+    return r;
 }
 
 struct W4Args {
@@ -125,86 +138,258 @@ struct W4Args {
     int64_t M, x_stride, y_stride;
 };
 
-// A workgroup computes NT tiles of 16 columns for up to 16 MF rows; its waves
-// split the blocks of K and add up through LDS at the end, in wave order.
-template <class T, int WAVES, int NT, int MF, int SUBS, bool ZEROS>
-__global__ __launch_bounds__(64 * WAVES) void w4_kernel(const W4Args a)
-{
-    typedef typename W4Type<T>::frag frag;
-    constexpr int kSteps = 4 / SUBS;  // MFMA steps (32 inputs) per scale
-    __shared__ f32x4 part[WAVES][NT][MF][64];
-    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
-    const int tile0 = blockIdx.x * NT;
-    const int64_t m0 = (int64_t)blockIdx.y * (16 * MF);
-    f32x4 acc[NT][MF] = {};
-    // rows past the last read it again; their results are not stored
-    const T* xrow[MF];
-#pragma unroll
-    for (int f = 0; f < MF; ++f) {
-        int64_t m = m0 + f * 16 + (lane & 15);
-        m = m < a.M ? m : a.M - 1;
-        xrow[f] = static_cast<const T*>(a.x) + m * a.x_stride;
-    }
-    const int b0 = (int)((int64_t)a.l.blocks * wave / WAVES), b1 = (int)((int64_t)a.l.blocks * (wave + 1) / WAVES);
-    for (int b = b0; b < b1; ++b) {
-        u32x4 w[NT];
-        float sc[NT][SUBS];
-        uint32_t z[NT][SUBS];
+// What one block of 128 inputs brings: the weights, scales and zero points of NT tiles.
+template <class T, int NT, int SUBS, bool ZEROS>
+struct W4Block {
+    u32x4 w[NT];
+    T sc[NT][SUBS];
+    uint8_t z[NT][SUBS];
+
+    // tb: tile 0's index of the block; tiles are `blocks` apart.  Tiles past the last read it again.
+    __device__ __forceinline__ void load(const W4Args& a, int tile0, int b)
+    {
+        const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int tile = min(tile0 + t, a.l.tiles - 1);
             const int64_t tb = (int64_t)tile * a.l.blocks + b;
             w[t] = *reinterpret_cast<const u32x4*>(a.packed + (tb * 64 + lane) * 16);
             const int64_t at = tb * (kW4Tile * SUBS) + (lane & 15) * SUBS;
+            typedef T scales_t __attribute__((ext_vector_type(SUBS)));
+            typedef uint8_t zeros_t __attribute__((ext_vector_type(SUBS)));
+            const scales_t s = *reinterpret_cast<const scales_t*>(a.packed + a.l.scale_at + at * 2);
+            zeros_t zz;
+            if constexpr (ZEROS) zz = *reinterpret_cast<const zeros_t*>(a.packed + a.l.zero_at + at);
 #pragma unroll
-            for (int s = 0; s < SUBS; ++s) {
-                sc[t][s] = (float)reinterpret_cast<const T*>(a.packed + a.l.scale_at)[at + s];
-                z[t][s] = ZEROS ? reinterpret_cast<const uint8_t*>(a.packed + a.l.zero_at)[at + s] : 8u;
+            for (int u = 0; u < SUBS; ++u) {
+                sc[t][u] = s[u];
+                z[t][u] = ZEROS ? zz[u] : 8;
             }
         }
-        frag x[MF][4];
+    }
+    // acc[t][f] += the block's product with the rows x[f] (four steps of 32 inputs).  The part of the zero points,
+    // -(16 + z) times the sum of a row's inputs, is where a group's accumulator starts: that sum is one MFMA per step
+    // for all the tiles.
+    template <int MF>
+    __device__ __forceinline__ void multiply(const typename W4Type<T>::frag (&x)[MF][4], f32x4 (&acc)[NT][MF]) const
+    {
+        constexpr int kSteps = 4 / SUBS;  // steps per scale
+        const typename W4Type<T>::frag unit = w4_constant<T>(ZEROS ? -1.f : -24.f);
 #pragma unroll
-        for (int f = 0; f < MF; ++f)
+        for (int u = 0; u < SUBS; ++u) {
+            f32x4 start[MF] = {};
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                x[f][t] = __builtin_bit_cast(frag, load8(xrow[f], b * kW4Block + t * 32 + (lane >> 4) * 8, a.l.K));
+            for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+                for (int f = 0; f < MF; ++f) start[f] = W4Type<T>::mfma(x[f][u * kSteps + k], unit, start[f]);
 #pragma unroll
-            for (int s = 0; s < SUBS; ++s) {
-                const frag off = w4_offset<T>(z[t][s]);
-                f32x4 g[MF] = {};
+            for (int t = 0; t < NT; ++t) {
+                f32x4 g[MF];
+#pragma unroll
+                for (int f = 0; f < MF; ++f) g[f] = ZEROS ? start[f] * (float)(16 + z[t][u]) : start[f];
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
-                    const frag b8 = w4_expand<T>(w[t][s * kSteps + k]);
+                    const typename W4Type<T>::frag q = w4_expand<T>(w[t][u * kSteps + k]);
 #pragma unroll
-                    for (int f = 0; f < MF; ++f) {
-                        g[f] = W4Type<T>::mfma(x[f][s * kSteps + k], b8, g[f]);
-                        g[f] = W4Type<T>::mfma(x[f][s * kSteps + k], off, g[f]);
-                    }
+                    for (int f = 0; f < MF; ++f) g[f] = W4Type<T>::mfma(x[f][u * kSteps + k], q, g[f]);
                 }
+                const float scale = (float)sc[t][u];
 #pragma unroll
-                for (int f = 0; f < MF; ++f) acc[t][f] += g[f] * sc[t][s];
+                for (int f = 0; f < MF; ++f)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[t][f][r] = __builtin_fmaf(g[f][r], scale, acc[t][f][r]);
             }
+        }
     }
+};
+
+// Few rows: a workgroup computes NT tiles of 16 columns for up to 16 MF rows; its
+// waves split the blocks of K and add up through LDS at the end, in wave order.
+//   - Each wave keeps the weights of the next WA blocks and the rows of the next XA in
+//     flight, in registers that a block's loads refill in place once it is multiplied
+//     (a copy from one set to another would wait for the loads).
+//   - A load of x takes four rows' 256 bytes of a block, so whole lines; the fragments
+//     (16 rows x 64 bytes) are made in the wave's own part of LDS, 16-byte chunk c of
+//     row m at c ^ m % 16.  Loading fragments directly touches 16 half lines per
+//     instruction, of rows that share their cache set when they are a power of two
+//     apart (7168 x 8192, 24 rows, nothing else changed: 18.5 us so, 16.2 by LDS).
+//   - FEW (at most four rows) needs no LDS for it: the one load puts row m of step t
+//     into lane 4 t + m of each 16, and a step's fragment is that register shifted down
+//     4 t lanes (its rows past the fourth are other steps', and not stored).
+template <class T, int WAVES, int NT, int MF, bool FEW, int WA, int XA, int SUBS, bool ZEROS>
+__global__ __launch_bounds__(64 * WAVES) void w4_kernel(const W4Args a)
+{
+    static_assert(WA % XA == 0 && (!FEW || MF == 1), "register rings");
+    typedef typename W4Type<T>::frag frag;
+    typedef W4Block<T, NT, SUBS, ZEROS> Block;
+    constexpr int kLoads = FEW ? 1 : 4 * MF;
+    constexpr int kRow = kW4Block * 2, kArea = FEW ? 0 : 16 * MF * kRow;  // bytes of a row's block; of a wave's rows
+    constexpr int kPart = NT * MF * 64 * 16;                              // of a wave's results
+    __shared__ __attribute__((aligned(16))) char lds[WAVES * (kArea > kPart ? kArea : kPart)];
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+    char* const area = lds + wave * kArea;
+    const int tile0 = blockIdx.x * NT;
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * MF);
+    const int loads = FEW ? 1 : (int)min((a.M - m0 + 3) / 4, (int64_t)kLoads);
+    f32x4 acc[NT][MF] = {};
+    // Load i of a block: row 4 i + lane / 16, 16-byte chunk lane % 16 (FEW: row lane % 4, chunk lane % 16 / 4 of the
+    // step's four and step lane / 16 changed over).  A row past the last reads that again; rows of loads that are left
+    // out hold anything.  Neither's results are stored.
+    const int l16 = lane & 15, r0 = lane >> 4;
+    const int col0 = FEW ? 32 * (l16 >> 2) + 8 * r0 : 8 * l16;
+    auto row = [&](int i) {
+        const int64_t m = FEW ? l16 & 3 : m0 + 4 * i + r0;
+        return static_cast<const T*>(a.x) + (m < a.M ? m : a.M - 1) * a.x_stride;
+    };
+    auto load_x = [&](vec8<T> (&x)[kLoads], int b) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (i < loads) x[i] = *reinterpret_cast<const vec8<T>*>(row(i) + b * kW4Block + col0);
+    };
+    auto fragments = [&](const vec8<T> (&x)[kLoads], frag (&s)[MF][4]) {
+        if constexpr (FEW) {
+            const i32x4 v = __builtin_bit_cast(i32x4, x[0]);
+            s[0][0] = __builtin_bit_cast(frag, v);
+            s[0][1] = __builtin_bit_cast(frag, lanes_down<4>(v));
+            s[0][2] = __builtin_bit_cast(frag, lanes_down<8>(v));
+            s[0][3] = __builtin_bit_cast(frag, lanes_down<12>(v));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                if (i < loads)
+                    *reinterpret_cast<u32x4*>(area + (4 * i + r0) * kRow + ((l16 ^ ((4 * i + r0) & 15)) * 16)) =
+                        __builtin_bit_cast(u32x4, x[i]);
+#pragma unroll
+            for (int f = 0; f < MF; ++f)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    s[f][t] = *reinterpret_cast<const frag*>(area + (16 * f + l16) * kRow + (((4 * t + r0) ^ l16) * 16));
+        }
+    };
+    const int b0 = (int)((int64_t)a.l.blocks * wave / WAVES), b1 = (int)((int64_t)a.l.blocks * (wave + 1) / WAVES);
+    const int whole = min(b1, a.l.K / kW4Block);  // the last block may end past K
+    Block w[WA];
+    vec8<T> x[XA][kLoads];
+    frag s[MF][4];
+#pragma unroll
+    for (int i = 0; i < WA; ++i)
+        if (b0 + i < whole) {
+            w[i].load(a, tile0, b0 + i);
+            if (i < XA) load_x(x[i], b0 + i);
+        }
+    for (int b = b0; b < whole; b += WA) {
+#pragma unroll
+        for (int i = 0; i < WA; ++i) {
+            if (b + i < whole) {
+                fragments(x[i % XA], s);
+                if (b + i + XA < whole) load_x(x[i % XA], b + i + XA);
+                w[i].multiply(s, acc);
+            }
+            if (b + i + WA < whole) w[i].load(a, tile0, b + i + WA);
+        }
+    }
+    if (whole < b1) {
+        w[0].load(a, tile0, b1 - 1);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (i < loads) x[0][i] = load8(row(i), (b1 - 1) * kW4Block + col0, a.l.K);
+        fragments(x[0], s);
+        w[0].multiply(s, acc);
+    }
+    __syncthreads();
+    f32x4* const part = reinterpret_cast<f32x4*>(lds);  // [wave][tile][16 rows][lane]
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int f = 0; f < MF; ++f) part[wave][t][f][lane] = acc[t][f];
+        for (int f = 0; f < MF; ++f) part[((wave * NT + t) * MF + f) * 64 + lane] = acc[t][f];
     __syncthreads();
     // lane l of a tile holds rows 4 (l / 16) .. + 3 of column l % 16
     for (int i = threadIdx.x; i < NT * MF * 64; i += 64 * WAVES) {
         const int l = i & 63, f = (i >> 6) % MF, t = (i >> 6) / MF;
-        f32x4 s = part[0][t][f][l];
+        f32x4 sum = part[i];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) s += part[w][t][f][l];
+        for (int v = 1; v < WAVES; ++v) sum += part[v * NT * MF * 64 + i];
         const int n = (tile0 + t) * kW4Tile + (l & 15);
         if (n >= a.l.N) continue;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int64_t m = m0 + f * 16 + 4 * (l >> 4) + r;
-            if (m < a.M) static_cast<T*>(a.y)[m * a.y_stride + n] = (T)s[r];
+            if (m < a.M) static_cast<T*>(a.y)[m * a.y_stride + n] = (T)sum[r];
         }
+    }
+}
+
+// Many rows: 64 rows x 64 NT columns per workgroup, four waves of 64 x 16 NT over the
+// whole of K.  The rows' block of x goes through LDS (16-byte chunk c of row m at
+// c ^ m % 16), two blocks ahead in registers; each wave expands its own weights.
+constexpr int kW4Rows = 64;
+
+template <class T, int NT, int SUBS, bool ZEROS>
+__global__ __launch_bounds__(256, 2) void w4_tile_kernel(const W4Args a)
+{
+    typedef typename W4Type<T>::frag frag;
+    typedef W4Block<T, NT, SUBS, ZEROS> Block;
+    constexpr int kRow = kW4Block * 2;  // bytes of a row's block
+    __shared__ __attribute__((aligned(16))) char lds[2][kW4Rows * kRow];
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+    const int tile0 = (blockIdx.y * 4 + wave) * NT;
+    const int64_t m0 = (int64_t)blockIdx.x * kW4Rows;
+    const int chunk = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+    const T* xrow[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int64_t m = m0 + r0 + 16 * i;
+        m = m < a.M ? m : a.M - 1;
+        xrow[i] = static_cast<const T*>(a.x) + m * a.x_stride;
+    }
+    vec8<T> xr[4];
+    auto load_x = [&](int b) {
+        if (b >= a.l.blocks) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xr[i] = load8(xrow[i], b * kW4Block + chunk * 8, a.l.K);
+    };
+    auto put_x = [&](char* stage) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<u32x4*>(stage + (r0 + 16 * i) * kRow + ((chunk ^ r0) * 16)) = __builtin_bit_cast(u32x4, xr[i]);
+    };
+    f32x4 acc[NT][4] = {};
+    Block w[2];
+    load_x(0);
+    w[0].load(a, tile0, 0);
+    if (a.l.blocks > 1) w[1].load(a, tile0, 1);
+    put_x(lds[0]);
+    load_x(1);
+    __syncthreads();
+    for (int b = 0; b < a.l.blocks; b += 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (b + i < a.l.blocks) {
+                frag x[4][4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        x[f][t] = *reinterpret_cast<const frag*>(lds[i] + (f * 16 + (lane & 15)) * kRow +
+                                                                 (((4 * t + (lane >> 4)) ^ (lane & 15)) * 16));
+                if (b + i + 1 < a.l.blocks) put_x(lds[i ^ 1]);
+                load_x(b + i + 2);
+                w[i].multiply(x, acc);
+                if (b + i + 2 < a.l.blocks) w[i].load(a, tile0, b + i + 2);
+                __syncthreads();
+            }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int n = (tile0 + t) * kW4Tile + (lane & 15);
+        if (n >= a.l.N) continue;
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int64_t m = m0 + f * 16 + 4 * (lane >> 4) + r;
+                if (m < a.M) static_cast<T*>(a.y)[m * a.y_stride + n] = (T)acc[t][f][r];
+            }
     }
 }
 

@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -56,6 +57,13 @@ class gemm_rs_norm_config(ctypes.Structure):
         (n, _f32) for n in ("eps", "block_scale", "residual_scale")]
 
 
+# The argument blocks as calls pack them (setting a ctypes field costs as much as packing a whole block).
+_NORM_CONFIG = struct.Struct("7i3f")
+_NORM_ARGS = struct.Struct(f"{NORM_MAX_PARTS}QqQqQQqQQqQqQqQ")
+_NORM_GRAD_ARGS = struct.Struct("QqQqQqQqQQQQqQqQqQQQq")
+_WGRAD_ARGS = struct.Struct("2i3qQqQQQqQq")
+
+
 class gemm_rs_norm_args(ctypes.Structure):
     _fields_ = [("parts", _vp * NORM_MAX_PARTS), ("part_stride", _i64), ("residual", _vp), ("residual_stride", _i64),
                 ("post_weight", _vp), ("gate", _vp), ("gate_stride", _i64), ("pre_weight", _vp), ("h", _vp),
@@ -92,8 +100,8 @@ def lib():
                 f"{path} is missing: build it with `python -m tensor_gemm_reduce_amd.build` "
                 "(there is no fallback implementation)")
         L = ctypes.CDLL(path)
-        P = ctypes.POINTER
-        w4, norm, wg = P(gemm_rs_w4_config), P(gemm_rs_norm_config), P(gemm_rs_wgrad_args)
+        w4 = ctypes.POINTER(gemm_rs_w4_config)
+        norm = wg = _vp  # a structure by reference, or its packed bytes
         L.gemm_rs_layer_strerror.argtypes = [ctypes.c_int]
         L.gemm_rs_layer_strerror.restype = ctypes.c_char_p
         L.gemm_rs_w4_validate.argtypes = [w4]
@@ -101,9 +109,9 @@ def lib():
         L.gemm_rs_w4_pack.argtypes = [w4, _vp, _vp, _vp, _vp, _vp]
         L.gemm_rs_w4_linear.argtypes = [w4, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
         L.gemm_rs_norm_validate.argtypes = [norm]
-        L.gemm_rs_block_norm.argtypes = [norm, _i64, P(gemm_rs_norm_args), _vp]
+        L.gemm_rs_block_norm.argtypes = [norm, _i64, _vp, _vp]
         L.gemm_rs_block_norm_workspace.argtypes = [norm, _i64]
-        L.gemm_rs_block_norm_backward.argtypes = [norm, _i64, P(gemm_rs_norm_grad_args), _vp, _size, _vp]
+        L.gemm_rs_block_norm_backward.argtypes = [norm, _i64, _vp, _vp, _size, _vp]
         L.gemm_rs_ckpt_pack.argtypes = [_i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp]
         L.gemm_rs_ckpt_unpack.argtypes = [_i32, _i64, _i64, _vp, _vp, _vp, _i64, _vp]
         L.gemm_rs_ckpt_wgrad_workspace.argtypes = [wg]
@@ -127,26 +135,43 @@ def _check(code: int, what: str) -> None:
 
 # ---- argument checks ------------------------------------------------------------
 
-def _rows(t, name, shape, dtype):
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+def _device(t, name):
+    """Index of the current device, which has to be t's."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name}: must be a device tensor")
+    if d != _get_device():
+        raise ValueError(f"{name}: on device {d}, but the current device is {_get_device()}")
+    return d
+
+
+def _rows(t, name, rows, width, dtype, dev):
     """Checks a [rows][width] tensor with adjacent row elements; returns its row stride."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
-    rows, width = shape
+    if t.shape != (rows, width):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {(rows, width)}")
     s0, s1 = t.stride()
-    if not t.is_cuda or (s1 != 1 and width != 1) or (s0 < width and rows > 1):
-        raise ValueError(f"{name}: must be a device tensor whose rows hold their elements side by side")
+    if s1 != 1 and width != 1 or s0 < width and rows > 1:
+        raise ValueError(f"{name}: rows must hold their elements side by side, strides are {(s0, s1)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, not on the current device")
     return s0 if rows > 1 else max(s0, width)
 
 
-def _flat(t, name, shape, dtype):
+def _flat(t, name, shape, dtype, dev):
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: must be a contiguous device tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, not on the current device")
 
 
 def _two(t, name):
@@ -155,26 +180,12 @@ def _two(t, name):
     return t.shape
 
 
-def _same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {first.device}, but the current device is {torch.cuda.current_device()}")
-
-
-def _current(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _elsewhere(stream, device):
+def _elsewhere(stream, dev):
     """None, or the torch stream to switch to for a call whose `stream` is not the current one."""
-    if stream is None:
-        return None
     raw = stream if isinstance(stream, int) else stream.cuda_stream
-    if raw == _current(device):
+    if raw == _raw_stream(dev):
         return None
-    return torch.cuda.ExternalStream(raw, device=device) if isinstance(stream, int) else stream
+    return torch.cuda.ExternalStream(raw, device=dev) if isinstance(stream, int) else stream
 
 
 def _on_stream(call, stream, inputs, *args, **kw):
@@ -215,18 +226,18 @@ def w4_pack(q, scales, zeros=None, *, group, stream=None) -> W4Weight:
     cfg = gemm_rs_w4_config(N, 2 * half, group, _CODES[scales.dtype], int(zeros is not None))
     L = lib()
     _check(L.gemm_rs_w4_validate(ctypes.byref(cfg)), "gemm_rs_w4_validate")
+    dev = _device(q, "q")
     shape = (N, -(-cfg.K // group))
-    _flat(q, "q", (N, half), torch.uint8)
-    _flat(scales, "scales", shape, scales.dtype)
+    _flat(q, "q", (N, half), torch.uint8, dev)
+    _flat(scales, "scales", shape, scales.dtype, dev)
     if zeros is not None:
-        _flat(zeros, "zeros", shape, torch.uint8)
-    _same_device(q, scales, zeros)
-    other = _elsewhere(stream, q.device)
+        _flat(zeros, "zeros", shape, torch.uint8, dev)
+    other = None if stream is None else _elsewhere(stream, dev)
     if other is not None:
         return _on_stream(w4_pack, other, (q, scales, zeros), q, scales, zeros, group=group)
-    packed = torch.empty(L.gemm_rs_w4_packed_bytes(ctypes.byref(cfg)), dtype=torch.uint8, device=q.device)
+    packed = q.new_empty(L.gemm_rs_w4_packed_bytes(ctypes.byref(cfg)))
     _check(L.gemm_rs_w4_pack(ctypes.byref(cfg), q.data_ptr(), scales.data_ptr(),
-                             None if zeros is None else zeros.data_ptr(), packed.data_ptr(), _current(q.device)),
+                             None if zeros is None else zeros.data_ptr(), packed.data_ptr(), _raw_stream(dev)),
            "gemm_rs_w4_pack")
     return W4Weight(packed, cfg, scales.dtype)
 
@@ -234,21 +245,28 @@ def w4_pack(q, scales, zeros=None, *, group, stream=None) -> W4Weight:
 def w4_linear(x, weight: W4Weight, out=None, *, stream=None):
     """y = x w^T for x [M][K] (any M; made for few rows), FP32 accumulation, rounded once to x's type."""
     M, _ = _two(x, "x")
-    xs = _rows(x, "x", (M, weight.K), weight.dtype)
-    if out is not None:
-        ys = _rows(out, "out", (M, weight.N), weight.dtype)
-    _same_device(x, weight.packed, out)
-    other = _elsewhere(stream, x.device)
-    if other is not None:
-        return _on_stream(w4_linear, other, (x, weight.packed, out), x, weight, out)
+    N, dtype = weight.N, weight.dtype
+    dev = _device(x, "x")
+    xs = _rows(x, "x", M, weight.K, dtype, dev)
+    if weight.packed.get_device() != dev:
+        raise ValueError(f"weight: on {weight.packed.device}, not on the current device")
+    ys = N if out is None else _rows(out, "out", M, N, dtype, dev)
+    if stream is not None:
+        other = _elsewhere(stream, dev)
+        if other is not None:
+            return _on_stream(w4_linear, other, (x, weight.packed, out), x, weight, out)
     if out is None:
-        out, ys = x.new_empty((M, weight.N)), weight.N
+        out = x.new_empty((M, N))
     _check(lib().gemm_rs_w4_linear(weight.ref, weight.packed.data_ptr(), M, x.data_ptr(), xs, out.data_ptr(), ys,
-                                   _current(x.device)), "gemm_rs_w4_linear")
+                                   _raw_stream(dev)), "gemm_rs_w4_linear")
     return out
 
 
 # ---- block norm -----------------------------------------------------------------------
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
 
 class BlockNorm:
     """Outputs of block_norm: h, z (None without a pre weight), and with save=True y and rstd."""
@@ -268,21 +286,46 @@ class BlockNormGrads:
         self.residual, self.y, self.pre_weight, self.post_weight, self.gate = residual, y, pre_weight, post_weight, gate
 
 
-def _gate(gate, S, N, dtype):
+def _gate(gate, S, N, dtype, dev):
     """(kind, row stride) of a gate: [N] for every row, [S][1] per row or [S][N]."""
-    if gate is None:
-        return GATE_NONE, 0
     if gate.dim() == 1:
-        _flat(gate, "gate", (N,), dtype)
+        _flat(gate, "gate", (N,), dtype, dev)
         return GATE_CHANNEL, 0
     if gate.shape == (S, 1) and N != 1:
-        _flat(gate, "gate", (S, 1), dtype)
+        _flat(gate, "gate", (S, 1), dtype, dev)
         return GATE_TOKEN, 0
-    return GATE_FULL, _rows(gate, "gate", (S, N), dtype)
+    return GATE_FULL, _rows(gate, "gate", S, N, dtype, dev)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _weight(t, name, N, dtype, dev):
+    if t is None:
+        return 0
+    _flat(t, name, (N,), dtype, dev)
+    return t.data_ptr()
+
+
+def _parts(parts, dev):
+    """(first, pointers, row stride) of a [S][N] tensor, a list of them or a [P][S][N] tensor."""
+    if isinstance(parts, torch.Tensor):
+        if parts.dim() == 2:
+            return parts, (parts.data_ptr(),), _rows(parts, "parts", *parts.shape, parts.dtype, dev)
+        if parts.dim() != 3 or not 1 <= parts.shape[0] <= NORM_MAX_PARTS:
+            raise ValueError(f"parts: [S][N], or 1 to {NORM_MAX_PARTS} of them, got shape {tuple(parts.shape)}")
+        first = parts[0]
+        step, base = parts.stride(0) * parts.element_size(), parts.data_ptr()
+        stride = _rows(first, "parts[0]", *first.shape, first.dtype, dev)
+        return first, [base + i * step for i in range(parts.shape[0])], stride
+    if not 1 <= len(parts) <= NORM_MAX_PARTS:
+        raise ValueError(f"parts: 1 to {NORM_MAX_PARTS}, got {len(parts)}")
+    first = parts[0]
+    S, N = _two(first, "parts[0]")
+    strides = [_rows(p, f"parts[{i}]", S, N, first.dtype, dev) for i, p in enumerate(parts)]
+    if strides != strides[:1] * len(parts):
+        raise ValueError(f"parts: row strides differ: {strides}")
+    return first, [p.data_ptr() for p in parts], strides[0]
+
+
+_NO_PARTS = tuple((0,) * (NORM_MAX_PARTS - n) for n in range(NORM_MAX_PARTS + 1))
 
 
 def block_norm(parts, residual=None, *, pre_weight=None, post_weight=None, gate=None, block_scale=1.0,
@@ -298,60 +341,56 @@ def block_norm(parts, residual=None, *, pre_weight=None, post_weight=None, gate=
     gate: [N], [S][1] or [S][N].  h may be the residual itself, to update it in place.
     save=True also returns y and rstd ([2][S] float32: 1 / rms(y), 1 / rms(h)) for block_norm_backward.
     """
-    if isinstance(parts, torch.Tensor):
-        parts = list(parts.unbind(0)) if parts.dim() == 3 else [parts]
-    if not 1 <= len(parts) <= NORM_MAX_PARTS:
-        raise ValueError(f"parts: 1 to {NORM_MAX_PARTS}, got {len(parts)}")
-    first = parts[0]
-    S, N = shape = _two(first, "parts[0]")
+    if not isinstance(parts, torch.Tensor) and not parts:
+        raise ValueError(f"parts: 1 to {NORM_MAX_PARTS}, got none")
+    dev = _device(parts if isinstance(parts, torch.Tensor) else parts[0], "parts")
+    first, pointers, part_stride = _parts(parts, dev)
+    S, N = first.shape
     dtype = first.dtype
-    if dtype not in _CODES:
+    code = _CODES.get(dtype)
+    if code is None:
         raise TypeError(f"parts: expected bfloat16, float16 or float32, got {dtype}")
-    a = gemm_rs_norm_args()
-    for i, p in enumerate(parts):
-        stride = _rows(p, f"parts[{i}]", shape, dtype)
-        if i == 0:
-            a.part_stride = stride
-        elif stride != a.part_stride:
-            raise ValueError(f"parts[{i}]: row stride {stride} != {a.part_stride} of parts[0]")
-        a.parts[i] = p.data_ptr()
-    rdtype = dtype
+    rdtype, residual_ptr, residual_stride = dtype, 0, 0
     if residual is not None:
         rdtype = residual.dtype
         if rdtype is not dtype and rdtype is not torch.float32:
             raise TypeError(f"residual: expected {dtype} or float32, got {rdtype}")
-        a.residual, a.residual_stride = residual.data_ptr(), _rows(residual, "residual", shape, rdtype)
-    elif h is not None:
-        rdtype = h.dtype if h.dtype is torch.float32 else dtype
-    kind, a.gate_stride = _gate(gate, S, N, dtype)
-    a.gate = _ptr(gate)
-    for t, name in ((pre_weight, "pre_weight"), (post_weight, "post_weight")):
-        if t is not None:
-            _flat(t, name, (N,), dtype)
-            setattr(a, name, t.data_ptr())
+        residual_ptr, residual_stride = residual.data_ptr(), _rows(residual, "residual", S, N, rdtype, dev)
+    elif h is not None and h.dtype is torch.float32:
+        rdtype = torch.float32
+    kind = gate_ptr = gate_stride = 0
+    if gate is not None:
+        kind, gate_stride = _gate(gate, S, N, dtype, dev)
+        gate_ptr = gate.data_ptr()
+    pre, post = _weight(pre_weight, "pre_weight", N, dtype, dev), _weight(post_weight, "post_weight", N, dtype, dev)
+    h_stride = N if h is None else _rows(h, "h", S, N, rdtype, dev)
+    z_stride = N if z is None else _rows(z, "z", S, N, dtype, dev)
     if z is not None and pre_weight is None:
         raise ValueError("z: needs a pre_weight")
-    _same_device(first, *parts, residual, gate, pre_weight, post_weight, h, z)
-    other = _elsewhere(stream, first.device)
-    if other is not None:
-        return _on_stream(block_norm, other, (*parts, residual, gate, pre_weight, post_weight, h, z), parts, residual,
-                          pre_weight=pre_weight, post_weight=post_weight, gate=gate, block_scale=block_scale,
-                          residual_scale=residual_scale, eps=eps, save=save, h=h, z=z)
-    new = first.new_empty
+    if stream is not None:
+        other = _elsewhere(stream, dev)
+        if other is not None:
+            used = [parts] if isinstance(parts, torch.Tensor) else list(parts)
+            return _on_stream(block_norm, other, used + [residual, gate, pre_weight, post_weight, h, z], parts, residual,
+                              pre_weight=pre_weight, post_weight=post_weight, gate=gate, block_scale=block_scale,
+                              residual_scale=residual_scale, eps=eps, save=save, h=h, z=z)
     if h is None:
-        h = new(shape, dtype=rdtype)
-    a.h, a.h_stride = h.data_ptr(), _rows(h, "h", shape, rdtype)
+        h = first.new_empty((S, N)) if rdtype is dtype else first.new_empty((S, N), dtype=rdtype)
+    z_ptr = y_ptr = rstd_ptr = 0
+    y = rstd = None
     if pre_weight is not None:
         if z is None:
-            z = new(shape)
-        a.z, a.z_stride = z.data_ptr(), _rows(z, "z", shape, dtype)
-    y = rstd = None
+            z = first.new_empty((S, N))
+        z_ptr = z.data_ptr()
     if save:
-        y, rstd = new(shape), new((2, S), dtype=torch.float32)
-        a.y, a.y_stride, a.rstd = y.data_ptr(), N, rstd.data_ptr()
-    cfg = gemm_rs_norm_config(N, _CODES[dtype], _CODES[rdtype], len(parts), kind, int(post_weight is not None),
-                              int(pre_weight is not None), eps, block_scale, residual_scale)
-    _check(lib().gemm_rs_block_norm(ctypes.byref(cfg), S, ctypes.byref(a), _current(first.device)), "gemm_rs_block_norm")
+        y, rstd = first.new_empty((S, N)), first.new_empty((2, S), dtype=torch.float32)
+        y_ptr, rstd_ptr = y.data_ptr(), rstd.data_ptr()
+    n = len(pointers)
+    cfg = _NORM_CONFIG.pack(N, code, _CODES[rdtype], n, kind, post_weight is not None, pre_weight is not None, eps,
+                            block_scale, residual_scale)
+    args = _NORM_ARGS.pack(*pointers, *_NO_PARTS[n], part_stride, residual_ptr, residual_stride, post, gate_ptr,
+                           gate_stride, pre, h.data_ptr(), h_stride, z_ptr, z_stride, y_ptr, N, rstd_ptr)
+    _check(lib().gemm_rs_block_norm(cfg, S, args, _raw_stream(dev)), "gemm_rs_block_norm")
     return BlockNorm(h, z, y, rstd)
 
 
@@ -366,63 +405,64 @@ def block_norm_backward(dz, dh, h, y, rstd, *, pre_weight=None, post_weight=None
     like = dz if dz is not None else y
     if like is None:
         raise ValueError("dz or y is needed")
-    S, N = shape = _two(like, "dz" if dz is not None else "y")
+    name = "dz" if dz is not None else "y"
+    S, N = _two(like, name)
+    dev = _device(like, name)
     dtype = like.dtype
-    if dtype not in _CODES:
-        raise TypeError(f"dz, y: expected bfloat16, float16 or float32, got {dtype}")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {dtype}")
     stream_of = dh if dh is not None else h
     rdtype = dtype if stream_of is None else stream_of.dtype
     if rdtype is not dtype and rdtype is not torch.float32:
         raise TypeError(f"dh, h: expected {dtype} or float32, got {rdtype}")
-    a = gemm_rs_norm_grad_args()
-    kind, a.gate_stride = _gate(gate, S, N, dtype)
-    a.gate = _ptr(gate)
+    kind = gate_ptr = gate_stride = 0
+    if gate is not None:
+        kind, gate_stride = _gate(gate, S, N, dtype, dev)
+        gate_ptr = gate.data_ptr()
+    pre, post = _weight(pre_weight, "pre_weight", N, dtype, dev), _weight(post_weight, "post_weight", N, dtype, dev)
+    dz_ptr = dz_stride = h_ptr = h_stride = y_ptr = y_stride = dh_ptr = dh_stride = rstd_ptr = 0
     if pre_weight is not None:
         if dz is None or h is None:
             raise ValueError("a pre_weight needs dz and h")
-        _flat(pre_weight, "pre_weight", (N,), dtype)
-        a.pre_weight = pre_weight.data_ptr()
-        a.dz, a.dz_stride = dz.data_ptr(), _rows(dz, "dz", shape, dtype)
-        a.h, a.h_stride = h.data_ptr(), _rows(h, "h", shape, rdtype)
-    if post_weight is not None:
-        _flat(post_weight, "post_weight", (N,), dtype)
-        a.post_weight = post_weight.data_ptr()
+        dz_ptr, dz_stride = dz.data_ptr(), _rows(dz, "dz", S, N, dtype, dev)
+        h_ptr, h_stride = h.data_ptr(), _rows(h, "h", S, N, rdtype, dev)
     if post_weight is not None or gate is not None:
         if y is None:
             raise ValueError("a post_weight or a gate needs y")
-        a.y, a.y_stride = y.data_ptr(), _rows(y, "y", shape, dtype)
+        y_ptr, y_stride = y.data_ptr(), _rows(y, "y", S, N, dtype, dev)
     if pre_weight is not None or post_weight is not None:
         if rstd is None:
             raise ValueError("a pre_weight or post_weight needs rstd")
-        _flat(rstd, "rstd", (2, S), torch.float32)
-        a.rstd = rstd.data_ptr()
+        _flat(rstd, "rstd", (2, S), torch.float32, dev)
+        rstd_ptr = rstd.data_ptr()
     if dh is not None:
-        a.dh, a.dh_stride = dh.data_ptr(), _rows(dh, "dh", shape, rdtype)
-    _same_device(like, dz, dh, h, y, rstd, pre_weight, post_weight, gate)
-    other = _elsewhere(stream, like.device)
-    if other is not None:
-        return _on_stream(block_norm_backward, other, (dz, dh, h, y, rstd, pre_weight, post_weight, gate), dz, dh, h, y,
-                          rstd, pre_weight=pre_weight, post_weight=post_weight, gate=gate, block_scale=block_scale,
-                          residual_scale=residual_scale)
+        dh_ptr, dh_stride = dh.data_ptr(), _rows(dh, "dh", S, N, rdtype, dev)
+    if stream is not None:
+        other = _elsewhere(stream, dev)
+        if other is not None:
+            return _on_stream(block_norm_backward, other, (dz, dh, h, y, rstd, pre_weight, post_weight, gate), dz, dh, h,
+                              y, rstd, pre_weight=pre_weight, post_weight=post_weight, gate=gate,
+                              block_scale=block_scale, residual_scale=residual_scale)
     new = like.new_empty
-    dres, dy = new(shape, dtype=rdtype), new(shape)
-    a.dresidual, a.dresidual_stride, a.dy, a.dy_stride = dres.data_ptr(), N, dy.data_ptr(), N
-    dpre = new(N, dtype=torch.float32) if pre_weight is not None else None
-    dpost = new(N, dtype=torch.float32) if post_weight is not None else None
+    dy = new((S, N))
+    dres = new((S, N)) if rdtype is dtype else new((S, N), dtype=rdtype)
+    dpre = new(N, dtype=torch.float32) if pre else None
+    dpost = new(N, dtype=torch.float32) if post else None
     dgate = None
     if kind == GATE_CHANNEL:
         dgate = new(N, dtype=torch.float32)
     elif kind != GATE_NONE:
         dgate = new(gate.shape)
-        a.dgate_stride = N
-    a.dpre_weight, a.dpost_weight, a.dgate = _ptr(dpre), _ptr(dpost), _ptr(dgate)
-    cfg = gemm_rs_norm_config(N, _CODES[dtype], _CODES[rdtype], 1, kind, int(post_weight is not None),
-                              int(pre_weight is not None), 0.0, block_scale, residual_scale)
-    L, ref = lib(), ctypes.byref(cfg)
-    size = L.gemm_rs_block_norm_workspace(ref, S)
-    ws = new(size, dtype=torch.uint8)
-    _check(L.gemm_rs_block_norm_backward(ref, S, ctypes.byref(a), ws.data_ptr(), size, _current(like.device)),
-           "gemm_rs_block_norm_backward")
+    cfg = _NORM_CONFIG.pack(N, code, _CODES[rdtype], 1, kind, post_weight is not None, pre_weight is not None, 0.0,
+                            block_scale, residual_scale)
+    args = _NORM_GRAD_ARGS.pack(dz_ptr, dz_stride, dh_ptr, dh_stride, h_ptr, h_stride, y_ptr, y_stride, rstd_ptr, post,
+                                gate_ptr, pre, gate_stride, dres.data_ptr(), N, dy.data_ptr(), N, _ptr(dpre),
+                                _ptr(dpost), _ptr(dgate), N)
+    L = lib()
+    size = L.gemm_rs_block_norm_workspace(cfg, S)
+    ws = new(size // 4, dtype=torch.float32) if size else None
+    _check(L.gemm_rs_block_norm_backward(cfg, S, args, _ptr(ws), size, _raw_stream(dev)), "gemm_rs_block_norm_backward")
     return BlockNormGrads(dres, dy, dpre, dpost, dgate)
 
 
@@ -439,8 +479,9 @@ class Checkpoint:
         M, _ = _two(q, "q")
         if dtype not in _CODES:
             raise TypeError(f"dtype: expected bfloat16, float16 or float32, got {dtype}")
-        _flat(q, "q", (M, blocks * CKPT_BLOCK), torch.int8)
-        _flat(exps, "exps", (M, blocks), torch.int8)
+        dev = q.get_device()
+        _flat(q, "q", (M, blocks * CKPT_BLOCK), torch.int8, dev)
+        _flat(exps, "exps", (M, blocks), torch.int8, dev)
         self.q, self.exps, self.K, self.dtype = q, exps, K, dtype
 
 
@@ -448,36 +489,42 @@ def ckpt_pack(x, *, stream=None) -> Checkpoint:
     """Keeps x [M][K] (bfloat16, float16 or float32) in 8 bits: round(x 2^-e) with e = floor(log2(max |x|)) - 6 for
     every 32 columns of a row."""
     M, K = _two(x, "x")
-    if x.dtype not in _CODES:
-        raise TypeError(f"x: expected bfloat16, float16 or float32, got {x.dtype}")
+    dtype = x.dtype
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"x: expected bfloat16, float16 or float32, got {dtype}")
     if K < 1:
         raise ValueError("x: needs at least one column")
-    xs = _rows(x, "x", (M, K), x.dtype)
-    _same_device(x)
-    other = _elsewhere(stream, x.device)
-    if other is not None:
-        return _on_stream(ckpt_pack, other, (x,), x)
+    dev = _device(x, "x")
+    xs = _rows(x, "x", M, K, dtype, dev)
+    if stream is not None:
+        other = _elsewhere(stream, dev)
+        if other is not None:
+            return _on_stream(ckpt_pack, other, (x,), x)
     blocks = -(-K // CKPT_BLOCK)
     q = x.new_empty((M, blocks * CKPT_BLOCK), dtype=torch.int8)
-    exps = x.new_empty((M, blocks), dtype=torch.int8)
-    _check(lib().gemm_rs_ckpt_pack(_CODES[x.dtype], M, K, x.data_ptr(), xs, q.data_ptr(), exps.data_ptr(),
-                                   _current(x.device)), "gemm_rs_ckpt_pack")
-    return Checkpoint(q, exps, K, x.dtype)
+    exps = q.new_empty((M, blocks))
+    _check(lib().gemm_rs_ckpt_pack(code, M, K, x.data_ptr(), xs, q.data_ptr(), exps.data_ptr(), _raw_stream(dev)),
+           "gemm_rs_ckpt_pack")
+    kept = Checkpoint.__new__(Checkpoint)
+    kept.q, kept.exps, kept.K, kept.dtype = q, exps, K, dtype
+    return kept
 
 
 def ckpt_unpack(kept: Checkpoint, out=None, *, stream=None):
     """The values a checkpoint stands for, in the type it was made from."""
-    shape = (kept.q.shape[0], kept.K)
-    if out is not None:
-        stride = _rows(out, "out", shape, kept.dtype)
-    _same_device(kept.q, kept.exps, out)
-    other = _elsewhere(stream, kept.q.device)
-    if other is not None:
-        return _on_stream(ckpt_unpack, other, (kept.q, kept.exps, out), kept, out)
+    q, K = kept.q, kept.K
+    M = q.shape[0]
+    dev = _device(q, "checkpoint")
+    xs = K if out is None else _rows(out, "out", M, K, kept.dtype, dev)
+    if stream is not None:
+        other = _elsewhere(stream, dev)
+        if other is not None:
+            return _on_stream(ckpt_unpack, other, (q, kept.exps, out), kept, out)
     if out is None:
-        out, stride = kept.q.new_empty(shape, dtype=kept.dtype), kept.K
-    _check(lib().gemm_rs_ckpt_unpack(_CODES[kept.dtype], shape[0], kept.K, kept.q.data_ptr(), kept.exps.data_ptr(),
-                                     out.data_ptr(), stride, _current(out.device)), "gemm_rs_ckpt_unpack")
+        out = q.new_empty((M, K), dtype=kept.dtype)
+    _check(lib().gemm_rs_ckpt_unpack(_CODES[kept.dtype], M, K, q.data_ptr(), kept.exps.data_ptr(), out.data_ptr(), xs,
+                                     _raw_stream(dev)), "gemm_rs_ckpt_unpack")
     return out
 
 
@@ -488,32 +535,33 @@ def ckpt_wgrad(dy, kept: Checkpoint, *, add=None, out=None, dtype=torch.float32,
     dtype: float32 or dy's (out's, if given).  out may be `add` (float32): gradients accumulated in place.
     """
     M, N = _two(dy, "dy")
-    if dy.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"dy: expected bfloat16 or float16, got {dy.dtype}")
-    if dy.dtype is torch.float16 and kept.dtype is not torch.float16:
+    dev = _device(dy, "dy")
+    ydtype, q, K = dy.dtype, kept.q, kept.K
+    if ydtype is not torch.bfloat16 and ydtype is not torch.float16:
+        raise TypeError(f"dy: expected bfloat16 or float16, got {ydtype}")
+    if ydtype is torch.float16 and kept.dtype is not torch.float16:
         raise TypeError(f"dy: float16 with a checkpoint of {kept.dtype}")
-    if kept.q.shape[0] != M:
-        raise ValueError(f"dy has {M} rows, the checkpoint {kept.q.shape[0]}")
-    K = kept.K
+    if q.shape[0] != M:
+        raise ValueError(f"dy has {M} rows, the checkpoint {q.shape[0]}")
+    if q.get_device() != dev:
+        raise ValueError(f"checkpoint: on {q.device}, not on the current device")
     if out is not None:
         dtype = out.dtype
-    if dtype is not torch.float32 and dtype is not dy.dtype:
-        raise TypeError(f"dtype: expected float32 or {dy.dtype}, got {dtype}")
-    a = gemm_rs_wgrad_args(_CODES[dy.dtype], _CODES[dtype], M, N, K, dy.data_ptr(), _rows(dy, "dy", (M, N), dy.dtype),
-                           kept.q.data_ptr(), kept.exps.data_ptr())
-    if add is not None:
-        a.add, a.add_stride = add.data_ptr(), _rows(add, "add", (N, K), torch.float32)
-    if out is not None:
-        a.dw, a.dw_stride = out.data_ptr(), _rows(out, "out", (N, K), dtype)
-    _same_device(dy, kept.q, kept.exps, add, out)
-    other = _elsewhere(stream, dy.device)
-    if other is not None:
-        return _on_stream(ckpt_wgrad, other, (dy, kept.q, kept.exps, add, out), dy, kept, add=add, out=out, dtype=dtype)
+    if dtype is not torch.float32 and dtype is not ydtype:
+        raise TypeError(f"dtype: expected float32 or {ydtype}, got {dtype}")
+    ys = _rows(dy, "dy", M, N, ydtype, dev)
+    add_stride = 0 if add is None else _rows(add, "add", N, K, torch.float32, dev)
+    out_stride = K if out is None else _rows(out, "out", N, K, dtype, dev)
+    if stream is not None:
+        other = _elsewhere(stream, dev)
+        if other is not None:
+            return _on_stream(ckpt_wgrad, other, (dy, q, kept.exps, add, out), dy, kept, add=add, out=out, dtype=dtype)
     if out is None:
-        out = dy.new_empty((N, K), dtype=dtype)
-        a.dw, a.dw_stride = out.data_ptr(), K
-    L, ref = lib(), ctypes.byref(a)
-    size = L.gemm_rs_ckpt_wgrad_workspace(ref)
-    ws = dy.new_empty(size, dtype=torch.uint8)
-    _check(L.gemm_rs_ckpt_wgrad(ref, ws.data_ptr(), size, _current(dy.device)), "gemm_rs_ckpt_wgrad")
+        out = dy.new_empty((N, K)) if dtype is ydtype else dy.new_empty((N, K), dtype=dtype)
+    args = _WGRAD_ARGS.pack(_CODES[ydtype], _CODES[dtype], M, N, K, dy.data_ptr(), ys, q.data_ptr(),
+                            kept.exps.data_ptr(), _ptr(add), add_stride, out.data_ptr(), out_stride)
+    L = lib()
+    size = L.gemm_rs_ckpt_wgrad_workspace(args)
+    ws = q.new_empty(size) if size else None
+    _check(L.gemm_rs_ckpt_wgrad(args, _ptr(ws), size, _raw_stream(dev)), "gemm_rs_ckpt_wgrad")
     return out

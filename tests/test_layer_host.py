@@ -128,6 +128,20 @@ def test_calls_without_rows_or_with_bad_arguments_touch_no_gpu():
         assert L.gemm_rs_layer_strerror(code).decode()
 
 
+def test_packed_argument_blocks_match_the_structures():
+    for block, structure in ((layer._NORM_CONFIG, layer.gemm_rs_norm_config), (layer._NORM_ARGS, layer.gemm_rs_norm_args),
+                             (layer._NORM_GRAD_ARGS, layer.gemm_rs_norm_grad_args),
+                             (layer._WGRAD_ARGS, layer.gemm_rs_wgrad_args)):
+        assert block.size == ctypes.sizeof(structure)
+        n = len(block.unpack(bytes(block.size)))
+        packed = structure.from_buffer_copy(block.pack(*range(1, n + 1)))
+        values = []
+        for name, _ in structure._fields_:
+            v = getattr(packed, name)
+            values += list(v) if isinstance(v, ctypes.Array) else [v]
+        assert [int(v) for v in values] == list(range(1, n + 1))
+
+
 def test_workspace_is_asked_for():
     size = layer.lib().gemm_rs_block_norm_workspace
     assert size(ctypes.byref(norm(post_norm=0)), 3) == 3 * 8192 * 4
