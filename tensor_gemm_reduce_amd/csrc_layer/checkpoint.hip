@@ -17,10 +17,17 @@ bool wgrad_fast(const gemm_rs_wgrad_args& g)
 
 constexpr int kWgMinSteps = 4;    // a share is at least this many steps of 64 tokens
 
+// The 256 x 256 tile reads and turns its operands half as often for the same outputs, but
+// starts and ends slower.  Measured, us (256 / 128): 2048 x 8192 x 3584 214 / 208 (32
+// steps), 4096 x 8192 x 1024 86 / 93 (64), 4096 x 1280 x 8192 111 / 131, 8192 x 6144 x
+// 2048 236 / 284 (128), 32768 x 8192 x 3584 1786 / 2657; with few tiles the shares are
+// short: 16384 x 2048 x 512 (16) 63 / 72, 16384 x 256 x 128 (1) 74 / 49.
+constexpr int kWgBigSteps = 40;
+
 WgradPlan wgrad_plan(const gemm_rs_wgrad_args& g, int& big)
 {
     auto tiles = [&](int t) { return ceil_div(g.N, t) * ceil_div(g.K, t); };
-    big = tiles(256) >= kCus / 2;
+    big = ceil_div(g.M, kWgRows) >= kWgBigSteps && tiles(256) >= 16;
     const int edge = big ? 256 : 128, slots = big ? kCus : 2 * kCus;
     WgradPlan p = {};
     p.tiles_n = (int)ceil_div(g.N, edge);

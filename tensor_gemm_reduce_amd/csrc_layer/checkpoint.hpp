@@ -316,7 +316,7 @@ constexpr int kWgRows = 64;   // tokens per step
 constexpr int kWgCol = 128;   // LDS bytes of a column's tokens
 
 // LDS offset of chunk c (8 tokens) of column r
-__device__ __forceinline__ int wgrad_at(int r, int c) { return r * kWgCol + ((c ^ r ^ (r >> 3)) & 7) * 16; }
+__device__ __forceinline__ int wgrad_at(int r, int c) { return (r ^ ((r >> 6) & 1)) * kWgCol + ((c ^ r ^ (r >> 3)) & 7) * 16; }
 
 // A thread's share of a step: 8 tokens x 8 columns of dy and of the checkpoint.
 struct WgradRegs {
@@ -405,120 +405,175 @@ struct WgradTile {
     static constexpr int kLds = 2 * kStage;
 };
 
+// LDS offsets of a thread in each of the two stages: its first column of eight as a
+// loader (column j's chunk lies at offset ^ j (kWgCol + 16)), and its column of the
+// wave's first fragment, first chunk, as a reader: 16 tokens on, one block on or two
+// change that by an exclusive or of 32, 64 and kWgCol.  Kept to these few registers:
+// hide() takes their constancy from the compiler, or every sum would get a register.
+template <class T, int WN, int WK>
+struct WgradPlaces {
+    typedef WgradTile<WN, WK> Tile;
+    typedef typename Mfma<T>::frag frag;
+    static constexpr int kX = Tile::kBN * kWgCol;  // the checkpoint's columns after dy's
+    static constexpr int kPer = Tile::kBN / 8;     // threads side by side
+
+    char* const lds;
+    uint32_t put[2], get_y[2], get_x[2];
+
+    __device__ __forceinline__ explicit WgradPlaces(char* l) : lds(l)
+    {
+        static_assert(WN == WK, "square tiles");
+        const int tg = threadIdx.x / kPer % 8, cg = threadIdx.x % kPer, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            put[p] = p * Tile::kStage + wgrad_at(8 * cg, tg);
+            get_y[p] = p * Tile::kStage + wgrad_at((wave >> 1) * 32 * WN + (lane & 31), lane >> 5);
+            get_x[p] = p * Tile::kStage + wgrad_at((wave & 1) * 32 * WK + (lane & 31), lane >> 5);
+        }
+    }
+    __device__ __forceinline__ void hide(WgradLoader<T>& ld)
+    {
+        __asm__ __volatile__("" : "+v"(put[0]), "+v"(put[1]), "+v"(get_y[0]), "+v"(get_y[1]), "+v"(get_x[0]),
+                             "+v"(get_x[1]), "+v"(ld.yoff), "+v"(ld.xoff), "+v"(ld.eoff));
+    }
+    template <int P>
+    __device__ __forceinline__ void write(int j, bool x, const u32x4& v) const
+    {
+        *reinterpret_cast<u32x4*>(lds + (put[P] ^ (uint32_t)(j * (kWgCol + 16))) + (x ? kX : 0)) = v;
+    }
+    // the fragment of block b and 16 tokens `sub` of dy or the checkpoint
+    template <int P>
+    __device__ __forceinline__ frag read(int sub, int b, bool x) const
+    {
+        const uint32_t flip = 32u * sub ^ 64u * (b & 1) ^ (uint32_t)kWgCol * (b >> 1);
+        return *reinterpret_cast<const frag*>(lds + ((x ? get_x[P] : get_y[P]) ^ flip) + b * 32 * kWgCol + (x ? kX : 0));
+    }
+    static __device__ __forceinline__ void barrier()
+    {
+        __asm__ __volatile__("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+};
+
 // One tile over the steps s0 .. s1 - 1, tiles of 128 x 128: two workgroups share a CU
 // and cover each other's waits.  Waves 0 and 1 load and turn dy, waves 2 and 3 the
-// checkpoint, a step ahead.
-template <class T>
-__device__ __forceinline__ void wgrad_run_tile(const WgradArgs& a, char* lds, int tn, int tk, int64_t s0, int64_t s1,
-                                               f32x16 (&acc)[2][2])
-{
-    typedef WgradTile<2, 2> Tile;
-    typedef typename Mfma<T>::frag frag;
-    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
-    const int tg = (threadIdx.x >> 4) & 7, cg = threadIdx.x & 15;
-    WgradLoader<T> ld(a, tg, tn * Tile::kBN + 8 * cg, tk * Tile::kBK + 8 * cg, s1);
-    WgradRegs r;
-    auto load = [&](int64_t step) {
+// checkpoint (X), two steps ahead in two sets of registers.
+template <class T, bool X>
+struct WgradSmall : WgradPlaces<T, 2, 2> {
+    typedef WgradPlaces<T, 2, 2> Places;
+    typedef typename Places::frag frag;
+
+    f32x16 (&acc)[2][2];
+    WgradLoader<T> ld;
+    WgradRegs r[2];
+
+    __device__ __forceinline__ WgradSmall(const WgradArgs& a, char* l, int tn, int tk, int64_t s1, f32x16 (&c)[2][2])
+        : Places(l), acc(c),
+          ld(a, threadIdx.x / 16 % 8, tn * 128 + 8 * (threadIdx.x % 16), tk * 128 + 8 * (threadIdx.x % 16), s1)
+    {
+    }
+    __device__ __forceinline__ void load(WgradRegs& g, int64_t step)
+    {
         ld.at(step);
-        if (wave < 2) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ld.load_y(r, i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ld.load_x(r, i);
-            ld.load_e(r, 0);
-            ld.load_e(r, 1);
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (X) ld.load_x(g, i);
+            else ld.load_y(g, i);
         }
-    };
-    auto put = [&](char* stage) {
-        if (wave < 2) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<u32x4*>(stage + wgrad_at(8 * cg + j, tg)) =
-                    u32x4{wgrad_pair_y(r, j, 0), wgrad_pair_y(r, j, 1), wgrad_pair_y(r, j, 2), wgrad_pair_y(r, j, 3)};
-        } else {
-            float sc[8];
-            wgrad_scales(r, sc);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<u32x4*>(stage + Tile::kBN * kWgCol + wgrad_at(8 * cg + j, tg)) =
-                    u32x4{wgrad_pair_x<T>(r, sc, j, 0), wgrad_pair_x<T>(r, sc, j, 1), wgrad_pair_x<T>(r, sc, j, 2),
-                          wgrad_pair_x<T>(r, sc, j, 3)};
+        if constexpr (X) {
+            ld.load_e(g, 0);
+            ld.load_e(g, 1);
         }
-    };
-    load(s0);
-    put(lds);
-    load(s0 + 1);
-    __syncthreads();
-    for (int64_t s = s0; s < s1; ++s) {
-        const int cur = (int)(s - s0) & 1;
-        const char* stage = lds + cur * Tile::kStage;
+    }
+    template <int P>
+    __device__ __forceinline__ void put_all(const WgradRegs& g) const
+    {
+        float sc[8];
+        if constexpr (X) wgrad_scales(g, sc);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            u32x4 v;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                if constexpr (X) v[p] = wgrad_pair_x<T>(g, sc, j, p);
+                else v[p] = wgrad_pair_y(g, j, p);
+            }
+            this->template write<P>(j, X, v);
+        }
+    }
+    // stage s is written in buffer P, step s + 1's data in r[P ^ 1] or on its way there
+    template <int P>
+    __device__ __forceinline__ void step(int64_t s)
+    {
+        this->hide(ld);
+        load(r[P], s + 2);
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub) {
             frag fy[2], fx[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int c = 2 * sub + (lane >> 5);
-                fy[i] = *reinterpret_cast<const frag*>(stage + wgrad_at((wave >> 1) * 64 + i * 32 + (lane & 31), c));
-                fx[i] = *reinterpret_cast<const frag*>(stage + Tile::kBN * kWgCol +
-                                                       wgrad_at((wave & 1) * 64 + i * 32 + (lane & 31), c));
+                fx[i] = this->template read<P>(sub, i, true);
+                fy[i] = this->template read<P>(sub, i, false);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) acc[i][j] = Mfma<T>::run(fx[j], fy[i], acc[i][j]);
         }
-        if (s + 1 < s1) put(lds + (cur ^ 1) * Tile::kStage);
-        if (s + 2 < s1) load(s + 2);
-        __syncthreads();
+        put_all<P ^ 1>(r[P ^ 1]);
+        this->barrier();
     }
+    __device__ __forceinline__ void run(int64_t s0, int64_t s1)
+    {
+        load(r[0], s0);
+        load(r[1], s0 + 1);
+        put_all<0>(r[0]);
+        this->barrier();
+        // in twos: a step past the range multiplies the zeros its loads gave
+        for (int64_t s = s0; s < s1; s += 2) {
+            step<0>(s);
+            step<1>(s + 1);
+        }
+    }
+};
+
+template <class T>
+__device__ __forceinline__ void wgrad_run_tile(const WgradArgs& a, char* lds, int tn, int tk, int64_t s0, int64_t s1,
+                                               f32x16 (&acc)[2][2])
+{
+    // the same barriers in both
+    if (uni(threadIdx.x >> 6) < 2) WgradSmall<T, false>(a, lds, tn, tk, s1, acc).run(s0, s1);
+    else WgradSmall<T, true>(a, lds, tn, tk, s1, acc).run(s0, s1);
 }
 
 // The same for tiles of 256 x 256: one workgroup per CU, one wave per SIMD, whose 256
-// accumulators leave no second wave to cover a wait.  Every other instruction of a
-// step therefore has a place after one of its 64 MFMAs, and fences keep it there:
-//   MFMA 16 u ..     (u = 0, 1, 2) the fragment reads of the next 16 tokens,
-//   MFMA 0 .. 31     the next step's checkpoint, a column every four MFMAs,
-//   MFMA 32 .. 47    the next step's dy, two columns every four,
-//   MFMA 0 .. 35     the loads of the step after that, into the other set of
-//                    registers: they have more than a step (2048 cycles) to arrive,
-//   before MFMA 48   the barrier: the next step is written, and the buffer that the
-//                    step after will be written to has been read,
-//   MFMA 48 ..       the fragment reads of the next step's first 16 tokens.
+// accumulators leave no second wave to cover a wait.  So every other instruction of a
+// step has a place after one of its 64 MFMAs, and fences keep it there; they are spread
+// evenly, since what does not fit under an MFMA's 32 cycles (or under the LDS queue's
+// pace, some 28 cycles per 16-byte instruction of one wave) adds to the step.
+//
+// A step runs from barrier to barrier.  At its start stage s is written, and the other
+// stage read but for fragments that are already in registers, so the whole step can
+// write stage s + 1:
+//   MFMA 0 ..     the last 16 tokens of step s - 1, then the first 48 of step s; the
+//                 fragment reads go 16 tokens ahead, eight in the first twelve places
+//   MFMA 7 j ..   column j of the thread's eight, of the checkpoint (a pair of tokens
+//                 every other place) and of dy (between them), each written when done
+//   the loads     of step s + 2, into the other set of registers: more than a step to
+//                 arrive
 template <class T>
-struct WgradBig {
-    typedef WgradTile<4, 4> Tile;
-    typedef typename Mfma<T>::frag frag;
+struct WgradBig : WgradPlaces<T, 4, 4> {
+    typedef WgradPlaces<T, 4, 4> Places;
+    typedef typename Places::frag frag;
 
-    const WgradArgs& a;
-    char* const lds;
     f32x16 (&acc)[4][4];
     WgradLoader<T> ld;
-    // LDS offsets in each of the two stages: this thread's first column of eight (column
-    // j's chunk lies at offset ^ 16 j), and this lane's column of the first fragment
-    // (x then dy) with the first chunk, where 16 tokens on or a block on changes the
-    // chunk by an exclusive or of 32 sub and 64 block.  Kept to these few registers: the
-    // step hides their constancy, or every sum would get a register of its own.
-    uint32_t put[2], get_y[2], get_x[2];
     WgradRegs r[2];
     frag fy[2][4], fx[2][4];
 
-    __device__ __forceinline__ WgradBig(const WgradArgs& args, char* l, int tn, int tk, int64_t s1, f32x16 (&c)[4][4])
-        : a(args), lds(l), acc(c),
-          ld(args, threadIdx.x >> 5, tn * Tile::kBN + 8 * (threadIdx.x & 31), tk * Tile::kBK + 8 * (threadIdx.x & 31), s1)
+    __device__ __forceinline__ WgradBig(const WgradArgs& a, char* l, int tn, int tk, int64_t s1, f32x16 (&c)[4][4])
+        : Places(l), acc(c), ld(a, threadIdx.x / 32, tn * 256 + 8 * (threadIdx.x % 32), tk * 256 + 8 * (threadIdx.x % 32), s1)
     {
-        const int tg = threadIdx.x >> 5, cg = threadIdx.x & 31, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            put[p] = p * Tile::kStage + wgrad_at(8 * cg, tg);
-            get_y[p] = p * Tile::kStage + wgrad_at((wave >> 1) * 128 + (lane & 31), lane >> 5);
-            get_x[p] = p * Tile::kStage + wgrad_at((wave & 1) * 128 + (lane & 31), lane >> 5);
-        }
-    }
-    __device__ __forceinline__ void hide()
-    {
-        __asm__ __volatile__("" : "+v"(put[0]), "+v"(put[1]), "+v"(get_y[0]), "+v"(get_y[1]), "+v"(get_x[0]),
-                             "+v"(get_x[1]), "+v"(ld.yoff), "+v"(ld.xoff), "+v"(ld.eoff));
     }
     __device__ __forceinline__ void load(WgradRegs& g, int i) const  // 0 .. 17
     {
@@ -526,60 +581,42 @@ struct WgradBig {
         else if (i < 10) ld.load_x(g, i - 2);
         else ld.load_y(g, i - 10);
     }
-    template <int P>
-    __device__ __forceinline__ void write(int j, bool x, const u32x4& v) const
-    {
-        *reinterpret_cast<u32x4*>(lds + (put[P] ^ (16u * j)) + j * kWgCol + (x ? Tile::kBN * kWgCol : 0)) = v;
-    }
-    template <int P>
-    __device__ __forceinline__ void read(int sub, int i, frag (&gy)[4], frag (&gx)[4]) const
-    {
-        const int b = i & 3;
-        const uint32_t flip = 32u * sub ^ 64u * (b & 1);
-        if (i < 4)
-            gy[b] = *reinterpret_cast<const frag*>(lds + (get_y[P] ^ flip) + b * 32 * kWgCol);
-        else
-            gx[b] = *reinterpret_cast<const frag*>(lds + (get_x[P] ^ flip) + b * 32 * kWgCol + Tile::kBN * kWgCol);
-    }
 
+    // Stage s in buffer P, step s + 1's data in r[P ^ 1].
     template <int P>
     __device__ __forceinline__ void step(int64_t s)
     {
-        hide();
+        this->hide(ld);
         WgradRegs& g = r[P ^ 1];
         ld.at(s + 2);
         float sc[8];
         wgrad_scales(g, sc);
-        u32x4 w0, w1;
+        u32x4 wx[2], wy;
 #pragma unroll
         for (int m = 0; m < 64; ++m) {
             const int u = m / 16, i = (m % 16) / 4, j = m % 4;
-            if (m == 48) {
-                __asm__ __volatile__("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                __builtin_amdgcn_sched_barrier(0);
+            // u = 0: fragments 3 of the step before, read into set 1
+            acc[i][j] = Mfma<T>::run(fx[(u + 1) & 1][j], fy[(u + 1) & 1][i], acc[i][j]);
+            const int q = m % 16;
+            if (q < 12 && q % 3 != 2) {
+                const int f = q / 3 * 2 + q % 3;  // the checkpoint's first: each MFMA row needs all four
+                if (f < 4) fx[u & 1][f] = this->template read<P>(u, f, true);
+                else fy[u & 1][f - 4] = this->template read<P>(u, f - 4, false);
             }
-            acc[i][j] = Mfma<T>::run(fx[u & 1][j], fy[u & 1][i], acc[i][j]);
-            if (m % 2 == 0) {
-                const int f = (m % 16) / 2;  // x fragments first: the next MFMA needs all four and one of dy's
-                if (u < 3) read<P>(u + 1, f ^ 4, fy[(u + 1) & 1], fx[(u + 1) & 1]);
-                else read<P ^ 1>(0, f ^ 4, fy[0], fx[0]);
-            } else if (m < 36) {
-                load(r[P], m / 2);
-            }
-            if (m < 32) {
-                w0[j] = wgrad_pair_x<T>(g, sc, m / 4, j);
-                if (j == 3) write<P ^ 1>(m / 4, true, w0);
-            } else if (m < 48) {
-                const int col = 2 * ((m - 32) / 4);
-                w0[j] = wgrad_pair_y(g, col, j);
-                w1[j] = wgrad_pair_y(g, col + 1, j);
-                if (j == 3) {
-                    write<P ^ 1>(col, false, w0);
-                    write<P ^ 1>(col + 1, false, w1);
+            if (m % 3 == 2 && m / 3 < 18) load(r[P], m / 3);
+            const int c = m / 7, k = m % 7;  // column and place in its seven
+            if (c < 8) {
+                if (k % 2 == 0) wx[c & 1][k / 2] = wgrad_pair_x<T>(g, sc, c, k / 2);
+                if (k % 2 == 1) wy[k / 2] = wgrad_pair_y(g, c, k / 2);
+                if (k == 5) {
+                    wy[3] = wgrad_pair_y(g, c, 3);
+                    this->template write<P ^ 1>(c, false, wy);
                 }
             }
+            if (c > 0 && k == 1) this->template write<P ^ 1>(c - 1, true, wx[(c - 1) & 1]);
             __builtin_amdgcn_sched_barrier(0);
         }
+        this->barrier();
     }
 
     __device__ __forceinline__ void run(int64_t s0, int64_t s1)
@@ -600,17 +637,22 @@ struct WgradBig {
                 x[p] = wgrad_pair_x<T>(r[0], sc, j, p);
                 y[p] = wgrad_pair_y(r[0], j, p);
             }
-            write<0>(j, false, y);
-            write<0>(j, true, x);
+            this->template write<0>(j, false, y);
+            this->template write<0>(j, true, x);
         }
-        __syncthreads();
+        // nothing before the first step: its first 16 MFMAs add zeros
 #pragma unroll
-        for (int i = 0; i < 8; ++i) read<0>(0, i, fy[0], fx[0]);
+        for (int i = 0; i < 4; ++i) fy[1][i] = fx[1][i] = frag{};
+        this->barrier();
         // in twos: a step past the range multiplies the zeros its loads gave
         for (int64_t s = s0; s < s1; s += 2) {
             step<0>(s);
             step<1>(s + 1);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = Mfma<T>::run(fx[1][j], fy[1][i], acc[i][j]);
         __syncthreads();
     }
 };

@@ -400,10 +400,9 @@ def wgrad_case(M, N, K, dtype, seed=0, integer=False):
 
 
 def wgrad_exact(dy, kept, add=None):
-    v = ref.ckpt_value(kept.q.cpu().numpy(), kept.exps.cpu().numpy(), kept.K)
-    d = ref.f64(dy)
-    with np.errstate(invalid="ignore"):
-        w, m = d.T @ v, np.abs(d).T @ np.abs(v)
+    v = torch.from_numpy(ref.ckpt_value(kept.q.cpu().numpy(), kept.exps.cpu().numpy(), kept.K))
+    d = dy.double().cpu().t()
+    w, m = (d @ v).numpy(), (d.abs() @ v.abs()).numpy()
     if add is not None:
         w, m = w + ref.f64(add), m + np.abs(ref.f64(add))
     return w, m
@@ -411,7 +410,7 @@ def wgrad_exact(dy, kept, add=None):
 
 WGRAD_SHAPES = [(1, 1, 1), (1, 8, 32), (2, 33, 31), (31, 128, 128), (32, 129, 130), (33, 100, 1000), (64, 256, 256),
                 (65, 264, 72), (257, 520, 264), (512, 1024, 128), (1000, 300, 200), (4100, 136, 96), (128, 1000, 1037),
-                (300, 776, 520)]
+                (300, 776, 520), (2570, 1030, 1000)]
 
 
 @pytest.mark.parametrize("M,N,K", WGRAD_SHAPES)
@@ -424,7 +423,10 @@ def test_wgrad(M, N, K, dtype):
         ref.assert_close(got, *wgrad_exact(dy, kept, a), -(-M // 16) + 40, f"{out_dtype} add={a is not None}")
 
 
-@pytest.mark.parametrize("M,N,K", [(40, 130, 70), (512, 1024, 256), (2048, 512, 520), (777, 264, 1000)])
+@pytest.mark.parametrize("M,N,K", [(40, 130, 70), (512, 1024, 256), (2048, 512, 520), (777, 264, 1000),
+                                   # tiles of 256 x 256: 16 tiles in shares, an odd number of steps, ragged in every
+                                   # direction; one whole round and a rest; a rest too short to cut
+                                   (2624, 1024, 1024), (2570, 1030, 1000), (2560, 4104, 4130), (2700, 4096, 4096)])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_wgrad_integers_are_exact(M, N, K, dtype):
     """Every sum is a multiple of 1/2 below 2^23, so FP32 holds it exactly whatever the order."""
@@ -450,9 +452,10 @@ def test_wgrad_in_place_strides_and_no_rows():
     assert torch.equal(layer.ckpt_wgrad(dy[:0], none), torch.zeros_like(add))
 
 
-def test_wgrad_special_values():
+@pytest.mark.parametrize("M,N,K", [(70, 140, 200), (2600, 1000, 1000)])
+def test_wgrad_special_values(M, N, K):
     """A NaN block reaches its 32 columns of every row, a NaN in dy its row of dw; nothing else changes."""
-    dy, kept = wgrad_case(70, 140, 200, BF16, seed=8)
+    dy, kept = wgrad_case(M, N, K, BF16, seed=8)
     clean = layer.ckpt_wgrad(dy, kept)
     kept.exps[13, 2] = layer.CKPT_NAN
     dy[50, 7] = float("nan")
