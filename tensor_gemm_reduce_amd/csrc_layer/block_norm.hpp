@@ -3,8 +3,6 @@
 // norm before the next block, and the gradients of all of them.
 #pragma once
 
-#include <type_traits>
-
 #include "common.hpp"
 
 namespace gemm_rs_layer {
@@ -136,10 +134,6 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
     }
 }
 
-// Keeps the loads of a later chunk from being moved up into registers that an
-// earlier one still needs.
-__device__ __forceinline__ void one_chunk_at_a_time() { __asm__ __volatile__("" ::: "memory"); }
-
 struct NormGradArgs {
     const void *dz, *dh, *h, *y;
     const float* rstd;
@@ -151,189 +145,226 @@ struct NormGradArgs {
     int n, gate_kind, sums;
 };
 
-// Workgroup g takes rows g, g + grid, ...  With t^ = t r (r = 1 / rms(t)) a norm
-// t^ w passes a gradient d on as r (w d - t^ mean(w d t^)); the statistics come
-// from the forward pass, so the two means are the only sums over a row (a third
-// one is the gradient of a gate per row).  The sums over rows stay in registers
-// and leave as one partial row per workgroup (norm_sums_kernel adds them).
-// WIDE (rows too wide for that): the inputs are read again where they are needed
-// again, from cache, and the sums over rows are kept in the workgroup's partial
-// row.
-template <class T, class R, int THREADS, int ITEMS, bool WIDE>
+// What a thread reads of a row: its eight columns of each input.
+template <class T, class R>
+struct NormGradRow {
+    vec8<T> dz, y, gate;
+    vec8<R> dh, h;
+
+    __device__ __forceinline__ void load(const NormGradArgs& a, int64_t row, int col)
+    {
+        dz = y = gate = vec8<T>{};
+        dh = h = vec8<R>{};
+        if (a.pre_weight) {
+            dz = load8(static_cast<const T*>(a.dz) + row * a.dz_stride, col, a.n);
+            h = load8(static_cast<const R*>(a.h) + row * a.h_stride, col, a.n);
+        }
+        if (a.dh) dh = load8(static_cast<const R*>(a.dh) + row * a.dh_stride, col, a.n);
+        if (a.post_weight || a.gate) y = load8(static_cast<const T*>(a.y) + row * a.y_stride, col, a.n);
+        if (a.gate_kind == GEMM_RS_GATE_FULL) gate = load8(static_cast<const T*>(a.gate) + row * a.gate_stride, col, a.n);
+    }
+};
+
+// Weights and sums over rows of a thread's eight columns.
+template <class T>
+struct NormGradColumns {
+    vec8<T> pre, post, gate;
+    float sum_pre[8], sum_post[8], sum_gate[8];
+
+    __device__ __forceinline__ void load(const NormGradArgs& a, int col)
+    {
+        pre = post = gate = vec8<T>{};
+        if (a.pre_weight) pre = load8(static_cast<const T*>(a.pre_weight), col, a.n);
+        if (a.post_weight) post = load8(static_cast<const T*>(a.post_weight), col, a.n);
+        if (a.gate_kind == GEMM_RS_GATE_CHANNEL) gate = load8(static_cast<const T*>(a.gate), col, a.n);
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum_pre[j] = sum_post[j] = sum_gate[j] = 0.f;
+    }
+    // the workgroup's partial row: [sums][n]
+    __device__ __forceinline__ void keep(const NormGradArgs& a, float* part, int col) const
+    {
+        if (a.pre_weight) {
+            store8(part, col, a.n, sum_pre);
+            part += a.n;
+        }
+        if (a.post_weight) {
+            store8(part, col, a.n, sum_post);
+            part += a.n;
+        }
+        if (a.gate_kind == GEMM_RS_GATE_CHANNEL) store8(part, col, a.n, sum_gate);
+    }
+    __device__ __forceinline__ void fetch(const NormGradArgs& a, const float* part, int col)
+    {
+        if (a.pre_weight) {
+            widen<float>(load8(part, col, a.n), sum_pre);
+            part += a.n;
+        }
+        if (a.post_weight) {
+            widen<float>(load8(part, col, a.n), sum_post);
+            part += a.n;
+        }
+        if (a.gate_kind == GEMM_RS_GATE_CHANNEL) widen<float>(load8(part, col, a.n), sum_gate);
+    }
+};
+
+// The arithmetic of one row, in three stages between the sums over the row.  With
+// t^ = t r (r = 1 / rms(t)) a norm t^ w passes a gradient d on as r (w d - t^ mean(w d t^)).
+template <class T, class R>
+struct NormGradMath {
+    const NormGradArgs& a;
+    float ry, rh, g_row;
+
+    __device__ __forceinline__ NormGradMath(const NormGradArgs& args, int64_t row) : a(args)
+    {
+        ry = a.post_weight ? a.rstd[row] : 1.f;
+        rh = a.pre_weight ? a.rstd[a.rows + row] : 0.f;
+        g_row = a.gate_kind == GEMM_RS_GATE_TOKEN ? (float)static_cast<const T*>(a.gate)[row] : 1.f;
+    }
+    // sum of w d t^ of the next block's norm
+    __device__ __forceinline__ float dot_h(const NormGradRow<T, R>& r, const NormGradColumns<T>& c) const
+    {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += (float)c.pre[j] * (float)r.dz[j] * ((float)r.h[j] * rh);
+        return s;
+    }
+    // through that norm, the residual's and the gate's gradients; leaves the block norm's w d in d
+    __device__ __forceinline__ void middle(const NormGradRow<T, R>& r, NormGradColumns<T>& c, float mean_h, int64_t row, int col,
+                                           float (&d)[8], float& dot_y, float& dot_gate) const
+    {
+        float o[8], dg[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float g = (float)r.dh[j];
+            if (a.pre_weight) {
+                const float hh = (float)r.h[j] * rh, z = (float)r.dz[j];
+                g += rh * ((float)c.pre[j] * z - hh * mean_h);
+                c.sum_pre[j] += z * hh;
+            }
+            o[j] = a.residual_scale * g;
+            const float yy = (float)r.y[j] * ry;
+            g *= a.block_scale;
+            dg[j] = g * (a.post_weight ? yy * (float)c.post[j] : yy);
+            dot_gate += dg[j];
+            if (a.gate_kind == GEMM_RS_GATE_CHANNEL) {
+                c.sum_gate[j] += dg[j];
+                g *= (float)c.gate[j];
+            }
+            if (a.gate_kind == GEMM_RS_GATE_FULL) g *= (float)r.gate[j];
+            g *= g_row;
+            if (a.post_weight) {
+                c.sum_post[j] += g * yy;
+                g *= (float)c.post[j];
+                dot_y += g * yy;
+            }
+            d[j] = g;
+        }
+        if (a.dresidual) store8(static_cast<R*>(a.dresidual) + row * a.dresidual_stride, col, a.n, o);
+        if (a.gate_kind == GEMM_RS_GATE_FULL) store8(static_cast<T*>(a.dgate) + row * a.dgate_stride, col, a.n, dg);
+    }
+    // through the block's own norm
+    __device__ __forceinline__ void last(const vec8<T>& y, float mean_y, int64_t row, int col, float (&d)[8]) const
+    {
+        if (a.post_weight) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[j] = ry * (d[j] - (float)y[j] * ry * mean_y);
+        }
+        store8(static_cast<T*>(a.dy) + row * a.dy_stride, col, a.n, d);
+    }
+};
+
+// Workgroup g takes rows g, g + grid, ..., a thread the same eight columns of each: the
+// weights and the sums over rows stay in its registers, and leave as one partial row per
+// workgroup (norm_sums_kernel adds them).  Other workgroups' loads cover a row's waits
+// (the next row's loads in registers of their own cost more occupancy than they hid:
+// 4096 rows of 4096 columns 91 us against 81).  The statistics come from the forward pass, so a row
+// needs one or two sums over the workgroup (three with a gate per row).
+template <class T, class R, int THREADS>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormGradArgs a)
 {
-    __shared__ float slots[3][THREADS / 64];
-    constexpr int kHeld = WIDE ? 1 : ITEMS;
-    const int n = a.n;
-    const float inv_n = 1.f / (float)n;
-    const bool pre = a.pre_weight != nullptr, post = a.post_weight != nullptr;
-    const bool channel = a.gate_kind == GEMM_RS_GATE_CHANNEL, full = a.gate_kind == GEMM_RS_GATE_FULL;
-    const bool token = a.gate_kind == GEMM_RS_GATE_TOKEN;
-    const bool need_y = post || a.gate_kind != GEMM_RS_GATE_NONE;
-    const T* const gate = static_cast<const T*>(a.gate);
-    float* const part_pre = a.partial + (int64_t)blockIdx.x * a.sums * n;
-    float* const part_post = part_pre + (pre ? n : 0);
-    float* const part_gate = part_post + (post ? n : 0);
-    auto column = [](int i) { return (i * THREADS + (int)threadIdx.x) * 8; };
-    auto load_if = [&](bool on, auto* p, int i) {
-        auto v = vec8<std::remove_cv_t<std::remove_pointer_t<decltype(p)>>>{};
-        if (on) v = load8(p, column(i), n);
-        return v;
-    };
-
-    float sum_pre[kHeld][8] = {}, sum_post[kHeld][8] = {}, sum_gate[kHeld][8] = {};
-    vec8<T> wpre[kHeld], wpost[kHeld], wgate[kHeld];
-    if constexpr (!WIDE) {
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            wpre[i] = load_if(pre, static_cast<const T*>(a.pre_weight), i);
-            wpost[i] = load_if(post, static_cast<const T*>(a.post_weight), i);
-            wgate[i] = load_if(channel, gate, i);
-        }
-    }
-
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const T* const dzrow = static_cast<const T*>(a.dz) + row * a.dz_stride;
-        const T* const yrow = static_cast<const T*>(a.y) + row * a.y_stride;
-        const R* const hrow = static_cast<const R*>(a.h) + row * a.h_stride;
-        const R* const dhrow = static_cast<const R*>(a.dh) + row * a.dh_stride;
-        const T* const gaterow = gate + (full ? row * a.gate_stride : 0);
-        vec8<T> dz[kHeld], y[kHeld], gf[kHeld];
-        vec8<R> dh[kHeld], hv[kHeld];
-        if constexpr (!WIDE) {
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-                dz[i] = load_if(pre, dzrow, i);
-                hv[i] = load_if(pre, hrow, i);
-                dh[i] = load_if(a.dh != nullptr, dhrow, i);
-                y[i] = load_if(need_y, yrow, i);
-                gf[i] = load_if(full, gaterow, i);
-            }
-        }
-        const float ry = post ? a.rstd[row] : 1.f;
-        const float rh = pre ? a.rstd[a.rows + row] : 0.f;
-        const float g_row = token ? (float)gate[row] : 1.f;
-
-        // through the next block's norm
-        float mean_h = 0.f;
-        if (pre) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-                if constexpr (WIDE) {
-                    one_chunk_at_a_time();
-                    dz[0] = load_if(true, dzrow, i);
-                    hv[0] = load_if(true, hrow, i);
-                    wpre[0] = load_if(true, static_cast<const T*>(a.pre_weight), i);
-                }
-                const int k = WIDE ? 0 : i;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s += (float)wpre[k][j] * (float)dz[k][j] * ((float)hv[k][j] * rh);
-            }
-            mean_h = block_sum<THREADS>(s, slots[0]) * inv_n;
-        }
-        float d[ITEMS][8];  // the gradient of h, then of u
-        float s_tok = 0.f, s_y = 0.f;
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int col = column(i), k = WIDE ? 0 : i;
-            if constexpr (WIDE) {
-                one_chunk_at_a_time();
-                dz[0] = load_if(pre, dzrow, i);
-                hv[0] = load_if(pre, hrow, i);
-                dh[0] = load_if(a.dh != nullptr, dhrow, i);
-                y[0] = load_if(need_y, yrow, i);
-                gf[0] = load_if(full, gaterow, i);
-                wpre[0] = load_if(pre, static_cast<const T*>(a.pre_weight), i);
-                wpost[0] = load_if(post, static_cast<const T*>(a.post_weight), i);
-                wgate[0] = load_if(channel, gate, i);
-                if (row != blockIdx.x) {
-                    widen<float>(load_if(pre, part_pre, i), sum_pre[0]);
-                    widen<float>(load_if(post, part_post, i), sum_post[0]);
-                    widen<float>(load_if(channel, part_gate, i), sum_gate[0]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum_pre[0][j] = sum_post[0][j] = sum_gate[0][j] = 0.f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float g = (float)dh[k][j];
-                if (pre) {
-                    const float hh = (float)hv[k][j] * rh, z = (float)dz[k][j];
-                    g += rh * ((float)wpre[k][j] * z - hh * mean_h);
-                    sum_pre[k][j] += z * hh;
-                }
-                d[i][j] = g;
-            }
-            if (a.dresidual) {
-                float o[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = a.residual_scale * d[i][j];
-                store8(static_cast<R*>(a.dresidual) + row * a.dresidual_stride, col, n, o);
-            }
-            float dg[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float yy = (float)y[k][j] * ry;
-                const float u = post ? yy * (float)wpost[k][j] : yy;
-                float g = a.block_scale * d[i][j];
-                dg[j] = g * u;
-                s_tok += dg[j];
-                if (channel) {
-                    sum_gate[k][j] += dg[j];
-                    g *= (float)wgate[k][j];
-                }
-                if (full) g *= (float)gf[k][j];
-                if (token) g *= g_row;
-                if (post) {
-                    sum_post[k][j] += g * yy;
-                    g *= (float)wpost[k][j];
-                    s_y += g * yy;
-                }
-                d[i][j] = g;
-            }
-            if (full) store8(static_cast<T*>(a.dgate) + row * a.dgate_stride, col, n, dg);
-            if constexpr (WIDE) {
-                if (pre) store8(part_pre, col, n, sum_pre[0]);
-                if (post) store8(part_post, col, n, sum_post[0]);
-                if (channel) store8(part_gate, col, n, sum_gate[0]);
-            }
-        }
-        if (token) {
-            const float t = block_sum<THREADS>(s_tok, slots[1]);
+    __shared__ float slots[2][3][THREADS / 64];
+    const float inv_n = 1.f / (float)a.n;
+    const int col = (int)threadIdx.x * 8;
+    NormGradColumns<T> c;
+    c.load(a, col);
+    c.clear();
+    // `half` alternates, so that a row's sums do not overwrite those of the row before while they are read
+    auto compute = [&](const NormGradRow<T, R>& r, int64_t row, int half) {
+        const NormGradMath<T, R> m(a, row);
+        float mean_h = 0.f, mean_y = 0.f, dot_y = 0.f, dot_gate = 0.f, d[8];
+        if (a.pre_weight) mean_h = block_sum<THREADS>(m.dot_h(r, c), slots[half][0]) * inv_n;
+        m.middle(r, c, mean_h, row, col, d, dot_y, dot_gate);
+        if (a.gate_kind == GEMM_RS_GATE_TOKEN) {
+            const float t = block_sum<THREADS>(dot_gate, slots[half][1]);
             if (threadIdx.x == 0) static_cast<T*>(a.dgate)[row] = (T)t;
         }
-        // through the block's own norm
-        float mean_y = 0.f;
-        if (post) mean_y = block_sum<THREADS>(s_y, slots[2]) * inv_n;
+        if (a.post_weight) mean_y = block_sum<THREADS>(dot_y, slots[half][2]) * inv_n;
+        m.last(r.y, mean_y, row, col, d);
+    };
+    int half = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, half ^= 1) {
+        NormGradRow<T, R> r;
+        r.load(a, row, col);
+        compute(r, row, half);
+    }
+    c.keep(a, a.partial + (int64_t)blockIdx.x * a.sums * a.n, col);
+}
+
+// Rows wider than 8 x 1024: ITEMS chunks of eight columns per thread.  The inputs are read
+// again where they are needed again, from cache, and the sums over rows are kept in the
+// workgroup's partial row.
+template <class T, class R, int ITEMS>
+__global__ __launch_bounds__(1024) void norm_backward_wide_kernel(const NormGradArgs a)
+{
+    __shared__ float slots[3][1024 / 64];
+    const float inv_n = 1.f / (float)a.n;
+    float* const part = a.partial + (int64_t)blockIdx.x * a.sums * a.n;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const NormGradMath<T, R> m(a, row);
+        float mean_h = 0.f, mean_y = 0.f, dot_h = 0.f, dot_y = 0.f, dot_gate = 0.f, d[ITEMS][8];
+        if (a.pre_weight) {
+#pragma unroll 1
+            for (int col = (int)threadIdx.x * 8; col < a.n; col += 8192) {
+                NormGradRow<T, R> r;
+                NormGradColumns<T> c;
+                r.load(a, row, col);
+                c.load(a, col);
+                dot_h += m.dot_h(r, c);
+            }
+            mean_h = block_sum<1024>(dot_h, slots[0]) * inv_n;
+        }
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const int k = WIDE ? 0 : i;
-            if (post) {
-                if constexpr (WIDE) {
-                    one_chunk_at_a_time();
-                    y[0] = load_if(true, yrow, i);
-                }
+            const int col = (i * 1024 + (int)threadIdx.x) * 8;
+            NormGradRow<T, R> r;
+            NormGradColumns<T> c;
+            r.load(a, row, col);
+            c.load(a, col);
+            if (row == blockIdx.x) c.clear();
+            else c.fetch(a, part, col);
+            m.middle(r, c, mean_h, row, col, d[i], dot_y, dot_gate);
+            c.keep(a, part, col);
+        }
+        if (a.gate_kind == GEMM_RS_GATE_TOKEN) {
+            const float t = block_sum<1024>(dot_gate, slots[1]);
+            if (threadIdx.x == 0) static_cast<T*>(a.dgate)[row] = (T)t;
+        }
+        if (a.post_weight) mean_y = block_sum<1024>(dot_y, slots[2]) * inv_n;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[i][j] = ry * (d[i][j] - (float)y[k][j] * ry * mean_y);
-            }
-            store8(static_cast<T*>(a.dy) + row * a.dy_stride, column(i), n, d[i]);
+        for (int i = 0; i < ITEMS; ++i) {
+            const int col = (i * 1024 + (int)threadIdx.x) * 8;
+            vec8<T> y = {};
+            if (a.post_weight) y = load8(static_cast<const T*>(a.y) + row * a.y_stride, col, a.n);
+            m.last(y, mean_y, row, col, d[i]);
         }
         __syncthreads();  // the slots are free for the next row
     }
-
-    if constexpr (!WIDE) {
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            if (pre) store8(part_pre, column(i), n, sum_pre[i]);
-            if (post) store8(part_post, column(i), n, sum_post[i]);
-            if (channel) store8(part_gate, column(i), n, sum_gate[i]);
-        }
-    }
 }
 
-// Adds the workgroups' partial sums, in workgroup order within each of eight
+// Adds the workgroups' partial sums, in workgroup order within each of sixteen
 // strided sets and then over the sets.  blockIdx.y is the sum, out[] its target.
 struct NormSumsArgs {
     const float* partial;
@@ -341,17 +372,32 @@ struct NormSumsArgs {
     int n, sums, groups;
 };
 
-constexpr int kSumCols = 32, kSumSets = 8;
+constexpr int kSumCols = 32, kSumSets = 16;  // columns of a workgroup; sets of groups
 
 __global__ __launch_bounds__(kSumCols * kSumSets) void norm_sums_kernel(const NormSumsArgs a)
 {
     __shared__ float part[kSumSets][kSumCols];
     const int c = threadIdx.x % kSumCols, set = threadIdx.x / kSumCols;
     const int col = blockIdx.x * kSumCols + c;
+    const int64_t step = (int64_t)a.sums * a.n;
     float s = 0.f;
-    if (col < a.n)
-        for (int g = set; g < a.groups; g += kSumSets)
-            s += a.partial[((int64_t)g * a.sums + blockIdx.y) * a.n + col];
+    if (col < a.n) {
+        const float* p = a.partial + set * step + (int64_t)blockIdx.y * a.n + col;
+        int g = set;
+        // eight loads in flight, added in order
+        for (; g + 7 * kSumSets < a.groups; g += 8 * kSumSets) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = p[k * kSumSets * step];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+            p += 8 * kSumSets * step;
+        }
+        for (; g < a.groups; g += kSumSets) {
+            s += *p;
+            p += kSumSets * step;
+        }
+    }
     part[set][c] = s;
     __syncthreads();
     if (set == 0 && col < a.n) {

@@ -305,16 +305,19 @@ def _weight(t, name, N, dtype, dev):
 
 
 def _parts(parts, dev):
-    """(first, pointers, row stride) of a [S][N] tensor, a list of them or a [P][S][N] tensor."""
+    """(a tensor of them, S, N, pointers, row stride) of a [S][N] tensor, a list of them or a [P][S][N] tensor."""
     if isinstance(parts, torch.Tensor):
         if parts.dim() == 2:
-            return parts, (parts.data_ptr(),), _rows(parts, "parts", *parts.shape, parts.dtype, dev)
+            S, N = parts.shape
+            return parts, S, N, (parts.data_ptr(),), _rows(parts, "parts", S, N, parts.dtype, dev)
         if parts.dim() != 3 or not 1 <= parts.shape[0] <= NORM_MAX_PARTS:
             raise ValueError(f"parts: [S][N], or 1 to {NORM_MAX_PARTS} of them, got shape {tuple(parts.shape)}")
-        first = parts[0]
-        step, base = parts.stride(0) * parts.element_size(), parts.data_ptr()
-        stride = _rows(first, "parts[0]", *first.shape, first.dtype, dev)
-        return first, [base + i * step for i in range(parts.shape[0])], stride
+        P, S, N = parts.shape
+        s0, s1, s2 = parts.stride()
+        if s2 != 1 and N != 1 or s1 < N and S > 1:
+            raise ValueError(f"parts: rows must hold their elements side by side, strides are {(s0, s1, s2)}")
+        step, base = s0 * parts.element_size(), parts.data_ptr()
+        return parts, S, N, range(base, base + P * step, step) if step > 0 else [base] * P, s1 if S > 1 else max(s1, N)
     if not 1 <= len(parts) <= NORM_MAX_PARTS:
         raise ValueError(f"parts: 1 to {NORM_MAX_PARTS}, got {len(parts)}")
     first = parts[0]
@@ -322,7 +325,7 @@ def _parts(parts, dev):
     strides = [_rows(p, f"parts[{i}]", S, N, first.dtype, dev) for i, p in enumerate(parts)]
     if strides != strides[:1] * len(parts):
         raise ValueError(f"parts: row strides differ: {strides}")
-    return first, [p.data_ptr() for p in parts], strides[0]
+    return first, S, N, [p.data_ptr() for p in parts], strides[0]
 
 
 _NO_PARTS = tuple((0,) * (NORM_MAX_PARTS - n) for n in range(NORM_MAX_PARTS + 1))
@@ -344,8 +347,7 @@ def block_norm(parts, residual=None, *, pre_weight=None, post_weight=None, gate=
     if not isinstance(parts, torch.Tensor) and not parts:
         raise ValueError(f"parts: 1 to {NORM_MAX_PARTS}, got none")
     dev = _device(parts if isinstance(parts, torch.Tensor) else parts[0], "parts")
-    first, pointers, part_stride = _parts(parts, dev)
-    S, N = first.shape
+    first, S, N, pointers, part_stride = _parts(parts, dev)
     dtype = first.dtype
     code = _CODES.get(dtype)
     if code is None:
