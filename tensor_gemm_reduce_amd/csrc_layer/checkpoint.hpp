@@ -281,9 +281,9 @@ __global__ __launch_bounds__(kWgThreads) void wgrad_any_kernel(const WgradArgs a
 //     then holds, for every column, 64 tokens in eight 16-byte chunks, and both sides
 //     use 16-byte accesses.  (Staging token-major and reading with the transposing
 //     LDS loads moves the same bytes in twice the reads, 8 bytes each.)
-//   - Chunk c of column r lies at chunk c ^ ((r ^ r / 8) & 7): eight (sixteen)
-//     consecutive columns, as a fragment read takes them, and eight columns 8 apart,
-//     as the threads write them, lie in different banks.
+//   - Chunk c of column r lies at chunk c ^ (r ^ r / 8 & 3) & 7: eight (sixteen)
+//     consecutive columns, as a fragment read takes them, lie in different banks, and
+//     the blocks of 32 columns alike, so that a lane needs one address per 16 tokens.
 //   - A workgroup's work is a list of tiles, then a share of the tiles that do not
 //     fill the device a last time: those are cut along the tokens into equal shares
 //     (wgrad_join_kernel adds the pieces in token order).
@@ -316,7 +316,7 @@ constexpr int kWgRows = 64;   // tokens per step
 constexpr int kWgCol = 128;   // LDS bytes of a column's tokens
 
 // LDS offset of chunk c (8 tokens) of column r
-__device__ __forceinline__ int wgrad_at(int r, int c) { return (r ^ ((r >> 6) & 1)) * kWgCol + ((c ^ r ^ (r >> 3)) & 7) * 16; }
+__device__ __forceinline__ int wgrad_at(int r, int c) { return r * kWgCol + ((c ^ r ^ ((r >> 3) & 3)) & 7) * 16; }
 
 // A thread's share of a step: 8 tokens x 8 columns of dy and of the checkpoint.
 struct WgradRegs {
@@ -406,10 +406,8 @@ struct WgradTile {
 };
 
 // LDS offsets of a thread in each of the two stages: its first column of eight as a
-// loader (column j's chunk lies at offset ^ j (kWgCol + 16)), and its column of the
-// wave's first fragment, first chunk, as a reader: 16 tokens on, one block on or two
-// change that by an exclusive or of 32, 64 and kWgCol.  Kept to these few registers:
-// hide() takes their constancy from the compiler, or every sum would get a register.
+// loader (column j's chunk lies at offset ^ 16 j, j columns on), and its column of the
+// wave's first fragment as a reader, for each 16 tokens.
 template <class T, int WN, int WK>
 struct WgradPlaces {
     typedef WgradTile<WN, WK> Tile;
@@ -418,7 +416,7 @@ struct WgradPlaces {
     static constexpr int kPer = Tile::kBN / 8;     // threads side by side
 
     char* const lds;
-    uint32_t put[2], get_y[2], get_x[2];
+    uint32_t put[2], get_y[2][4], get_x[2][4];
 
     __device__ __forceinline__ explicit WgradPlaces(char* l) : lds(l)
     {
@@ -427,26 +425,28 @@ struct WgradPlaces {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             put[p] = p * Tile::kStage + wgrad_at(8 * cg, tg);
-            get_y[p] = p * Tile::kStage + wgrad_at((wave >> 1) * 32 * WN + (lane & 31), lane >> 5);
-            get_x[p] = p * Tile::kStage + wgrad_at((wave & 1) * 32 * WK + (lane & 31), lane >> 5);
+#pragma unroll
+            for (int sub = 0; sub < 4; ++sub) {
+                get_y[p][sub] = p * Tile::kStage + wgrad_at((wave >> 1) * 32 * WN + (lane & 31), 2 * sub + (lane >> 5));
+                get_x[p][sub] = p * Tile::kStage + wgrad_at((wave & 1) * 32 * WK + (lane & 31), 2 * sub + (lane >> 5));
+            }
         }
     }
+    // Takes the constancy of these from the compiler, which would give every sum with them a register of its own.
     __device__ __forceinline__ void hide(WgradLoader<T>& ld)
     {
-        __asm__ __volatile__("" : "+v"(put[0]), "+v"(put[1]), "+v"(get_y[0]), "+v"(get_y[1]), "+v"(get_x[0]),
-                             "+v"(get_x[1]), "+v"(ld.yoff), "+v"(ld.xoff), "+v"(ld.eoff));
+        __asm__ __volatile__("" : "+v"(put[0]), "+v"(put[1]), "+v"(ld.yoff), "+v"(ld.xoff), "+v"(ld.eoff));
     }
     template <int P>
     __device__ __forceinline__ void write(int j, bool x, const u32x4& v) const
     {
-        *reinterpret_cast<u32x4*>(lds + (put[P] ^ (uint32_t)(j * (kWgCol + 16))) + (x ? kX : 0)) = v;
+        *reinterpret_cast<u32x4*>(lds + (put[P] ^ (uint32_t)(16 * j)) + j * kWgCol + (x ? kX : 0)) = v;
     }
     // the fragment of block b and 16 tokens `sub` of dy or the checkpoint
     template <int P>
     __device__ __forceinline__ frag read(int sub, int b, bool x) const
     {
-        const uint32_t flip = 32u * sub ^ 64u * (b & 1) ^ (uint32_t)kWgCol * (b >> 1);
-        return *reinterpret_cast<const frag*>(lds + ((x ? get_x[P] : get_y[P]) ^ flip) + b * 32 * kWgCol + (x ? kX : 0));
+        return *reinterpret_cast<const frag*>(lds + (x ? get_x[P][sub] : get_y[P][sub]) + b * 32 * kWgCol + (x ? kX : 0));
     }
     static __device__ __forceinline__ void barrier()
     {
