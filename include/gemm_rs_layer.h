@@ -26,6 +26,9 @@
  *   - Row strides are in elements, at least the row's width.  Buffers may be
  *     larger than 4 GiB: offsets are 64-bit.
  *   - Outputs must not overlap inputs unless stated.
+ *   - Sizes past the limits given give GEMM_RS_ERR_UNSUPPORTED_SHAPE: N and K up
+ *     to 2^22 each (4-bit weights: N K up to 2^37), M of the 4-bit product up to
+ *     2^20, rows of a norm up to 2^22 - 1, M K of a checkpoint up to 2^36.
  *   - A call with no rows returns GEMM_RS_OK and enqueues nothing, except where
  *     a sum over rows is an output: that is then zero.
  */
@@ -192,7 +195,7 @@ int gemm_rs_ckpt_unpack(int32_t dtype, int64_t M, int64_t K, const void *q, cons
  * fixed order, one rounding to out_dtype (F32 or dy's).
  *   add   [N][K] FP32 or NULL; may be dw when out_dtype is F32 and the strides
  *         agree (gradient accumulation in place).
- * N and K: 1 .. 2^24; M may be 0 (dw = add, or zero). */
+ * M may be 0 (dw = add, or zero). */
 typedef struct gemm_rs_wgrad_args {
     int32_t dtype, out_dtype;
     int64_t M, N, K;

@@ -94,7 +94,7 @@ int gemm_rs_block_norm(const gemm_rs_norm_config* c, int64_t rows, const gemm_rs
     int rc = gemm_rs_norm_validate(c);
     if (rc != GEMM_RS_OK) return rc;
     if (!g || rows < 0) return GEMM_RS_ERR_INVALID_ARG;
-    if (rows >= kMaxRows) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (rows > kMaxThreads / 1024) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     if (rows == 0) return GEMM_RS_OK;
     const size_t eb = elem_bytes(c->dtype), rb = elem_bytes(c->residual_dtype);
     Checker k;
@@ -158,7 +158,7 @@ int gemm_rs_block_norm_backward(const gemm_rs_norm_config* c, int64_t rows, cons
     int rc = gemm_rs_norm_validate(c);
     if (rc != GEMM_RS_OK) return rc;
     if (!g || rows < 0) return GEMM_RS_ERR_INVALID_ARG;
-    if (rows >= kMaxRows) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (rows > kMaxThreads / 1024) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     const size_t eb = elem_bytes(c->dtype), rb = elem_bytes(c->residual_dtype);
     const bool channel = c->gate == GEMM_RS_GATE_CHANNEL;
     Checker k;

@@ -56,12 +56,16 @@ int launch2(void (*kernel)(A, B), dim3 grid, int lds, const A& a, const B& b, vo
 }
 
 template <class T, int WN, int WK>
-int wgrad_run(const WgradArgs& a, const WgradPlan& p, void* stream)
+int wgrad_run(const WgradArgs& a, const WgradPlan& p, int device, void* stream)
 {
     constexpr int kLds = WgradTile<WN, WK>::kLds;
-    static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(wgrad_kernel<T, WN, WK>),
-                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-    if (allowed != hipSuccess) return hip_fail(allowed, "hipFuncSetAttribute");
+    static std::atomic<bool> allowed[kMaxDevices];  // the LDS of one workgroup, once per device
+    if (!allowed[device].load(std::memory_order_relaxed)) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(wgrad_kernel<T, WN, WK>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+        if (e != hipSuccess) return hip_fail(e, "hipFuncSetAttribute");
+        allowed[device].store(true, std::memory_order_relaxed);
+    }
     int rc = launch2(wgrad_kernel<T, WN, WK>, dim3((unsigned)p.grid), kLds, a, p, stream);
     if (rc != GEMM_RS_OK || p.shares == 0) return rc;
     const int64_t rest = (int64_t)p.tiles_n * p.tiles_k - p.full;
@@ -90,7 +94,7 @@ static int ckpt_check(int32_t dtype, int64_t M, int64_t K, const void* x, int64_
                       const void* exps)
 {
     if (dtype < GEMM_RS_DTYPE_BF16 || dtype > GEMM_RS_DTYPE_F32 || M < 0 || K < 1) return GEMM_RS_ERR_INVALID_ARG;
-    if (M >= kMaxRows || K > (1 << 24) || ceil_div(M * (ceil_div(K, 32) * 2), kCkptThreads) > 0x7FFFFFFF)
+    if (M >= kMaxRows || K > (1 << 22) || M * (ceil_div(K, 32) * 2) > kMaxThreads - kCkptThreads)
         return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return GEMM_RS_OK;
     Checker k;
@@ -184,7 +188,8 @@ int gemm_rs_ckpt_wgrad(const gemm_rs_wgrad_args* g, void* workspace, size_t work
         else k.need(workspace, 16);
     }
     if (k.code != GEMM_RS_OK) return k.code;
-    if ((rc = check_device()) != GEMM_RS_OK) return rc;
+    int device = 0;
+    if ((rc = check_device(&device)) != GEMM_RS_OK) return rc;
     WgradArgs a = {};
     a.dy = g->dy;
     a.q = static_cast<const int8_t*>(g->q);
@@ -208,8 +213,8 @@ int gemm_rs_ckpt_wgrad(const gemm_rs_wgrad_args* g, void* workspace, size_t work
     int big;
     WgradPlan p = wgrad_plan(*g, big);
     p.pieces = static_cast<float*>(workspace);
-    if (bf16) return big ? wgrad_run<__bf16, 4, 4>(a, p, stream) : wgrad_run<__bf16, 2, 2>(a, p, stream);
-    return big ? wgrad_run<_Float16, 4, 4>(a, p, stream) : wgrad_run<_Float16, 2, 2>(a, p, stream);
+    if (bf16) return big ? wgrad_run<__bf16, 4, 4>(a, p, device, stream) : wgrad_run<__bf16, 2, 2>(a, p, device, stream);
+    return big ? wgrad_run<_Float16, 4, 4>(a, p, device, stream) : wgrad_run<_Float16, 2, 2>(a, p, device, stream);
 }
 
 }  // extern "C"

@@ -23,21 +23,25 @@ inline int hip_fail(hipError_t e, const char* what)
     return GEMM_RS_ERR_HIP;
 }
 
+constexpr int kMaxDevices = 64;
+
 // The current device is a gfx950: looked up once per device.
-inline int check_device()
+inline int check_device(int* device = nullptr)
 {
-    static std::atomic<int> known[64];  // 0: not looked up, 1: gfx950, 2: another
+    static std::atomic<int> known[kMaxDevices];  // 0: not looked up, 1: gfx950, 2: another
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e == hipErrorNoDevice || e == hipErrorInvalidDevice) return GEMM_RS_ERR_NO_DEVICE;
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-    int k = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (dev < 0 || dev >= kMaxDevices) return GEMM_RS_ERR_NO_DEVICE;
+    if (device) *device = dev;
+    int k = known[dev].load(std::memory_order_relaxed);
     if (k == 0) {
         hipDeviceProp_t p;
         e = hipGetDeviceProperties(&p, dev);
         if (e != hipSuccess) return hip_fail(e, "hipGetDeviceProperties");
         k = strncmp(p.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-        if (dev >= 0 && dev < 64) known[dev].store(k, std::memory_order_relaxed);
+        known[dev].store(k, std::memory_order_relaxed);
     }
     return k == 1 ? GEMM_RS_OK : GEMM_RS_ERR_NO_DEVICE;
 }
@@ -78,6 +82,8 @@ struct Checker {
 };
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;
+// A launch has fewer than 2^32 threads in its first dimension.
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
 constexpr int kCus = 256;  // compute units of an MI355X
 
 }  // namespace gemm_rs_layer

@@ -85,9 +85,9 @@ int gemm_rs_w4_validate(const gemm_rs_w4_config* c)
     if (!c || c->N < 0 || c->K < 0 || c->group <= 0 || (c->zero_points != 0 && c->zero_points != 1) ||
         (c->dtype != GEMM_RS_DTYPE_BF16 && c->dtype != GEMM_RS_DTYPE_F16))
         return GEMM_RS_ERR_INVALID_ARG;
-    // tiles are counted in 32 bits by the launch grid, inputs by the kernels
-    if (c->K < 2 || c->K % 2 != 0 || c->K > (1 << 24) || c->N < 1 || c->N > (1 << 24) ||
-        ceil_div(c->N, kW4Tile) * ceil_div(c->K, kW4Block) > 0x7FFFFFFF)
+    // packing takes a wave per tile and block
+    if (c->K < 2 || c->K % 2 != 0 || c->K > (1 << 22) || c->N < 1 || c->N > (1 << 22) ||
+        ceil_div(c->N, kW4Tile) * ceil_div(c->K, kW4Block) * 64 > kMaxThreads)
         return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     if (c->group % 32 != 0 && c->group != c->K) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     return GEMM_RS_OK;

@@ -565,6 +565,49 @@ def test_offsets_past_32_bits():
     assert torch.equal(layer.w4_linear(x, weight, put(torch.zeros_like(want))), want)
 
 
+@pytest.mark.parametrize("S,N", [(9, 520), (5, 9000), (3, 20000)])
+def test_block_norm_backward_in_place(S, N):
+    """The C call may write the residual's gradient over dh and y's over dz."""
+    import ctypes
+    c = grad_case(S, N, BF16, BF16, True, "none", seed=21)
+    want = run_grad(c)
+    dz, dh = c["dz"].clone(), c["dh"].clone()
+    sums = torch.empty((2, N), device="cuda")
+    cfg = layer.gemm_rs_norm_config(N, layer.DTYPE_BF16, layer.DTYPE_BF16, 1, layer.GATE_NONE, 1, 1, 1e-5, 0.7, -0.9)
+    a = layer.gemm_rs_norm_grad_args(
+        dz.data_ptr(), N, dh.data_ptr(), N, c["h"].data_ptr(), N, c["y"].data_ptr(), N, c["rstd"].data_ptr(),
+        c["post"].data_ptr(), None, c["pre"].data_ptr(), 0, dh.data_ptr(), N, dz.data_ptr(), N, sums[0].data_ptr(),
+        sums[1].data_ptr(), None, 0)
+    L = layer.lib()
+    size = L.gemm_rs_block_norm_workspace(ctypes.byref(cfg), S)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    call = lambda n: L.gemm_rs_block_norm_backward(ctypes.byref(cfg), S, ctypes.byref(a), ws.data_ptr(), n,  # noqa: E731
+                                                   torch.cuda.current_stream().cuda_stream)
+    assert call(size - 1) == -8  # the workspace's size is checked
+    assert call(size) == 0
+    assert torch.equal(dz, want.y) and torch.equal(dh, want.residual)
+    assert torch.equal(sums[0], want.pre_weight) and torch.equal(sums[1], want.post_weight)
+
+
+@pytest.mark.parametrize("name,tokens", [("tiny", 1), ("tiny", 16), ("o_proj", 5)])
+def test_example_runs_them_together(name, tokens):
+    """The example's training step and decode: the operators on the layer's own buffers.  BF16 roundings (2^-9 rms) of
+    h's or z's terms; 8-bit inputs: half a step of at most 2^-6 of a block's largest of 32 normal values; 4-bit
+    weights: half of a fifteenth of a group's range, uniform."""
+    import os
+    import sys
+
+    import synthetic
+    from conftest import ROOT
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import layer_block
+
+    found = layer_block.run(synthetic.CONFIGS[name], tokens, verbose=False)
+    for k, limit in {"h": 4e-3, "z": 8e-3, "weight gradient (8-bit input)": 2e-2, "4-bit partial": 0.15, "decode h": 4e-3,
+                     "decode z": 8e-3}.items():
+        assert found[k] <= limit, (k, found[k])
+
+
 def test_refusals():
     x, q, s, z = w4_case(4, 64, 128, 64, BF16, True, seed=1)
     weight = layer.w4_pack(q, s, z, group=64)
