@@ -15,7 +15,10 @@ bool wgrad_fast(const gemm_rs_wgrad_args& g)
     return g.M > 0 && aligned(g.dy, 4) && g.dy_stride % 2 == 0 && g.N % 2 == 0 && g.dy_stride < (1 << 23);
 }
 
-constexpr int kWgMinSteps = 4;    // a share is at least this many steps of 64 tokens
+// A share of a cut tile is at least this many steps of 64 tokens: shorter ones cost more
+// in starts and in joining than they spread (us with 4 / 8 / 16 / 32: 512 x 4096 x 1024
+// 28 / 14 / 14 / 14, 16384 x 256 x 128 49 / 33 / 30 / 37, 4096 x 512 x 512 27 / 23 / 24 / 34).
+constexpr int kWgMinSteps = 12;
 
 // The 256 x 256 tile reads and turns its operands half as often for the same outputs, but
 // starts and ends slower.  Measured, us (256 / 128): 2048 x 8192 x 3584 214 / 208 (32
