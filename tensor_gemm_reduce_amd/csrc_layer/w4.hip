@@ -55,25 +55,50 @@ int w4_tile_launch(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
 {
     const dim3 grid((unsigned)ceil_div(a.M, kW4Rows), (unsigned)ceil_div(a.l.tiles, 4 * NT));
     return w4_forms(a.l, c.zero_points, [&](auto subs, auto zeros) {
-        return launch(w4_tile_kernel<T, NT, decltype(subs)::value, decltype(zeros)::value>, grid, 256, a, stream,
+        return launch(w4_tile_kernel<T, NT, decltype(subs)::value, decltype(zeros)::value>, grid, 512, a, stream,
                       "gemm_rs_w4_linear");
     });
 }
 
-// Few rows: the kernel whose waves split K; 4, 16, 32 rows or 64 at a time.  Many: the
-// kernel whose workgroups keep 64 rows in LDS, once there is one for every second
-// CU (fewer leave too much of the chip idle, since each runs all of K).  Measured, us
-// (few / many): 7168 x 8192 at 128 rows (112 workgroups) 60 / 77, at 200 (224) 105 / 77;
-// 1280 x 8192 at 300 rows (50) 31 / 78, at 1000 (160) 90 / 75.
+// Up to 32 rows: the kernel whose waves split K, with one tile of columns and more waves
+// per workgroup where the tiles are no more than the CUs, else two tiles.  Measured, us
+// (one / two): 3584 x 4096 at 1 row 4.5 / 4.8 (8 waves, one tile too), at 9 rows 5.5 / 7.0,
+// at 24 7.1 / 8.5; 7168 x 8192 at 9 rows 15.4 / 11.5, at 24 20 / 14.4.
+//
+// More rows: whichever of six kernels costs least, as rounds of workgroups over the CUs
+// times a round's cost.  A round takes a time that grows with the columns per workgroup,
+// though not from zero (all run the whole of K).  Measured at K = 8192, us for groups of
+// 128 and of 32: the kernel above with 64 rows and 16 columns 19, 20; with 32 columns 29,
+// 37; the kernel whose workgroups keep 64 rows in LDS with 64 columns 36, 40; 128: 44, 52;
+// 192: 55, 68; 256: 66, 84.
 template <class T>
 int w4_run(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
 {
-    if (a.M <= 4) return w4_launch<T, 8, 1, 1, true, 4, 4>(c, a, stream);
-    if (a.M <= 16) return w4_launch<T, 8, 2, 1, false, 4, 4>(c, a, stream);
-    if (a.M <= 32) return w4_launch<T, 8, 2, 2, false, 2, 1>(c, a, stream);
-    const int64_t many = ceil_div(a.M, kW4Rows) * ceil_div(a.l.tiles, 4 * 2);
-    if (a.M <= 64 || many < kCus / 2) return w4_launch<T, 4, 2, 4, false, 2, 1>(c, a, stream);
-    return w4_tile_launch<T, 2>(c, a, stream);
+    const bool narrow = a.l.tiles <= kCus;
+    if (a.M <= 4)
+        return narrow ? w4_launch<T, 16, 1, 1, true, 2, 2>(c, a, stream) : w4_launch<T, 8, 1, 1, true, 4, 4>(c, a, stream);
+    if (a.M <= 16)
+        return narrow ? w4_launch<T, 16, 1, 1, false, 2, 2>(c, a, stream) : w4_launch<T, 8, 2, 1, false, 4, 4>(c, a, stream);
+    if (a.M <= 32)
+        return narrow ? w4_launch<T, 8, 1, 2, false, 2, 1>(c, a, stream) : w4_launch<T, 8, 2, 2, false, 2, 1>(c, a, stream);
+    constexpr int kTiles[6] = {1, 2, 4, 8, 12, 16}, kCost[6] = {3, 5, 6, 8, 10, 12};
+    int best = 0;
+    int64_t cost = INT64_MAX;
+    for (int i = 0; i < 6; ++i) {
+        const int64_t rounds = ceil_div(ceil_div(a.M, kW4Rows) * ceil_div(a.l.tiles, kTiles[i]), kCus);
+        if (rounds * kCost[i] < cost) {
+            cost = rounds * kCost[i];
+            best = i;
+        }
+    }
+    switch (best) {
+    case 0: return w4_launch<T, 8, 1, 4, false, 2, 1>(c, a, stream);
+    case 1: return w4_launch<T, 4, 2, 4, false, 2, 1>(c, a, stream);
+    case 2: return w4_tile_launch<T, 1>(c, a, stream);
+    case 3: return w4_tile_launch<T, 2>(c, a, stream);
+    case 4: return w4_tile_launch<T, 3>(c, a, stream);
+    default: return w4_tile_launch<T, 4>(c, a, stream);
+    }
 }
 
 }  // namespace
@@ -116,6 +141,7 @@ int gemm_rs_w4_pack(const gemm_rs_w4_config* c, const void* q, const void* scale
     a.scales = static_cast<const uint16_t*>(scales);
     a.zeros = static_cast<const uint8_t*>(zeros);
     a.packed = static_cast<char*>(packed);
+    a.bf16 = c->dtype == GEMM_RS_DTYPE_BF16;
     return launch(w4_pack_kernel, dim3((unsigned)((int64_t)a.l.tiles * a.l.blocks)), 64, a, stream, "gemm_rs_w4_pack");
 }
 

@@ -13,6 +13,8 @@
 //   - The group's accumulator times its scale is added to the result's (FP32).
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace gemm_rs_layer {
@@ -24,13 +26,16 @@ constexpr int kW4Block = 128;  // inputs per block of a tile: 64 lanes x 16 byte
 // zero points, each [tile][block][row of the tile][sub], with `subs` (1, 2 or 4)
 // scales per row and block.
 //   Word t (0..3) of lane l holds row l % 16, inputs 32 t + 8 (l / 16) + 0..7 of
-//   the block: nibble i < 4 is input 2 i, nibble 4 + i input 2 i + 1, so a shift
-//   and a mask give the pair (2 i, 2 i + 1) in the halves of a word.
+//   the block.  Turned right by w4_turn(type, i) bits it holds inputs 2 i and 2 i + 1
+//   at the top of the mantissas of its two halves, so a pair costs a turn (none for
+//   i = 0) and one and-or.
 struct W4Layout {
     int N, K, group;
     int tiles, blocks, groups, subs;  // groups: per row, as given
     int64_t scale_at, zero_at, bytes;
 };
+
+constexpr __device__ int w4_turn(bool bf16, int i) { return i < 2 ? 4 * i : i == 2 ? (bf16 ? 8 : 28) : bf16 ? 28 : 24; }
 
 struct W4PackArgs {
     W4Layout l;
@@ -38,6 +43,7 @@ struct W4PackArgs {
     const uint16_t* scales;
     const uint8_t* zeros;
     char* packed;
+    int bf16;
 };
 
 // One wave per (tile, block).  Weights past N or K are stored as zeros with a zero
@@ -57,7 +63,9 @@ __global__ __launch_bounds__(64) void w4_pack_kernel(const W4PackArgs a)
             uint32_t nib = 0;
             if (n < a.l.N && k + j < a.l.K)
                 nib = (a.q[(int64_t)n * (a.l.K / 2) + (k + j) / 2] >> (4 * ((k + j) & 1))) & 15u;
-            v |= nib << (4 * (j / 2 + 4 * (j & 1)));
+            const uint32_t at = nib << ((a.bf16 ? 3 : 6) + 16 * (j & 1));
+            const int turn = w4_turn(a.bf16, j / 2);
+            v |= at << turn | (turn ? at >> (32 - turn) : 0u);
         }
         w[t] = v;
     }
@@ -78,35 +86,44 @@ struct W4Type;
 template <>
 struct W4Type<__bf16> {
     typedef bf16x8 frag;
-    static constexpr uint32_t kMask = 0x00780078u, kMagic = 0x41804180u;  // 16.0 in both halves
-    static constexpr int kShift = 3;                                      // the nibble's place in the mantissa
+    static constexpr uint32_t kMask = 0x00780078u, kMagic = 0x41804180u;  // the nibbles' places; 16.0 in both halves
+    static constexpr bool kBf16 = true;
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float add2(uint32_t v, float c)  // both halves and c
+    {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v), __builtin_bit_cast(bf16x2, 0x3F803F80u), c, false);
     }
 };
 template <>
 struct W4Type<_Float16> {
     typedef f16x8 frag;
     static constexpr uint32_t kMask = 0x03C003C0u, kMagic = 0x4C004C00u;
-    static constexpr int kShift = 6;
+    static constexpr bool kBf16 = false;
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
+    static __device__ __forceinline__ float add2(uint32_t v, float c)
+    {
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, v), __builtin_bit_cast(f16x2, 0x3C003C00u), c, false);
+    }
 };
 
-// The eight weights of a word as 16 + q.
+// The eight weights of a word as 16 + q.  The constants sit in a scalar and a vector
+// register: and-or takes neither as a literal, and one scalar.
 template <class T>
 __device__ __forceinline__ typename W4Type<T>::frag w4_expand(uint32_t w)
 {
+    uint32_t mask = W4Type<T>::kMask, magic = W4Type<T>::kMagic;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(magic));
     u32x4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int sh = 4 * i - W4Type<T>::kShift;
-        const uint32_t b = sh >= 0 ? w >> (sh >= 0 ? sh : 0) : w << (sh < 0 ? -sh : 0);
-        v[i] = (b & W4Type<T>::kMask) | W4Type<T>::kMagic;
-    }
+    for (int i = 0; i < 4; ++i)
+        v[i] = ((i ? __builtin_amdgcn_alignbit(w, w, w4_turn(W4Type<T>::kBf16, i)) : w) & mask) | magic;
     return __builtin_bit_cast(typename W4Type<T>::frag, v);
 }
 
@@ -130,6 +147,13 @@ __device__ __forceinline__ i32x4 lanes_down(const i32x4& v)
     return r;
 }
 
+// What a sum of inputs is multiplied by: all of -(16 + 8) where every zero point is 8, else the sign.
+template <bool ZEROS>
+constexpr float w4_unit()
+{
+    return ZEROS ? -1.f : -24.f;
+}
+
 struct W4Args {
     W4Layout l;
     const char* packed;
@@ -142,8 +166,10 @@ struct W4Args {
 template <class T, int NT, int SUBS, bool ZEROS>
 struct W4Block {
     u32x4 w[NT];
-    T sc[NT][SUBS];
-    uint8_t z[NT][SUBS];
+    typedef T scales_t __attribute__((ext_vector_type(SUBS)));
+    typedef uint8_t zeros_t __attribute__((ext_vector_type(SUBS)));
+    scales_t sc[NT];
+    zeros_t z[NT];
 
     // tb: tile 0's index of the block; tiles are `blocks` apart.  Tiles past the last read it again.
     __device__ __forceinline__ void load(const W4Args& a, int tile0, int b)
@@ -155,51 +181,58 @@ struct W4Block {
             const int64_t tb = (int64_t)tile * a.l.blocks + b;
             w[t] = *reinterpret_cast<const u32x4*>(a.packed + (tb * 64 + lane) * 16);
             const int64_t at = tb * (kW4Tile * SUBS) + (lane & 15) * SUBS;
-            typedef T scales_t __attribute__((ext_vector_type(SUBS)));
-            typedef uint8_t zeros_t __attribute__((ext_vector_type(SUBS)));
-            const scales_t s = *reinterpret_cast<const scales_t*>(a.packed + a.l.scale_at + at * 2);
-            zeros_t zz;
-            if constexpr (ZEROS) zz = *reinterpret_cast<const zeros_t*>(a.packed + a.l.zero_at + at);
+            sc[t] = *reinterpret_cast<const scales_t*>(a.packed + a.l.scale_at + at * 2);
+            if constexpr (ZEROS) z[t] = *reinterpret_cast<const zeros_t*>(a.packed + a.l.zero_at + at);
+        }
+    }
+    // g[t][f] += step k (32 inputs) of the block's product with the rows x[f]; after a group's last step acc += its scale
+    // times g.  The part of the zero points, -(16 + z) times the sum of a row's inputs, is where g starts: start(u, f)
+    // gives that sum of sub-block u times w4_unit.
+    template <int MF, class F>
+    __device__ __forceinline__ void step(const typename W4Type<T>::frag (&x)[MF], int k, f32x4 (&g)[NT][MF],
+                                         f32x4 (&acc)[NT][MF], F start) const
+    {
+        constexpr int kSteps = 4 / SUBS;  // steps per scale
+        const int u = k / kSteps;
+        if (k % kSteps == 0)
 #pragma unroll
-            for (int u = 0; u < SUBS; ++u) {
-                sc[t][u] = s[u];
-                z[t][u] = ZEROS ? zz[u] : 8;
+            for (int f = 0; f < MF; ++f) {
+                const f32x4 s = start(u, f);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) g[t][f] = ZEROS ? s * (float)(16 + z[t][u]) : s;
+            }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const typename W4Type<T>::frag q = w4_expand<T>(w[t][k]);
+#pragma unroll
+            for (int f = 0; f < MF; ++f) g[t][f] = W4Type<T>::mfma(x[f], q, g[t][f]);
+        }
+        if (k % kSteps != kSteps - 1) return;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float scale = (float)sc[t][u];
+#pragma unroll
+            for (int f = 0; f < MF; ++f) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[t][f][r] = __builtin_fmaf(g[t][f][r], scale, acc[t][f][r]);
+                asm volatile("" : "+v"(acc[t][f]));  // here, not gathered behind the last step with every g kept
             }
         }
     }
-    // acc[t][f] += the block's product with the rows x[f] (four steps of 32 inputs).  The part of the zero points,
-    // -(16 + z) times the sum of a row's inputs, is where a group's accumulator starts: that sum is one MFMA per step
-    // for all the tiles.
+    // The whole block, the sums taken by an MFMA per step for all the tiles at once.
     template <int MF>
-    __device__ __forceinline__ void multiply(const typename W4Type<T>::frag (&x)[MF][4], f32x4 (&acc)[NT][MF]) const
+    __device__ __forceinline__ void multiply(const typename W4Type<T>::frag (&x)[4][MF], f32x4 (&acc)[NT][MF]) const
     {
-        constexpr int kSteps = 4 / SUBS;  // steps per scale
-        const typename W4Type<T>::frag unit = w4_constant<T>(ZEROS ? -1.f : -24.f);
+        const typename W4Type<T>::frag unit = w4_constant<T>(w4_unit<ZEROS>());
+        f32x4 g[NT][MF];
 #pragma unroll
-        for (int u = 0; u < SUBS; ++u) {
-            f32x4 start[MF] = {};
+        for (int k = 0; k < 4; ++k)
+            step(x[k], k, g, acc, [&](int u, int f) {
+                f32x4 s = {};
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                for (int f = 0; f < MF; ++f) start[f] = W4Type<T>::mfma(x[f][u * kSteps + k], unit, start[f]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f32x4 g[MF];
-#pragma unroll
-                for (int f = 0; f < MF; ++f) g[f] = ZEROS ? start[f] * (float)(16 + z[t][u]) : start[f];
-#pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    const typename W4Type<T>::frag q = w4_expand<T>(w[t][u * kSteps + k]);
-#pragma unroll
-                    for (int f = 0; f < MF; ++f) g[f] = W4Type<T>::mfma(x[f][u * kSteps + k], q, g[f]);
-                }
-                const float scale = (float)sc[t][u];
-#pragma unroll
-                for (int f = 0; f < MF; ++f)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[t][f][r] = __builtin_fmaf(g[f][r], scale, acc[t][f][r]);
-            }
-        }
+                for (int i = u * (4 / SUBS); i < (u + 1) * (4 / SUBS); ++i) s = W4Type<T>::mfma(x[i][f], unit, s);
+                return s;
+            });
     }
 };
 
@@ -246,13 +279,13 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(const W4Args a)
         for (int i = 0; i < kLoads; ++i)
             if (i < loads) x[i] = *reinterpret_cast<const vec8<T>*>(row(i) + b * kW4Block + col0);
     };
-    auto fragments = [&](const vec8<T> (&x)[kLoads], frag (&s)[MF][4]) {
+    auto fragments = [&](const vec8<T> (&x)[kLoads], frag (&s)[4][MF]) {
         if constexpr (FEW) {
             const i32x4 v = __builtin_bit_cast(i32x4, x[0]);
             s[0][0] = __builtin_bit_cast(frag, v);
-            s[0][1] = __builtin_bit_cast(frag, lanes_down<4>(v));
-            s[0][2] = __builtin_bit_cast(frag, lanes_down<8>(v));
-            s[0][3] = __builtin_bit_cast(frag, lanes_down<12>(v));
+            s[1][0] = __builtin_bit_cast(frag, lanes_down<4>(v));
+            s[2][0] = __builtin_bit_cast(frag, lanes_down<8>(v));
+            s[3][0] = __builtin_bit_cast(frag, lanes_down<12>(v));
         } else {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
@@ -263,14 +296,14 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(const W4Args a)
             for (int f = 0; f < MF; ++f)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    s[f][t] = *reinterpret_cast<const frag*>(area + (16 * f + l16) * kRow + (((4 * t + r0) ^ l16) * 16));
+                    s[t][f] = *reinterpret_cast<const frag*>(area + (16 * f + l16) * kRow + (((4 * t + r0) ^ l16) * 16));
         }
     };
     const int b0 = (int)((int64_t)a.l.blocks * wave / WAVES), b1 = (int)((int64_t)a.l.blocks * (wave + 1) / WAVES);
     const int whole = min(b1, a.l.K / kW4Block);  // the last block may end past K
     Block w[WA];
     vec8<T> x[XA][kLoads];
-    frag s[MF][4];
+    frag s[4][MF];
 #pragma unroll
     for (int i = 0; i < WA; ++i)
         if (b0 + i < whole) {
@@ -319,77 +352,143 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(const W4Args a)
     }
 }
 
-// Many rows: 64 rows x 64 NT columns per workgroup, four waves of 64 x 16 NT over the
-// whole of K.  The rows' block of x goes through LDS (16-byte chunk c of row m at
-// c ^ m % 16), two blocks ahead in registers; each wave expands its own weights.
+// Many rows: 64 rows x 64 NT columns per workgroup.  Two sets of four waves take half of
+// K's blocks each, a wave 64 x 16 NT, and add up through LDS at the end.  A set's rows of
+// a block go through LDS (16-byte chunk c of row m at c ^ m % 16), two blocks ahead in
+// registers; each wave expands its own weights.  Whoever writes a row's inputs also sums
+// them for the zero points: sums by MFMA, as the kernel above takes them, would repeat in
+// every wave and cost 1 / NT of the product.
 constexpr int kW4Rows = 64;
 
+// Adds another lane's value, within 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ float w4_lanes_add(float v)
+{
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
 template <class T, int NT, int SUBS, bool ZEROS>
-__global__ __launch_bounds__(256, 2) void w4_tile_kernel(const W4Args a)
+__global__ __launch_bounds__(512, 2) void w4_tile_kernel(const W4Args a)
 {
     typedef typename W4Type<T>::frag frag;
     typedef W4Block<T, NT, SUBS, ZEROS> Block;
     constexpr int kRow = kW4Block * 2;  // bytes of a row's block
-    __shared__ __attribute__((aligned(16))) char lds[2][kW4Rows * kRow];
-    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
-    const int tile0 = (blockIdx.y * 4 + wave) * NT;
+    struct Stage {
+        char x[kW4Rows * kRow];
+        float sum[SUBS][kW4Rows];
+    };
+    __shared__ __attribute__((aligned(16))) char lds[4 * sizeof(Stage)];
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), set = wave >> 2;
+    Stage* const stage = reinterpret_cast<Stage*>(lds) + 2 * set;
+    const int tile0 = (blockIdx.y * 4 + (wave & 3)) * NT;
     const int64_t m0 = (int64_t)blockIdx.x * kW4Rows;
-    const int chunk = threadIdx.x & 15, r0 = threadIdx.x >> 4;
-    const T* xrow[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        int64_t m = m0 + r0 + 16 * i;
-        m = m < a.M ? m : a.M - 1;
-        xrow[i] = static_cast<const T*>(a.x) + m * a.x_stride;
-    }
+    const int chunk = threadIdx.x & 15, r0 = (threadIdx.x & 255) >> 4;
+    const int share = a.l.K / kW4Block / 2, b0 = set * share;
+    auto xrow = [&](int i) {  // rows past the last read it again, and are not stored
+        const int64_t m = m0 + r0 + 16 * i;
+        return static_cast<const T*>(a.x) + (m < a.M ? m : a.M - 1) * a.x_stride;
+    };
     vec8<T> xr[4];
     auto load_x = [&](int b) {
-        if (b >= a.l.blocks) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) xr[i] = load8(xrow[i], b * kW4Block + chunk * 8, a.l.K);
+        for (int i = 0; i < 4; ++i) xr[i] = *reinterpret_cast<const vec8<T>*>(xrow(i) + b * kW4Block + chunk * 8);
     };
-    auto put_x = [&](char* stage) {
+    auto put_x = [&](Stage& st) {
+        float sum[4] = {};  // of the row's sub-block, over the 16 / SUBS lanes that hold it
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<u32x4*>(stage + (r0 + 16 * i) * kRow + ((chunk ^ r0) * 16)) = __builtin_bit_cast(u32x4, xr[i]);
+        for (int i = 0; i < 4; ++i) {
+            const u32x4 v = __builtin_bit_cast(u32x4, xr[i]);
+            *reinterpret_cast<u32x4*>(st.x + (r0 + 16 * i) * kRow + ((chunk ^ r0) * 16)) = v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[i] = W4Type<T>::add2(v[j], sum[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = w4_lanes_add<0xB1>(sum[i]);  // lane ^ 1
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = w4_lanes_add<0x4E>(sum[i]);  // lane ^ 2
+        if constexpr (SUBS < 4)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = w4_lanes_add<0x141>(sum[i]);  // the other four of eight
+        if constexpr (SUBS < 2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = w4_lanes_add<0x140>(sum[i]);  // the other eight of sixteen
+        const float lo = chunk & 1 ? sum[1] : sum[0], hi = chunk & 1 ? sum[3] : sum[2];
+        if (chunk % (16 / SUBS) < 4)
+            st.sum[chunk / (16 / SUBS)][r0 + 16 * (chunk & 3)] = (chunk & 2 ? hi : lo) * w4_unit<ZEROS>();
     };
     f32x4 acc[NT][4] = {};
+    auto multiply = [&](const Stage& st, const Block& w, auto load) {
+        frag x[2][4];
+        auto read_x = [&](int k) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+                x[k & 1][f] = *reinterpret_cast<const frag*>(st.x + (f * 16 + (lane & 15)) * kRow +
+                                                             (((4 * k + (lane >> 4)) ^ (lane & 15)) * 16));
+        };
+        read_x(0);
+        load();
+        f32x4 g[NT][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k < 3) read_x(k + 1);
+            w.step(x[k & 1], k, g, acc, [&](int u, int f) {
+                return *reinterpret_cast<const f32x4*>(&st.sum[u][f * 16 + 4 * (lane >> 4)]);
+            });
+        }
+    };
     Block w[2];
-    load_x(0);
-    w[0].load(a, tile0, 0);
-    if (a.l.blocks > 1) w[1].load(a, tile0, 1);
-    put_x(lds[0]);
-    load_x(1);
-    __syncthreads();
-    for (int b = 0; b < a.l.blocks; b += 2) {
+    if (share > 0) {
+        load_x(b0);
+        w[0].load(a, tile0, b0);
+        if (share > 1) w[1].load(a, tile0, b0 + 1);
+        put_x(stage[0]);
+        if (share > 1) load_x(b0 + 1);
+    }
+    for (int j = 0; j < share; j += 2) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (b + i < a.l.blocks) {
-                frag x[4][4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int f = 0; f < 4; ++f)
-                        x[f][t] = *reinterpret_cast<const frag*>(lds[i] + (f * 16 + (lane & 15)) * kRow +
-                                                                 (((4 * t + (lane >> 4)) ^ (lane & 15)) * 16));
-                if (b + i + 1 < a.l.blocks) put_x(lds[i ^ 1]);
-                load_x(b + i + 2);
-                w[i].multiply(x, acc);
-                if (b + i + 2 < a.l.blocks) w[i].load(a, tile0, b + i + 2);
+            if (j + i < share) {
                 __syncthreads();
+                multiply(stage[i], w[i], [&] {
+                    if (j + i + 1 < share) put_x(stage[i ^ 1]);
+                    if (j + i + 2 < share) load_x(b0 + j + i + 2);
+                });
+                if (j + i + 2 < share) w[i].load(a, tile0, b0 + j + i + 2);
             }
     }
+    // The block without a partner, and the one that ends past K
+    const int last = 2 * share + set;
+    __syncthreads();
+    if (last < a.l.blocks) {
+        w[0].load(a, tile0, last);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xr[i] = load8(xrow(i), last * kW4Block + chunk * 8, a.l.K);
+        put_x(stage[0]);
+    }
+    __syncthreads();
+    if (last < a.l.blocks) multiply(stage[0], w[0], [] {});
+    __syncthreads();
+    f32x4* const part = reinterpret_cast<f32x4*>(lds) + (wave & 3) * (NT * 4 * 64) + lane;
+    static_assert(sizeof(lds) >= 4 * NT * 4 * 64 * 16, "the second set's results");
+    if (set)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) part[(t * 4 + f) * 64] = acc[t][f];
+    __syncthreads();
+    if (set) return;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int n = (tile0 + t) * kW4Tile + (lane & 15);
-        if (n >= a.l.N) continue;
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
+        for (int f = 0; f < 4; ++f) {
+            const f32x4 y = acc[t][f] + part[(t * 4 + f) * 64];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int64_t m = m0 + f * 16 + 4 * (lane >> 4) + r;
-                if (m < a.M) static_cast<T*>(a.y)[m * a.y_stride + n] = (T)acc[t][f][r];
+                if (n < a.l.N && m < a.M) static_cast<T*>(a.y)[m * a.y_stride + n] = (T)y[r];
             }
+        }
     }
 }
 
