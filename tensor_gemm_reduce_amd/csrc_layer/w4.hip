@@ -62,8 +62,8 @@ int w4_tile_launch(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
 
 // Up to 32 rows: the kernel whose waves split K, with one tile of columns and more waves
 // per workgroup where the tiles are no more than the CUs, else two tiles.  Measured, us
-// (one / two): 3584 x 4096 at 1 row 4.5 / 4.8 (8 waves, one tile too), at 9 rows 5.5 / 7.0,
-// at 24 7.1 / 8.5; 7168 x 8192 at 9 rows 15.4 / 11.5, at 24 20 / 14.4.
+// (one / two): 3584 x 4096 at 4 rows 4.7 / 6.2, at 9 5.5 / 7.0, at 24 7.1 / 8.5; 7168 x 8192
+// at 4 rows 12.1 (8 waves) / 10.7, at 9 15.4 / 11.5, at 24 20 / 14.4.
 //
 // More rows: whichever of six kernels costs least, as rounds of workgroups over the CUs
 // times a round's cost.  A round takes a time that grows with the columns per workgroup,
@@ -76,7 +76,7 @@ int w4_run(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
 {
     const bool narrow = a.l.tiles <= kCus;
     if (a.M <= 4)
-        return narrow ? w4_launch<T, 16, 1, 1, true, 2, 2>(c, a, stream) : w4_launch<T, 8, 1, 1, true, 4, 4>(c, a, stream);
+        return narrow ? w4_launch<T, 16, 1, 1, true, 2, 2>(c, a, stream) : w4_launch<T, 8, 2, 1, true, 4, 4>(c, a, stream);
     if (a.M <= 16)
         return narrow ? w4_launch<T, 16, 1, 1, false, 2, 2>(c, a, stream) : w4_launch<T, 8, 2, 1, false, 4, 4>(c, a, stream);
     if (a.M <= 32)

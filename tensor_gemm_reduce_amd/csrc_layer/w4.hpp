@@ -194,29 +194,32 @@ struct W4Block {
     {
         constexpr int kSteps = 4 / SUBS;  // steps per scale
         const int u = k / kSteps;
+        f32x4 s[MF];
         if (k % kSteps == 0)
 #pragma unroll
-            for (int f = 0; f < MF; ++f) {
-                const f32x4 s = start(u, f);
+            for (int f = 0; f < MF; ++f) s[f] = start(u, f);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) g[t][f] = ZEROS ? s * (float)(16 + z[t][u]) : s;
+        for (int t0 = 0; t0 < NT; t0 += 2) {
+#pragma unroll
+            for (int t = t0; t < NT && t < t0 + 2; ++t) {
+                if (k % kSteps == 0)
+#pragma unroll
+                    for (int f = 0; f < MF; ++f) g[t][f] = ZEROS ? s[f] * (float)(16 + z[t][u]) : s[f];
+                const typename W4Type<T>::frag q = w4_expand<T>(w[t][k]);
+#pragma unroll
+                for (int f = 0; f < MF; ++f) g[t][f] = W4Type<T>::mfma(x[f], q, g[t][f]);
             }
+            if (k % kSteps == kSteps - 1)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const typename W4Type<T>::frag q = w4_expand<T>(w[t][k]);
+                for (int t = t0; t < NT && t < t0 + 2; ++t) {
+                    const float scale = (float)sc[t][u];
 #pragma unroll
-            for (int f = 0; f < MF; ++f) g[t][f] = W4Type<T>::mfma(x[f], q, g[t][f]);
-        }
-        if (k % kSteps != kSteps - 1) return;
+                    for (int f = 0; f < MF; ++f) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const float scale = (float)sc[t][u];
-#pragma unroll
-            for (int f = 0; f < MF; ++f) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[t][f][r] = __builtin_fmaf(g[t][f][r], scale, acc[t][f][r]);
-                asm volatile("" : "+v"(acc[t][f]));  // here, not gathered behind the last step with every g kept
-            }
+                        for (int r = 0; r < 4; ++r) acc[t][f][r] = __builtin_fmaf(g[t][f][r], scale, acc[t][f][r]);
+                        asm volatile("" : "+v"(acc[t][f]));  // here, not gathered behind the last step with every g kept
+                    }
+                }
         }
     }
     // The whole block, the sums taken by an MFMA per step for all the tiles at once.
