@@ -318,22 +318,26 @@ constexpr int kWgCol = 128;   // LDS bytes of a column's tokens
 // LDS offset of chunk c (8 tokens) of column r
 __device__ __forceinline__ int wgrad_at(int r, int c) { return r * kWgCol + ((c ^ r ^ ((r >> 3) & 3)) & 7) * 16; }
 
-// A thread's share of a step: 8 tokens x 8 columns of dy and of the checkpoint.
+// A thread's share of a step: 8 tokens x C columns of dy and of the checkpoint.
+template <int C>
 struct WgradRegs {
-    u32x4 y[8];
-    u32x2 x[8];
+    typedef uint32_t y_t __attribute__((ext_vector_type(C / 2)));
+    typedef uint32_t x_t __attribute__((ext_vector_type(C / 4)));
+    y_t y[8];
+    x_t x[8];
     int e[2];  // scales of tokens 2 (lane % 4) and the next: four lanes share a block of 32 columns
 };
 
-template <class T>
+template <class T, int C>
 struct WgradLoader {
+    typedef WgradRegs<C> Regs;
     const WgradArgs& a;
     uint32_t yoff, xoff, eoff, ypitch;
     int eper;
     int64_t end;  // first step past the range
     __amdgpu_buffer_rsrc_t ry, rq, re;
 
-    // tg: which eight of the step's tokens; n, k: the first of the eight columns of dy and x
+    // tg: which eight of the step's tokens; n, k: the first of the C columns of dy and x
     __device__ __forceinline__ WgradLoader(const WgradArgs& args, int tg, int n, int k, int64_t stop) : a(args), end(stop)
     {
         ypitch = (uint32_t)a.dy_stride * 2u;
@@ -353,22 +357,27 @@ struct WgradLoader {
         rq = __builtin_amdgcn_make_buffer_rsrc((void*)(a.q + m * a.Kp), 0, rows * a.Kp, kRsrcFlags);
         re = __builtin_amdgcn_make_buffer_rsrc((void*)(a.e + m * eper), 0, rows * eper, kRsrcFlags);
     }
-    __device__ __forceinline__ void load_y(WgradRegs& r, int i) const
+    __device__ __forceinline__ void load_y(Regs& r, int i) const
     {
-        r.y[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ry, yoff + (uint32_t)i * ypitch, 0, 0));
+        const uint32_t at = yoff + (uint32_t)i * ypitch;
+        if constexpr (C == 8) r.y[i] = __builtin_bit_cast(typename Regs::y_t, __builtin_amdgcn_raw_buffer_load_b128(ry, at, 0, 0));
+        else r.y[i] = __builtin_bit_cast(typename Regs::y_t, __builtin_amdgcn_raw_buffer_load_b64(ry, at, 0, 0));
     }
-    __device__ __forceinline__ void load_x(WgradRegs& r, int i) const
+    __device__ __forceinline__ void load_x(Regs& r, int i) const
     {
-        r.x[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rq, xoff + (uint32_t)(i * a.Kp), 0, 0));
+        const uint32_t at = xoff + (uint32_t)(i * a.Kp);
+        if constexpr (C == 8) r.x[i] = __builtin_bit_cast(typename Regs::x_t, __builtin_amdgcn_raw_buffer_load_b64(rq, at, 0, 0));
+        else r.x[i] = __builtin_bit_cast(typename Regs::x_t, __builtin_amdgcn_raw_buffer_load_b32(rq, at, 0, 0));
     }
-    __device__ __forceinline__ void load_e(WgradRegs& r, int i) const
+    __device__ __forceinline__ void load_e(Regs& r, int i) const
     {
         r.e[i] = (int8_t)__builtin_amdgcn_raw_buffer_load_b8(re, eoff + (uint32_t)(i * eper), 0, 0);
     }
 };
 
 // The eight tokens' scales from the four lanes that hold two each.
-__device__ __forceinline__ void wgrad_scales(const WgradRegs& r, float (&sc)[8])
+template <int C>
+__device__ __forceinline__ void wgrad_scales(const WgradRegs<C>& r, float (&sc)[8])
 {
     const int s[2] = {(int)__float_as_uint(block_scale(r.e[0])), (int)__float_as_uint(block_scale(r.e[1]))};
 #pragma unroll
@@ -381,8 +390,8 @@ __device__ __forceinline__ void wgrad_scales(const WgradRegs& r, float (&sc)[8])
 }
 
 // Tokens 2 p and 2 p + 1 of column j of the checkpoint as a pair of T.
-template <class T>
-__device__ __forceinline__ uint32_t wgrad_pair_x(const WgradRegs& r, const float (&sc)[8], int j, int p)
+template <class T, int C>
+__device__ __forceinline__ uint32_t wgrad_pair_x(const WgradRegs<C>& r, const float (&sc)[8], int j, int p)
 {
     typedef T t2 __attribute__((ext_vector_type(2)));
     const t2 v = {(T)(byte_value(r.x[2 * p][j / 4], j % 4) * sc[2 * p]),
@@ -391,7 +400,8 @@ __device__ __forceinline__ uint32_t wgrad_pair_x(const WgradRegs& r, const float
 }
 
 // Tokens 2 p and 2 p + 1 of column j of dy.
-__device__ __forceinline__ uint32_t wgrad_pair_y(const WgradRegs& r, int j, int p)
+template <int C>
+__device__ __forceinline__ uint32_t wgrad_pair_y(const WgradRegs<C>& r, int j, int p)
 {
     return __builtin_amdgcn_perm(r.y[2 * p + 1][j / 2], r.y[2 * p][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
 }
@@ -405,7 +415,7 @@ struct WgradTile {
     static constexpr int kLds = 2 * kStage;
 };
 
-// LDS offsets of a thread in each of the two stages: its first column of eight as a
+// LDS offsets of a thread in each of the two stages: its first column as a
 // loader (column j's chunk lies at offset ^ 16 j, j columns on), and its column of the
 // wave's first fragment as a reader, for each 16 tokens.
 template <class T, int WN, int WK>
@@ -413,7 +423,7 @@ struct WgradPlaces {
     typedef WgradTile<WN, WK> Tile;
     typedef typename Mfma<T>::frag frag;
     static constexpr int kX = Tile::kBN * kWgCol;  // the checkpoint's columns after dy's
-    static constexpr int kPer = Tile::kBN / 8;     // threads side by side
+    static constexpr int kCols = Tile::kBN / 32;   // columns a thread loads
 
     char* const lds;
     uint32_t put[2], get_y[2][4], get_x[2][4];
@@ -421,10 +431,10 @@ struct WgradPlaces {
     __device__ __forceinline__ explicit WgradPlaces(char* l) : lds(l)
     {
         static_assert(WN == WK, "square tiles");
-        const int tg = threadIdx.x / kPer % 8, cg = threadIdx.x % kPer, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int tg = threadIdx.x / 32, cg = threadIdx.x % 32, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            put[p] = p * Tile::kStage + wgrad_at(8 * cg, tg);
+            put[p] = p * Tile::kStage + wgrad_at(kCols * cg, tg);
 #pragma unroll
             for (int sub = 0; sub < 4; ++sub) {
                 get_y[p][sub] = p * Tile::kStage + wgrad_at((wave >> 1) * 32 * WN + (lane & 31), 2 * sub + (lane >> 5));
@@ -433,7 +443,7 @@ struct WgradPlaces {
         }
     }
     // Takes the constancy of these from the compiler, which would give every sum with them a register of its own.
-    __device__ __forceinline__ void hide(WgradLoader<T>& ld)
+    __device__ __forceinline__ void hide(WgradLoader<T, kCols>& ld)
     {
         __asm__ __volatile__("" : "+v"(put[0]), "+v"(put[1]), "+v"(ld.yoff), "+v"(ld.xoff), "+v"(ld.eoff));
     }
@@ -455,127 +465,42 @@ struct WgradPlaces {
     }
 };
 
-// One tile over the steps s0 .. s1 - 1, tiles of 128 x 128: two workgroups share a CU
-// and cover each other's waits.  Waves 0 and 1 load and turn dy, waves 2 and 3 the
-// checkpoint (X), two steps ahead in two sets of registers.
-template <class T, bool X>
-struct WgradSmall : WgradPlaces<T, 2, 2> {
-    typedef WgradPlaces<T, 2, 2> Places;
+// One tile over the steps s0 .. s1 - 1.  A step runs from barrier to barrier.  At its
+// start stage s is written, and the other stage read but for fragments that are already
+// in registers, so the whole step can write stage s + 1.  Each of its 4 W^2 MFMAs is
+// followed by a share of the step's other work, and fences keep it there: what waited for
+// the MFMAs' end, or came in one piece, would find nothing to run beside.
+//   MFMA 0 ..   the last 16 tokens of step s - 1, then the first 48 of step s; the
+//               fragment reads go 16 tokens ahead
+//   columns     of the thread's, of the checkpoint and of dy, a pair of tokens at a time,
+//               each written when done
+//   the loads   of step s + 2, into the other set of registers: more than a step to
+//               arrive
+// W = 4, tiles of 256 x 256: one workgroup per CU, one wave per SIMD, whose 256
+// accumulators leave no second wave to cover a wait.  What does not fit under an MFMA's 32
+// cycles (or under the LDS queue's pace, some 28 cycles per 16-byte instruction of one
+// wave) adds to the step, so all of it is spread evenly.
+// W = 2, tiles of 128 x 128: two workgroups share a CU.  The loads come first, three to a
+// place: 512 x 2048 x 512 takes 11.5 us so, 12.0 with one to a place, 12.5 with all in the
+// first.  LDS (16 reads and 8 writes a wave) and the conversion of the checkpoint bound a
+// step: 1.3 us for the two workgroups, of which the MFMAs take 0.45.
+template <class T, int W>
+struct WgradRun : WgradPlaces<T, W, W> {
+    typedef WgradPlaces<T, W, W> Places;
     typedef typename Places::frag frag;
+    static constexpr int kCols = Places::kCols, kBN = Places::Tile::kBN;
 
-    f32x16 (&acc)[2][2];
-    WgradLoader<T> ld;
-    WgradRegs r[2];
+    f32x16 (&acc)[W][W];
+    WgradLoader<T, kCols> ld;
+    WgradRegs<kCols> r[2];
+    frag fy[2][W], fx[2][W];
 
-    __device__ __forceinline__ WgradSmall(const WgradArgs& a, char* l, int tn, int tk, int64_t s1, f32x16 (&c)[2][2])
+    __device__ __forceinline__ WgradRun(const WgradArgs& a, char* l, int tn, int tk, int64_t s1, f32x16 (&c)[W][W])
         : Places(l), acc(c),
-          ld(a, threadIdx.x / 16 % 8, tn * 128 + 8 * (threadIdx.x % 16), tk * 128 + 8 * (threadIdx.x % 16), s1)
+          ld(a, threadIdx.x / 32, tn * kBN + kCols * (threadIdx.x % 32), tk * kBN + kCols * (threadIdx.x % 32), s1)
     {
     }
-    __device__ __forceinline__ void load(WgradRegs& g, int64_t step)
-    {
-        ld.at(step);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (X) ld.load_x(g, i);
-            else ld.load_y(g, i);
-        }
-        if constexpr (X) {
-            ld.load_e(g, 0);
-            ld.load_e(g, 1);
-        }
-    }
-    template <int P>
-    __device__ __forceinline__ void put_all(const WgradRegs& g) const
-    {
-        float sc[8];
-        if constexpr (X) wgrad_scales(g, sc);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            u32x4 v;
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                if constexpr (X) v[p] = wgrad_pair_x<T>(g, sc, j, p);
-                else v[p] = wgrad_pair_y(g, j, p);
-            }
-            this->template write<P>(j, X, v);
-        }
-    }
-    // stage s is written in buffer P, step s + 1's data in r[P ^ 1] or on its way there
-    template <int P>
-    __device__ __forceinline__ void step(int64_t s)
-    {
-        this->hide(ld);
-        load(r[P], s + 2);
-#pragma unroll
-        for (int sub = 0; sub < 4; ++sub) {
-            frag fy[2], fx[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fx[i] = this->template read<P>(sub, i, true);
-                fy[i] = this->template read<P>(sub, i, false);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = Mfma<T>::run(fx[j], fy[i], acc[i][j]);
-        }
-        put_all<P ^ 1>(r[P ^ 1]);
-        this->barrier();
-    }
-    __device__ __forceinline__ void run(int64_t s0, int64_t s1)
-    {
-        load(r[0], s0);
-        load(r[1], s0 + 1);
-        put_all<0>(r[0]);
-        this->barrier();
-        // in twos: a step past the range multiplies the zeros its loads gave
-        for (int64_t s = s0; s < s1; s += 2) {
-            step<0>(s);
-            step<1>(s + 1);
-        }
-    }
-};
-
-template <class T>
-__device__ __forceinline__ void wgrad_run_tile(const WgradArgs& a, char* lds, int tn, int tk, int64_t s0, int64_t s1,
-                                               f32x16 (&acc)[2][2])
-{
-    // the same barriers in both
-    if (uni(threadIdx.x >> 6) < 2) WgradSmall<T, false>(a, lds, tn, tk, s1, acc).run(s0, s1);
-    else WgradSmall<T, true>(a, lds, tn, tk, s1, acc).run(s0, s1);
-}
-
-// The same for tiles of 256 x 256: one workgroup per CU, one wave per SIMD, whose 256
-// accumulators leave no second wave to cover a wait.  So every other instruction of a
-// step has a place after one of its 64 MFMAs, and fences keep it there; they are spread
-// evenly, since what does not fit under an MFMA's 32 cycles (or under the LDS queue's
-// pace, some 28 cycles per 16-byte instruction of one wave) adds to the step.
-//
-// A step runs from barrier to barrier.  At its start stage s is written, and the other
-// stage read but for fragments that are already in registers, so the whole step can
-// write stage s + 1:
-//   MFMA 0 ..     the last 16 tokens of step s - 1, then the first 48 of step s; the
-//                 fragment reads go 16 tokens ahead, eight in the first twelve places
-//   MFMA 7 j ..   column j of the thread's eight, of the checkpoint (a pair of tokens
-//                 every other place) and of dy (between them), each written when done
-//   the loads     of step s + 2, into the other set of registers: more than a step to
-//                 arrive
-template <class T>
-struct WgradBig : WgradPlaces<T, 4, 4> {
-    typedef WgradPlaces<T, 4, 4> Places;
-    typedef typename Places::frag frag;
-
-    f32x16 (&acc)[4][4];
-    WgradLoader<T> ld;
-    WgradRegs r[2];
-    frag fy[2][4], fx[2][4];
-
-    __device__ __forceinline__ WgradBig(const WgradArgs& a, char* l, int tn, int tk, int64_t s1, f32x16 (&c)[4][4])
-        : Places(l), acc(c), ld(a, threadIdx.x / 32, tn * 256 + 8 * (threadIdx.x % 32), tk * 256 + 8 * (threadIdx.x % 32), s1)
-    {
-    }
-    __device__ __forceinline__ void load(WgradRegs& g, int i) const  // 0 .. 17
+    __device__ __forceinline__ void load(WgradRegs<kCols>& g, int i) const  // 0 .. 17
     {
         if (i < 2) ld.load_e(g, i);
         else if (i < 10) ld.load_x(g, i - 2);
@@ -587,33 +512,45 @@ struct WgradBig : WgradPlaces<T, 4, 4> {
     __device__ __forceinline__ void step(int64_t s)
     {
         this->hide(ld);
-        WgradRegs& g = r[P ^ 1];
+        WgradRegs<kCols>& g = r[P ^ 1];
         ld.at(s + 2);
         float sc[8];
         wgrad_scales(g, sc);
         u32x4 wx[2], wy;
 #pragma unroll
-        for (int m = 0; m < 64; ++m) {
-            const int u = m / 16, i = (m % 16) / 4, j = m % 4;
+        for (int m = 0; m < 4 * W * W; ++m) {
+            const int u = m / (W * W), q = m % (W * W), i = q / W, j = q % W;
             // u = 0: fragments 3 of the step before, read into set 1
             acc[i][j] = Mfma<T>::run(fx[(u + 1) & 1][j], fy[(u + 1) & 1][i], acc[i][j]);
-            const int q = m % 16;
-            if (q < 12 && q % 3 != 2) {
-                const int f = q / 3 * 2 + q % 3;  // the checkpoint's first: each MFMA row needs all four
-                if (f < 4) fx[u & 1][f] = this->template read<P>(u, f, true);
-                else fy[u & 1][f - 4] = this->template read<P>(u, f - 4, false);
-            }
-            if (m % 3 == 2 && m / 3 < 18) load(r[P], m / 3);
-            const int c = m / 7, k = m % 7;  // column and place in its seven
-            if (c < 8) {
-                if (k % 2 == 0) wx[c & 1][k / 2] = wgrad_pair_x<T>(g, sc, c, k / 2);
-                if (k % 2 == 1) wy[k / 2] = wgrad_pair_y(g, c, k / 2);
-                if (k == 5) {
-                    wy[3] = wgrad_pair_y(g, c, 3);
-                    this->template write<P ^ 1>(c, false, wy);
+            if constexpr (W == 4) {
+                if (q < 12 && q % 3 != 2) {
+                    const int f = q / 3 * 2 + q % 3;  // the checkpoint's first: each MFMA row needs all four
+                    if (f < 4) fx[u & 1][f] = this->template read<P>(u, f, true);
+                    else fy[u & 1][f - 4] = this->template read<P>(u, f - 4, false);
+                }
+                if (m % 3 == 2 && m / 3 < 18) load(r[P], m / 3);
+                const int c = m / 7, k = m % 7;  // column and place in its seven
+                if (c < 8) {
+                    if (k % 2 == 0) wx[c & 1][k / 2] = wgrad_pair_x<T>(g, sc, c, k / 2);
+                    if (k % 2 == 1) wy[k / 2] = wgrad_pair_y(g, c, k / 2);
+                    if (k == 5) {
+                        wy[3] = wgrad_pair_y(g, c, 3);
+                        this->template write<P ^ 1>(c, false, wy);
+                    }
+                }
+                if (c > 0 && k == 1) this->template write<P ^ 1>(c - 1, true, wx[(c - 1) & 1]);
+            } else {
+                if (q % 2 == 0) fx[u & 1][q / 2] = this->template read<P>(u, q / 2, true);
+                else fy[u & 1][q / 2] = this->template read<P>(u, q / 2, false);
+#pragma unroll
+                for (int l = 3 * m; l < 3 * m + 3 && l < 18; ++l) load(r[P], l);
+                wx[0][q] = wgrad_pair_x<T>(g, sc, u, q);
+                wy[q] = wgrad_pair_y(g, u, q);
+                if (q == 3) {
+                    this->template write<P ^ 1>(u, false, wy);
+                    this->template write<P ^ 1>(u, true, wx[0]);
                 }
             }
-            if (c > 0 && k == 1) this->template write<P ^ 1>(c - 1, true, wx[(c - 1) & 1]);
             __builtin_amdgcn_sched_barrier(0);
         }
         this->barrier();
@@ -621,16 +558,16 @@ struct WgradBig : WgradPlaces<T, 4, 4> {
 
     __device__ __forceinline__ void run(int64_t s0, int64_t s1)
     {
-        ld.at(s0);
 #pragma unroll
-        for (int i = 0; i < 18; ++i) load(r[0], i);
-        ld.at(s0 + 1);
+        for (int p = 0; p < 2; ++p) {
+            ld.at(s0 + p);
 #pragma unroll
-        for (int i = 0; i < 18; ++i) load(r[1], i);
+            for (int i = 0; i < 18; ++i) load(r[p], i);
+        }
         float sc[8];
         wgrad_scales(r[0], sc);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kCols; ++j) {
             u32x4 x, y;
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
@@ -640,9 +577,9 @@ struct WgradBig : WgradPlaces<T, 4, 4> {
             this->template write<0>(j, false, y);
             this->template write<0>(j, true, x);
         }
-        // nothing before the first step: its first 16 MFMAs add zeros
+        // nothing before the first step: its first MFMAs add zeros
 #pragma unroll
-        for (int i = 0; i < 4; ++i) fy[1][i] = fx[1][i] = frag{};
+        for (int i = 0; i < W; ++i) fy[1][i] = fx[1][i] = frag{};
         this->barrier();
         // in twos: a step past the range multiplies the zeros its loads gave
         for (int64_t s = s0; s < s1; s += 2) {
@@ -650,19 +587,12 @@ struct WgradBig : WgradPlaces<T, 4, 4> {
             step<1>(s + 1);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < W; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = Mfma<T>::run(fx[1][j], fy[1][i], acc[i][j]);
+            for (int j = 0; j < W; ++j) acc[i][j] = Mfma<T>::run(fx[1][j], fy[1][i], acc[i][j]);
         __syncthreads();
     }
 };
-
-template <class T>
-__device__ __forceinline__ void wgrad_run_tile(const WgradArgs& a, char* lds, int tn, int tk, int64_t s0, int64_t s1,
-                                               f32x16 (&acc)[4][4])
-{
-    WgradBig<T>(a, lds, tn, tk, s1, acc).run(s0, s1);
-}
 
 template <class T, int WN, int WK>
 __global__ __launch_bounds__(kWgThreads, WN == 4 ? 1 : 2) void wgrad_kernel(const WgradArgs a, const WgradPlan p)
@@ -683,7 +613,7 @@ __global__ __launch_bounds__(kWgThreads, WN == 4 ? 1 : 2) void wgrad_kernel(cons
         int tn, tk;
         wgrad_tile(p, t, tn, tk);
         clear();
-        wgrad_run_tile<T>(a, lds, tn, tk, 0, p.steps, acc);
+        WgradRun<T, WN>(a, lds, tn, tk, p.steps, acc).run(0, p.steps);
 #pragma unroll
         for (int i = 0; i < WN; ++i)
             wgrad_store_rows<T, WK>(a, lds + wave * (32 * 32 * WK * 4), tn * Tile::kBN + (wave >> 1) * 32 * WN + 32 * i,
@@ -698,7 +628,7 @@ __global__ __launch_bounds__(kWgThreads, WN == 4 ? 1 : 2) void wgrad_kernel(cons
         int tn, tk;
         wgrad_tile(p, p.full + (int)t, tn, tk);
         clear();
-        wgrad_run_tile<T>(a, lds, tn, tk, at - t * p.steps, stop - t * p.steps, acc);
+        WgradRun<T, WN>(a, lds, tn, tk, stop - t * p.steps, acc).run(at - t * p.steps, stop - t * p.steps);
         // in the order of the registers: [block][four accumulators][thread]
         f32x4* out = reinterpret_cast<f32x4*>(p.pieces + (int64_t)(2 * me + slot) * Tile::kFloats) + threadIdx.x;
 #pragma unroll
