@@ -15,10 +15,13 @@ bool wgrad_fast(const gemm_rs_wgrad_args& g)
     return g.M > 0 && aligned(g.dy, 4) && g.dy_stride % 2 == 0 && g.N % 2 == 0 && g.dy_stride < (1 << 23);
 }
 
-// A share of a cut tile is at least this many steps of 64 tokens: shorter ones cost more
-// in starts and in joining than they spread (us with 4 / 8 / 16 / 32: 512 x 4096 x 1024
-// 28 / 14 / 14 / 14, 16384 x 256 x 128 49 / 33 / 30 / 37, 4096 x 512 x 512 27 / 23 / 24 / 34).
-constexpr int kWgMinSteps = 12;
+// A share of a cut tile is at least kWgMinSteps steps of 64 tokens (shorter ones cost more
+// in starts and in joining than they spread), and tiles are cut only if that saves more
+// than the kWgJoinSteps steps that joining takes.  Measured, us, with 6 / 8 / 12 steps:
+// 2048 x 1024 x 1024 27 / 20 / 24, 4096 x 512 x 512 23 / 21 / 24, 8192 x 1024 x 1024
+// 48 / 48 / 52, 16384 x 256 x 128 36 / 29 / 28; 1000 x 4104 x 2088 (16 steps) 47 cut and
+// 57 whole, 700 x 1000 x 1000 (11) 22 cut and 15 whole.
+constexpr int kWgMinSteps = 8, kWgJoinSteps = 6;
 
 // The 256 x 256 tile reads and turns its operands half as often for the same outputs, but
 // starts and ends slower.  Measured, us (256 / 128): 2048 x 8192 x 3584 214 / 208 (32
@@ -40,7 +43,7 @@ WgradPlan wgrad_plan(const gemm_rs_wgrad_args& g, int& big)
     p.full = (int)(all - rest);
     int64_t shares = rest * p.steps / kWgMinSteps;
     shares = shares < slots ? shares : slots;
-    if (shares <= rest) {  // nothing to gain from cutting them
+    if (shares == 0 || rest * p.steps / shares + kWgJoinSteps >= p.steps) {  // nothing to gain from cutting them
         p.full = (int)all;
         shares = 0;
     }
@@ -50,10 +53,10 @@ WgradPlan wgrad_plan(const gemm_rs_wgrad_args& g, int& big)
 }
 
 template <class A, class B>
-int launch2(void (*kernel)(A, B), dim3 grid, int lds, const A& a, const B& b, void* stream)
+int launch2(void (*kernel)(A, B), dim3 grid, int threads, int lds, const A& a, const B& b, void* stream)
 {
     void* p[] = {const_cast<A*>(&a), const_cast<B*>(&b)};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kWgThreads), p, lds,
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), p, lds,
                                          static_cast<hipStream_t>(stream));
     return e == hipSuccess ? GEMM_RS_OK : hip_fail(e, "gemm_rs_ckpt_wgrad");
 }
@@ -69,10 +72,10 @@ int wgrad_run(const WgradArgs& a, const WgradPlan& p, int device, void* stream)
         if (e != hipSuccess) return hip_fail(e, "hipFuncSetAttribute");
         allowed[device].store(true, std::memory_order_relaxed);
     }
-    int rc = launch2(wgrad_kernel<T, WN, WK>, dim3((unsigned)p.grid), kLds, a, p, stream);
+    int rc = launch2(wgrad_kernel<T, WN, WK>, dim3((unsigned)p.grid), kWgThreads, kLds, a, p, stream);
     if (rc != GEMM_RS_OK || p.shares == 0) return rc;
     const int64_t rest = (int64_t)p.tiles_n * p.tiles_k - p.full;
-    return launch2(wgrad_join_kernel<T, WN, WK>, dim3((unsigned)rest, WN), 0, a, p, stream);
+    return launch2(wgrad_join_kernel<T, WN, WK>, dim3((unsigned)rest, 4 * WN), 64, 0, a, p, stream);
 }
 
 }  // namespace
