@@ -7,17 +7,27 @@ using namespace gemm_rs_layer;
 
 namespace {
 
+// Threads per workgroup: eight columns each, 1024 for wider rows.
+int norm_threads(int n)
+{
+    return n <= 1024 ? 128 : n <= 2048 ? 256 : n <= 3072 ? 384 : n <= 4096 ? 512 : n <= 6144 ? 768 : 1024;
+}
+
 template <class T, class R, int MAXP>
 int norm_forward_sized(const NormArgs& a, void* stream)
 {
     auto go = [&](void (*k)(NormArgs), int threads) {
         return launch(k, dim3((unsigned)a.rows), threads, a, stream, "gemm_rs_block_norm");
     };
-    const int chunks = (a.n + 7) / 8;
-    if (chunks <= 256) return go(norm_forward_kernel<T, R, 256, 1, MAXP>, 256);
-    if (chunks <= 512) return go(norm_forward_kernel<T, R, 256, 2, MAXP>, 256);
-    if (chunks <= 1024) return go(norm_forward_kernel<T, R, 256, 4, MAXP>, 256);
-    return go(norm_forward_kernel<T, R, 1024, 4, MAXP>, 1024);
+    switch (norm_threads(a.n)) {
+    case 128: return go(norm_forward_kernel<T, R, 128, 1, MAXP>, 128);
+    case 256: return go(norm_forward_kernel<T, R, 256, 1, MAXP>, 256);
+    case 384: return go(norm_forward_kernel<T, R, 384, 1, MAXP>, 384);
+    case 512: return go(norm_forward_kernel<T, R, 512, 1, MAXP>, 512);
+    case 768: return go(norm_forward_kernel<T, R, 768, 1, MAXP>, 768);
+    default:
+        return a.n <= 8192 ? go(norm_forward_kernel<T, R, 1024, 1, MAXP>, 1024) : go(norm_forward_kernel<T, R, 1024, 4, MAXP>, 1024);
+    }
 }
 
 template <class T, class R>
@@ -25,9 +35,6 @@ int norm_forward(const NormArgs& a, void* stream)
 {
     return a.nparts == 1 ? norm_forward_sized<T, R, 1>(a, stream) : norm_forward_sized<T, R, 8>(a, stream);
 }
-
-// Threads per workgroup of the backward pass: eight columns each, 1024 for wider rows.
-int norm_threads(int n) { return n <= 1024 ? 128 : n <= 2048 ? 256 : n <= 4096 ? 512 : 1024; }
 
 template <class T, class R>
 int norm_backward(const NormGradArgs& a, int grid, void* stream)
@@ -41,7 +48,9 @@ int norm_backward(const NormGradArgs& a, int grid, void* stream)
     switch (threads) {
     case 128: return go(norm_backward_kernel<T, R, 128>);
     case 256: return go(norm_backward_kernel<T, R, 256>);
+    case 384: return go(norm_backward_kernel<T, R, 384>);
     case 512: return go(norm_backward_kernel<T, R, 512>);
+    case 768: return go(norm_backward_kernel<T, R, 768>);
     default: return go(norm_backward_kernel<T, R, 1024>);
     }
 }
@@ -58,18 +67,23 @@ int norm_types(const gemm_rs_norm_config& c, F f)
     }
 }
 
-// Workgroups of the backward pass, each with one row of partial sums: as many as give
-// every CU 16 waves.  Fewer leave a row's waits uncovered, more write more partial rows:
-// 4096 rows of 8192 columns 180 / 135 / 146 us with 8 / 16 / 32 waves, of 4096 columns
-// 84 / 82 / 87, of 2048 columns 34 / 32 / 40.
-int norm_groups(int n, int64_t rows)
-{
-    const int64_t most = kCus * 16 * 64 / norm_threads(n);
-    return (int)(rows < most ? rows : most);
-}
 int norm_sums(const gemm_rs_norm_config& c)
 {
     return (c.pre_norm ? 1 : 0) + (c.post_norm ? 1 : 0) + (c.gate == GEMM_RS_GATE_CHANNEL ? 1 : 0);
+}
+
+
+// Workgroups of the backward pass, each with one row of partial sums: as many as give
+// every CU 16 waves (fewer leave a row's waits uncovered, more write more partial rows:
+// 4096 rows of 8192 columns 180 / 135 / 146 us with 8 / 16 / 32 waves, of 4096 columns
+// 84 / 82 / 87, of 2048 columns 34 / 32 / 40).  With more rows than CUs a workgroup takes
+// two at least (1021 rows of 1000 columns 20 us with one, 16 with two, 16 with four; 512 rows
+// of 4096 columns 21, 18, 20; 200 rows of 256 columns 7.7, 9.2).
+int norm_groups(const gemm_rs_norm_config& c, int64_t rows)
+{
+    const int64_t most = kCus * (16 * 64 / norm_threads(c.width));
+    if (rows > kCus && norm_sums(c) > 0) rows = rows < 2 * kCus ? kCus : ceil_div(rows, 2);
+    return (int)(rows < most ? rows : most);
 }
 
 }  // namespace
@@ -149,7 +163,7 @@ int gemm_rs_block_norm(const gemm_rs_norm_config* c, int64_t rows, const gemm_rs
 size_t gemm_rs_block_norm_workspace(const gemm_rs_norm_config* c, int64_t rows)
 {
     if (gemm_rs_norm_validate(c) != GEMM_RS_OK || rows <= 0) return 0;
-    return (size_t)norm_groups(c->width, rows) * norm_sums(*c) * c->width * sizeof(float);
+    return (size_t)norm_groups(*c, rows) * norm_sums(*c) * c->width * sizeof(float);
 }
 
 int gemm_rs_block_norm_backward(const gemm_rs_norm_config* c, int64_t rows, const gemm_rs_norm_grad_args* g,
@@ -201,7 +215,7 @@ int gemm_rs_block_norm_backward(const gemm_rs_norm_config* c, int64_t rows, cons
     }
     if (k.code != GEMM_RS_OK) return k.code;
     if ((rc = check_device()) != GEMM_RS_OK) return rc;
-    const int grid = norm_groups(c->width, rows), sums = norm_sums(*c);
+    const int grid = norm_groups(*c, rows), sums = norm_sums(*c);
     if (rows > 0) {
         NormGradArgs a = {};
         a.dz = g->dz;
@@ -243,8 +257,11 @@ int gemm_rs_block_norm_backward(const gemm_rs_norm_config* c, int64_t rows, cons
     if (c->pre_norm) s.out[i++] = g->dpre_weight;
     if (c->post_norm) s.out[i++] = g->dpost_weight;
     if (channel) s.out[i++] = static_cast<float*>(g->dgate);
-    return launch(norm_sums_kernel, dim3((unsigned)ceil_div(c->width, kSumCols), (unsigned)sums), kSumCols * kSumSets, s,
-                  stream, "gemm_rs_block_norm_backward");
+    const dim3 blocks((unsigned)ceil_div(c->width, kSumCols), (unsigned)sums);
+    // a batch of loads per thread
+    if (grid <= 8 * 16)
+        return launch(norm_sums_kernel<16>, blocks, kSumCols * 16, s, stream, "gemm_rs_block_norm_backward");
+    return launch(norm_sums_kernel<32>, blocks, kSumCols * 32, s, stream, "gemm_rs_block_norm_backward");
 }
 
 }  // extern "C"

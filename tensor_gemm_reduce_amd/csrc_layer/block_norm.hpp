@@ -22,47 +22,46 @@ struct NormArgs {
 // One workgroup per row; thread t holds the chunks t, t + THREADS, ... of eight
 // columns in registers from the first load to the last store, so every input is
 // read once and every output written once.  MAXP: 1, or 8 for up to eight parts.
+// Bytes bound it from some 1000 rows (4096 x 8192, eight parts, residual and statistics in
+// 32 bits 184 us, 5.1 TB/s), one row's latency below: with one chunk per thread (ITEMS = 1)
+// all of a row's loads are on their way at once, the weights and the gate too, so that
+// nothing is waited for after a sum over the row.  1 x 8192, eight parts, takes 4.3 us so,
+// 7.0 with four chunks per thread; 4096 x 8192, one part, 93 and 102; 4096 x 256 8.4 with
+// 128 threads, 12.6 with 256.
 template <class T, class R, int THREADS, int ITEMS, int MAXP>
 __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
 {
     __shared__ float slots[2][THREADS / 64];
+    constexpr bool kEarly = ITEMS == 1;
     const int64_t row = blockIdx.x;
     const int n = a.n;
     float v[ITEMS][8];
 
-    // every part's chunk in flight at once where the registers hold them (1024
-    // threads have 128 each: one chunk's parts at a time)
-    constexpr int kAhead = THREADS < 1024 ? ITEMS : 1;
+    const R* rrow = static_cast<const R*>(a.residual) + row * a.residual_stride;
+    const bool gated = a.gate_kind == GEMM_RS_GATE_CHANNEL || a.gate_kind == GEMM_RS_GATE_FULL;
+    const T* gate = static_cast<const T*>(a.gate) + (a.gate_kind == GEMM_RS_GATE_FULL ? row * a.gate_stride : 0);
+    vec8<R> early_res = {};
+    vec8<T> early_post = {}, early_gate = {}, early_pre = {};
 #pragma unroll
-    for (int i0 = 0; i0 < ITEMS; i0 += kAhead) {
-        vec8<T> p[MAXP][kAhead];
+    for (int i = 0; i < ITEMS; ++i) {
+        const int col = (i * THREADS + (int)threadIdx.x) * 8;
+        vec8<T> p[MAXP];
 #pragma unroll
         for (int k = 0; k < MAXP; ++k)
+            if (k < a.nparts) p[k] = load8(static_cast<const T*>(a.parts[k]) + row * a.part_stride, col, n);
+        if constexpr (kEarly) {
+            if (a.residual) early_res = load8(rrow, col, n);
+            if (a.post_weight) early_post = load8(static_cast<const T*>(a.post_weight), col, n);
+            if (gated) early_gate = load8(gate, col, n);
+            if (a.pre_weight) early_pre = load8(static_cast<const T*>(a.pre_weight), col, n);
+        }
+        widen<T>(p[0], v[i]);
+#pragma unroll
+        for (int k = 1; k < MAXP; ++k)
             if (k < a.nparts) {
-                const T* src = static_cast<const T*>(a.parts[k]) + row * a.part_stride;
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) p[k][i] = load8(src, ((i0 + i) * THREADS + (int)threadIdx.x) * 8, n);
+                for (int j = 0; j < 8; ++j) v[i][j] += (float)p[k][j];
             }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            widen<T>(p[0][i], v[i0 + i]);
-#pragma unroll
-            for (int k = 1; k < MAXP; ++k)
-                if (k < a.nparts) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i0 + i][j] += (float)p[k][i][j];
-                }
-        }
-    }
-
-    const R* rrow = static_cast<const R*>(a.residual) + row * a.residual_stride;
-    vec8<R> res[kAhead];  // before the first sum over the row, with the parts
-    if (kAhead == ITEMS) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            res[i] = vec8<R>{};
-            if (a.residual) res[i] = load8(rrow, (i * THREADS + (int)threadIdx.x) * 8, n);
-        }
     }
 
     if (a.y) {
@@ -81,7 +80,8 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
         ry = 1.f / sqrtf(block_sum<THREADS>(s, slots[0]) / (float)n + a.eps);
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const vec8<T> w = load8(static_cast<const T*>(a.post_weight), (i * THREADS + (int)threadIdx.x) * 8, n);
+            const vec8<T> w = kEarly ? early_post
+                                     : load8(static_cast<const T*>(a.post_weight), (i * THREADS + (int)threadIdx.x) * 8, n);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * ry * (float)w[j];
         }
@@ -89,26 +89,22 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
 
     float row_scale = a.block_scale;
     if (a.gate_kind == GEMM_RS_GATE_TOKEN) row_scale *= (float)static_cast<const T*>(a.gate)[row];
-    const bool gated = a.gate_kind == GEMM_RS_GATE_CHANNEL || a.gate_kind == GEMM_RS_GATE_FULL;
-    const T* gate = static_cast<const T*>(a.gate) + (a.gate_kind == GEMM_RS_GATE_FULL ? row * a.gate_stride : 0);
     R* hrow = static_cast<R*>(a.h) + row * a.h_stride;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         const int col = (i * THREADS + (int)threadIdx.x) * 8;
         if (gated) {
-            const vec8<T> g = load8(gate, col, n);
+            const vec8<T> g = kEarly ? early_gate : load8(gate, col, n);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] *= (float)g[j];
         }
-        if (kAhead < ITEMS) {
-            res[0] = vec8<R>{};
-            if (a.residual) res[0] = load8(rrow, col, n);
-        }
+        vec8<R> res = early_res;
+        if (!kEarly && a.residual) res = load8(rrow, col, n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float h = row_scale * v[i][j];
-            if (a.residual) h += a.residual_scale * (float)res[kAhead == ITEMS ? i : 0][j];
+            if (a.residual) h += a.residual_scale * (float)res[j];
             v[i][j] = h;
             s += h * h;
         }
@@ -122,7 +118,7 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const int col = (i * THREADS + (int)threadIdx.x) * 8;
-            const vec8<T> w = load8(static_cast<const T*>(a.pre_weight), col, n);
+            const vec8<T> w = kEarly ? early_pre : load8(static_cast<const T*>(a.pre_weight), col, n);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rh * (float)w[j];
             store8(zrow, col, n, v[i]);
@@ -364,38 +360,37 @@ __global__ __launch_bounds__(1024) void norm_backward_wide_kernel(const NormGrad
     }
 }
 
-// Adds the workgroups' partial sums, in workgroup order within each of sixteen
-// strided sets and then over the sets.  blockIdx.y is the sum, out[] its target.
+// Adds the workgroups' partial sums, in workgroup order within each of SETS strided sets
+// and then over the sets.  blockIdx.y is the sum, out[] its target.  Latency bounds it:
+// every thread has eight loads in flight.  Measured with the gradients it ends, us (16 /
+// 32 sets): 64 groups of 8192 columns 8.4 / 8.8, 1021 of 1000 columns 12.9 / 11.2, 2000 of
+// 1000 columns 21 / 18.
 struct NormSumsArgs {
     const float* partial;
     float* out[3];
     int n, sums, groups;
 };
 
-constexpr int kSumCols = 32, kSumSets = 16;  // columns of a workgroup; sets of groups
+constexpr int kSumCols = 32;  // columns of a workgroup
 
-__global__ __launch_bounds__(kSumCols * kSumSets) void norm_sums_kernel(const NormSumsArgs a)
+template <int SETS>
+__global__ __launch_bounds__(kSumCols * SETS) void norm_sums_kernel(const NormSumsArgs a)
 {
-    __shared__ float part[kSumSets][kSumCols];
+    __shared__ float part[SETS][kSumCols];
     const int c = threadIdx.x % kSumCols, set = threadIdx.x / kSumCols;
     const int col = blockIdx.x * kSumCols + c;
     const int64_t step = (int64_t)a.sums * a.n;
     float s = 0.f;
     if (col < a.n) {
         const float* p = a.partial + set * step + (int64_t)blockIdx.y * a.n + col;
-        int g = set;
-        // eight loads in flight, added in order
-        for (; g + 7 * kSumSets < a.groups; g += 8 * kSumSets) {
+        // eight loads in flight, added in order; past the last group zeros
+        for (int g = set; g < a.groups; g += 8 * SETS) {
             float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = p[k * kSumSets * step];
+            for (int k = 0; k < 8; ++k) v[k] = g + k * SETS < a.groups ? p[k * SETS * step] : 0.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) s += v[k];
-            p += 8 * kSumSets * step;
-        }
-        for (; g < a.groups; g += kSumSets) {
-            s += *p;
-            p += kSumSets * step;
+            p += 8 * SETS * step;
         }
     }
     part[set][c] = s;
@@ -403,7 +398,7 @@ __global__ __launch_bounds__(kSumCols * kSumSets) void norm_sums_kernel(const No
     if (set == 0 && col < a.n) {
         s = 0.f;
 #pragma unroll
-        for (int k = 0; k < kSumSets; ++k) s += part[k][c];
+        for (int k = 0; k < SETS; ++k) s += part[k][c];
         a.out[blockIdx.y][col] = s;
     }
 }
