@@ -24,21 +24,23 @@ bool wgrad_fast(const gemm_rs_wgrad_args& g)
 constexpr int kWgMinSteps = 8, kWgJoinSteps = 6;
 
 // The 256 x 256 tile reads and turns its operands half as often for the same outputs, but
-// starts and ends slower.  Measured, us (256 / 128): 2048 x 8192 x 3584 214 / 208 (32
-// steps), 4096 x 8192 x 1024 86 / 93 (64), 4096 x 1280 x 8192 111 / 131, 8192 x 6144 x
-// 2048 236 / 284 (128), 32768 x 8192 x 3584 1786 / 2657; with few tiles the shares are
-// short: 16384 x 2048 x 512 (16) 63 / 72, 16384 x 256 x 128 (1) 74 / 49.
-constexpr int kWgBigSteps = 40;
+// starts and ends slower: for products of at least kWgBigSteps steps, and kWgBigWork of
+// its steps per CU.  Measured, us (256 / 128): 2048 x 8192 x 3584 214 / 208 (32 steps),
+// 2600 x 8192 x 1024 66 / 62 (41), 3000 x 8192 x 3584 260 / 274 (47), 4096 x 1280 x 8192 110 / 131 (64), 32768 x 8192 x 3584
+// 1786 / 2657 (512); 8192 x 1024 x 1024 47 / 42 (8 a CU), 5000 x 1024 x 2048 47 / 46 (10),
+// 16384 x 2048 x 512 59 / 64 (16), 4096 x 2048 x 2048 59 / 63 (16).
+constexpr int kWgBigSteps = 44, kWgBigWork = 12;
 
 WgradPlan wgrad_plan(const gemm_rs_wgrad_args& g, int& big)
 {
     auto tiles = [&](int t) { return ceil_div(g.N, t) * ceil_div(g.K, t); };
-    big = ceil_div(g.M, kWgRows) >= kWgBigSteps && tiles(256) >= 16;
+    const int64_t steps = ceil_div(g.M, kWgRows);
+    big = steps >= kWgBigSteps && tiles(256) * steps >= kWgBigWork * kCus;
     const int edge = big ? 256 : 128, slots = big ? kCus : 2 * kCus;
     WgradPlan p = {};
     p.tiles_n = (int)ceil_div(g.N, edge);
     p.tiles_k = (int)ceil_div(g.K, edge);
-    p.steps = ceil_div(g.M, kWgRows);
+    p.steps = steps;
     const int64_t all = (int64_t)p.tiles_n * p.tiles_k, rest = all % slots;
     p.full = (int)(all - rest);
     int64_t shares = rest * p.steps / kWgMinSteps;
@@ -75,7 +77,9 @@ int wgrad_run(const WgradArgs& a, const WgradPlan& p, int device, void* stream)
     int rc = launch2(wgrad_kernel<T, WN, WK>, dim3((unsigned)p.grid), kWgThreads, kLds, a, p, stream);
     if (rc != GEMM_RS_OK || p.shares == 0) return rc;
     const int64_t rest = (int64_t)p.tiles_n * p.tiles_k - p.full;
-    return launch2(wgrad_join_kernel<T, WN, WK>, dim3((unsigned)rest, 4 * WN), 64, 0, a, p, stream);
+    const dim3 grid((unsigned)rest, 4 * WN);
+    return p.shares > 6 * rest ? launch2(wgrad_join_kernel<T, WN, WK, 4>, grid, 256, 0, a, p, stream)
+                               : launch2(wgrad_join_kernel<T, WN, WK, 1>, grid, 64, 0, a, p, stream);
 }
 
 }  // namespace

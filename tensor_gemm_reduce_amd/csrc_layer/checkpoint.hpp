@@ -642,23 +642,26 @@ __global__ __launch_bounds__(kWgThreads, WN == 4 ? 1 : 2) void wgrad_kernel(cons
     }
 }
 
-// Adds the pieces of the cut tiles in token order: one wave per tile, wave of the tile's
-// workgroup and row of its blocks.  The latency of the pieces bounds it, so the next four
-// of them are on their way (one of a 256 x 256 tile, whose blocks fill the registers):
-// 16384 x 512 x 256, 21 pieces a tile, takes 31.7 us so and 32.8 with two on their way;
-// with one, and workgroups of four waves, 33.6.
-template <class T, int WN, int WK>
-__global__ __launch_bounds__(64) void wgrad_join_kernel(const WgradArgs a, const WgradPlan p)
+// Adds the pieces of the cut tiles: one workgroup per tile, wave of the tile's workgroup
+// and row of its blocks.  Its WAVES waves take equal parts of the pieces, in token order,
+// and add up in that order.  The latency of the pieces bounds it: where tiles have many,
+// four waves read them at once (16384 x 512 x 256, 32 pieces a tile: 22 us, 32 with one
+// wave); where they have few, three waves would stand idle (4096 x 1280 x 8192: 119 us,
+// 109 with one wave).
+template <class T, int WN, int WK, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void wgrad_join_kernel(const WgradArgs a, const WgradPlan p)
 {
     typedef WgradTile<WN, WK> Tile;
-    __shared__ __attribute__((aligned(16))) char lds[32 * 32 * WK * 4];
+    constexpr int kArea = 32 * 32 * WK * 4;
+    __shared__ __attribute__((aligned(16))) char lds[WAVES * kArea];
     const int t = blockIdx.x, row = blockIdx.y / 4, wave = blockIdx.y % 4;
+    const int lane = threadIdx.x & 63, part = uni(threadIdx.x >> 6);
     const int64_t first = t * p.steps, last = first + p.steps, all = ((int64_t)p.tiles_n * p.tiles_k - p.full) * p.steps;
     // from the last share that begins at or before the tile to the last that begins within it
     const int64_t s0 = ((first + 1) * p.shares + all - 1) / all - 1, s1 = (last * p.shares + all - 1) / all;
-    const f32x4* in = reinterpret_cast<const f32x4*>(p.pieces) + row * WK * 4 * kWgThreads + wave * 64 + threadIdx.x;
+    const f32x4* in = reinterpret_cast<const f32x4*>(p.pieces) + row * WK * 4 * kWgThreads + wave * 64 + lane;
     constexpr int64_t kPiece = Tile::kFloats / 4;
-    constexpr int kAhead = WK == 4 ? 1 : 4;
+    constexpr int kAhead = WK == 4 || WAVES > 1 ? 1 : 4;
     f32x4 piece[kAhead][4 * WK];
     auto load = [&](f32x4 (&v)[4 * WK], int64_t s) {
         // the tile is the second one of a share that begins before it
@@ -675,17 +678,35 @@ __global__ __launch_bounds__(64) void wgrad_join_kernel(const WgradArgs a, const
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[g / 4][4 * (g % 4) + e] += v[g][e];
     };
+    const int64_t from = s0 + (s1 - s0) * part / WAVES, to = s0 + (s1 - s0) * (part + 1) / WAVES;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-        if (s0 + i < s1) load(piece[i], s0 + i);
-    for (int64_t s = s0; s < s1; s += kAhead) {
+        if (from + i < to) load(piece[i], from + i);
+    for (int64_t s = from; s < to; s += kAhead) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (s + i < s1) {
+            if (s + i < to) {
                 add(piece[i]);
-                if (s + i + kAhead < s1) load(piece[i], s + i + kAhead);
+                if (s + i + kAhead < to) load(piece[i], s + i + kAhead);
             }
     }
+    f32x4* const mine = reinterpret_cast<f32x4*>(lds + part * kArea) + lane;
+    if (part > 0)
+#pragma unroll
+        for (int g = 0; g < 4 * WK; ++g) {
+            const f32x16& v = acc[g / 4];
+            mine[g * 64] = f32x4{v[4 * (g % 4)], v[4 * (g % 4) + 1], v[4 * (g % 4) + 2], v[4 * (g % 4) + 3]};
+        }
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int q = 1; q < WAVES; ++q)
+#pragma unroll
+        for (int g = 0; g < 4 * WK; ++g) {
+            const f32x4 v = mine[(q * 4 * WK + g) * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[g / 4][4 * (g % 4) + e] += v[e];
+        }
     int tn, tk;
     wgrad_tile(p, p.full + t, tn, tk);
     wgrad_store_rows<T, WK>(a, lds, tn * Tile::kBN + (wave >> 1) * 32 * WN + 32 * row,

@@ -122,6 +122,65 @@ def test_w4_no_rows_and_rows_split_alike():
         check_w4(layer.w4_linear(x[:M], weight), x[:M], q, s, z, 128, f"M={M}")
 
 
+# Widths that put 1000 rows through each shape of workgroup: 16 and 32 columns, then 64, 128, 192 and 256 with the rows
+# in LDS; and few rows of weights with more tiles than compute units.
+W4_WIDTHS = [250, 500, 700, 1590, 2390, 3190]
+
+
+@pytest.mark.parametrize("N", W4_WIDTHS)
+@pytest.mark.parametrize("K,group", [(2, 32), (200, 64), (384, 128), (514, 32), (1154, 64), (1408, 128)])
+@pytest.mark.parametrize("dtype,zeros", [(BF16, False), (BF16, True), (F16, False), (F16, True)])
+def test_w4_linear_many_rows(N, K, group, dtype, zeros):
+    x, q, s, z = w4_case(1000, N, K, group, dtype, zeros, seed=N + K)
+    weight = layer.w4_pack(q, s, z, group=group)
+    check_w4(layer.w4_linear(x, weight), x, q, s, z, group, f"{N}x{K}/{group}")
+
+
+@pytest.mark.parametrize("M", [1, 3, 4, 12, 30])
+@pytest.mark.parametrize("K,group", [(514, 32), (400, 64), (1152, 128)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_w4_linear_wide_weights(M, K, group, zeros):
+    x, q, s, z = w4_case(M, 4200, K, group, F16, zeros, seed=M + K)
+    check_w4(layer.w4_linear(x, layer.w4_pack(q, s, z, group=group)), x, q, s, z, group, f"{M} rows")
+
+
+@pytest.mark.parametrize("N", W4_WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_integers_are_exact_many_rows(N, dtype, group):
+    """As above: multiples of 1/2, the sums of inputs for the zero points among them."""
+    x, q, s, z = w4_case(1000, N, 640, group, dtype, True, seed=11, integer=True)
+    w, _ = ref.w4_weights(q, s, z, group)
+    got = layer.w4_linear(x, layer.w4_pack(q, s, z, group=group)).cpu()
+    assert torch.equal(got, torch.from_numpy(ref.f64(x) @ w.T).to(dtype))
+
+
+@pytest.mark.parametrize("M,N", [(1, 40), (20, 40), (70, 40)] + [(1000, N) for N in W4_WIDTHS])
+def test_w4_subnormal_inputs(M, N):
+    """Inputs of a few times 2^-24, below half precision's normal range, times scales of 2^9 .. 2^11: exact in FP32."""
+    x, q, s, z = w4_case(M, N, 256, 64, F16, True, seed=13, integer=True)
+    x, s = x * 2.0**-24, s * 2.0**10
+    w, _ = ref.w4_weights(q, s, z, 64)
+    got = layer.w4_linear(x, layer.w4_pack(q, s, z, group=64)).cpu()
+    assert torch.equal(got, torch.from_numpy(ref.f64(x) @ w.T).to(F16))
+
+
+@pytest.mark.parametrize("N", W4_WIDTHS)
+@pytest.mark.parametrize("pad,offset", [(8, 8), (3, 1)])
+def test_w4_many_rows_strides_and_special_values(N, pad, offset):
+    x, q, s, z = w4_case(1000, N, 386, 128, BF16, True, seed=3)
+    weight = layer.w4_pack(q, s, z, group=128)
+    want = layer.w4_linear(x, weight)
+    out = strided(torch.zeros((1000, N), dtype=BF16, device="cuda"), pad, offset, fill=7.0)
+    assert torch.equal(layer.w4_linear(strided(x, pad, offset), weight, out), want)
+    assert torch.all(out._base[:, :offset] == 7.0) and torch.all(out._base[:, offset + N:] == 7.0)
+    x[2, 5], x[700, 385], x[999, 0] = float("nan"), float("inf"), float("nan")
+    got = layer.w4_linear(x, weight)
+    bad = torch.zeros(1000, dtype=torch.bool, device="cuda")
+    bad[[2, 700, 999]] = True
+    assert torch.equal(got[~bad], want[~bad]) and torch.all(torch.isnan(got[bad]))
+
+
 # ---- block norm -----------------------------------------------------------------------
 
 def gate_shape(kind, S, N):
@@ -253,6 +312,20 @@ def test_block_norm_backward_shapes_and_types(S, N, dtype, rdtype):
     post, gate = [(True, "channel"), (False, "none"), (True, "full"), (True, "token"), (False, "channel")][(S + N) % 5]
     c = grad_case(S, N, dtype, rdtype, post, gate, seed=S + N)
     check_grad(run_grad(c), c)
+
+
+# Rows and widths of every count of threads; one, two and more rows per workgroup; partial rows of one batch and more.
+@pytest.mark.parametrize("S,N", [(257, 520), (511, 1025), (513, 2050), (300, 2504), (300, 4100), (1300, 5000), (5, 6144),
+                                 (2100, 1000)])
+@pytest.mark.parametrize("dtype,rdtype,post,gate", [(BF16, F32, True, "channel"), (F16, F16, False, "token"),
+                                                    (F32, F32, True, "none")])
+def test_block_norm_rows_and_widths(S, N, dtype, rdtype, post, gate):
+    c = grad_case(S, N, dtype, rdtype, post, gate, seed=S + N)
+    check_norm(run_norm(c, save=True), c)
+    got = run_grad(c)
+    check_grad(got, c)
+    again = run_grad(c)
+    assert torch.equal(got.pre_weight, again.pre_weight)
 
 
 @pytest.mark.parametrize("post", [False, True])
@@ -434,6 +507,37 @@ def test_wgrad_integers_are_exact(M, N, K, dtype):
     add = torch.randint(-50, 50, (N, K), generator=gen(1)).float().cuda()
     want, _ = wgrad_exact(dy, kept, add)
     assert torch.equal(layer.ckpt_wgrad(dy, kept, add=add).double().cpu(), torch.from_numpy(want))
+
+
+# Tiles of 128 x 128 in many pieces; tiles of 256 x 256 all cut, one whole round and a rest in few pieces, and two
+# whole rounds but for a rest too short to cut
+LONG_WGRADS = [(4100, 300, 200), (16390, 100, 60), (12300, 1030, 1000), (2840, 4104, 4130), (2850, 8190, 4090)]
+
+
+@pytest.mark.parametrize("M,N,K", LONG_WGRADS)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_wgrad_integers_are_exact_long(M, N, K, dtype):
+    """Sums of at most 72 M, multiples of 1/2: below 2^23, so exact in FP32."""
+    dy, kept = wgrad_case(M, N, K, dtype, seed=6, integer=True)
+    add = torch.randint(-50, 50, (N, K), generator=gen(1)).float().cuda()
+    v = layer.ckpt_unpack(kept).double()
+    want = dy.double().t().contiguous() @ v + add
+    assert torch.equal(layer.ckpt_wgrad(dy, kept, add=add).double(), want)
+
+
+@pytest.mark.parametrize("M,N,K", LONG_WGRADS[:3])
+def test_wgrad_long_random_and_special_values(M, N, K):
+    dy, kept = wgrad_case(M, N, K, BF16, seed=8)
+    clean = layer.ckpt_wgrad(dy, kept, dtype=F32)
+    ref.assert_close(clean, *wgrad_exact(dy, kept), -(-M // 16) + 40, "f32")
+    assert torch.equal(clean, layer.ckpt_wgrad(dy, kept, dtype=F32))
+    kept.exps[M - 3, 1] = layer.CKPT_NAN
+    dy[M // 2, 7] = float("nan")
+    got = layer.ckpt_wgrad(dy, kept, dtype=F32)
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[:, 32:64] = True
+    bad[7] = True
+    assert torch.all(torch.isnan(got[bad])) and torch.equal(got[~bad], clean[~bad])
 
 
 def test_wgrad_in_place_strides_and_no_rows():
