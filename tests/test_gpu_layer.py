@@ -165,6 +165,16 @@ def test_w4_subnormal_inputs(M, N):
     assert torch.equal(got, torch.from_numpy(ref.f64(x) @ w.T).to(F16))
 
 
+@pytest.mark.parametrize("M,N", [(1, 40), (20, 40), (70, 40), (1000, 700), (1000, 3190)])
+def test_w4_subnormal_inputs_bf16(M, N):
+    """The same in BF16, inputs of a few times 2^-133 and scales that bring the results back."""
+    x, q, s, z = w4_case(M, N, 256, 64, BF16, True, seed=13, integer=True)
+    x, s = (x.double() * 2.0**-133).to(BF16), (s.double() * 2.0**40).to(BF16)
+    w, _ = ref.w4_weights(q, s, z, 64)
+    got = layer.w4_linear(x, layer.w4_pack(q, s, z, group=64)).cpu()
+    assert torch.equal(got, torch.from_numpy(ref.f64(x) @ w.T).to(BF16))
+
+
 @pytest.mark.parametrize("N", W4_WIDTHS)
 @pytest.mark.parametrize("pad,offset", [(8, 8), (3, 1)])
 def test_w4_many_rows_strides_and_special_values(N, pad, offset):
