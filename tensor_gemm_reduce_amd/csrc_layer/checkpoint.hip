@@ -15,13 +15,29 @@ bool wgrad_fast(const gemm_rs_wgrad_args& g)
     return g.M > 0 && aligned(g.dy, 4) && g.dy_stride % 2 == 0 && g.N % 2 == 0 && g.dy_stride < (1 << 23);
 }
 
-// A share of a cut tile is at least kWgMinSteps steps of 64 tokens (shorter ones cost more
-// in starts and in joining than they spread), and tiles are cut only if that saves more
-// than the kWgJoinSteps steps that joining takes.  Measured, us, with 6 / 8 / 12 steps:
-// 2048 x 1024 x 1024 27 / 20 / 24, 4096 x 512 x 512 23 / 21 / 24, 8192 x 1024 x 1024
-// 48 / 48 / 52, 16384 x 256 x 128 36 / 29 / 28; 1000 x 4104 x 2088 (16 steps) 47 cut and
-// 57 whole, 700 x 1000 x 1000 (11) 22 cut and 15 whole.
-constexpr int kWgMinSteps = 8, kWgJoinSteps = 6;
+// A share of a cut tile is at least this many steps of 64 tokens: shorter ones cost more
+// in starts and in joining than they spread (us with 6 / 8 / 12 steps: 2048 x 1024 x 1024
+// 27 / 20 / 24, 4096 x 512 x 512 23 / 21 / 24, 16384 x 256 x 128 36 / 29 / 28).
+constexpr int kWgMinSteps = 8;
+
+// Whether cutting the tiles of the last round into shares saves time: what a step costs
+// there (small tiles: 0.8 us, 1.3 with two workgroups per CU; big ones 1.1, since fewer
+// of them run at a higher clock), against starting the join and moving a piece for every
+// tile and share.  Measured, us, cut / whole: 1000 x 8192 x 1100 39 / 39, 2000 x 6000 x 1500
+// 61 / 68, 2048 x 8192 x 3584 205 / 183, 3000 x 8192 x 3584 259 / 249, 4096 x 1280 x 8192
+// 111 / 110, 6000 x 4000 x 2000 109 / 146, 32768 x 8192 x 3584 1718 / 1766.
+bool wgrad_cut_pays(bool big, int64_t rest, int64_t shares, int64_t steps)
+{
+    if (shares <= rest) return false;
+    auto ns = [&](int64_t groups) { return big ? 1100 : groups <= kCus ? 800 : 1300; };
+    return rest * steps / shares * ns(shares) + 1500 + (rest + shares) * (big ? 62 : 35) < steps * ns(rest);
+}
+
+// Neighbouring shares of one XCD (each reads the tiles' rows of its own tokens) or of all:
+// short shares are better the first way (2048 x 1024 x 1024, 8 steps, 20 us against 24;
+// 8000 x 2300 x 2300, 40 steps, 114 / 118), long ones the second (10000 x 2000 x 3500, 69 steps,
+// 165 / 160; 16384 x 3000 x 2500, 120 steps, 314 / 263).
+constexpr int kWgDealtSteps = 48;
 
 // The 256 x 256 tile reads and turns its operands half as often for the same outputs, but
 // starts and ends slower: for products of at least kWgBigSteps steps, and kWgBigWork of
@@ -45,12 +61,13 @@ WgradPlan wgrad_plan(const gemm_rs_wgrad_args& g, int& big)
     p.full = (int)(all - rest);
     int64_t shares = rest * p.steps / kWgMinSteps;
     shares = shares < slots ? shares : slots;
-    if (shares == 0 || rest * p.steps / shares + kWgJoinSteps >= p.steps) {  // nothing to gain from cutting them
+    if (!wgrad_cut_pays(big, rest, shares, p.steps)) {
         p.full = (int)all;
         shares = 0;
     }
     p.shares = (int)shares;
     p.grid = (int)(p.full >= slots || shares >= slots ? slots : p.full > shares ? p.full : shares);
+    p.dealt = shares > 0 && (shares < p.grid || rest * p.steps / shares >= kWgDealtSteps);
     return p;
 }
 

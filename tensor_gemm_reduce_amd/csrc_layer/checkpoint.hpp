@@ -289,12 +289,13 @@ __global__ __launch_bounds__(kWgThreads) void wgrad_any_kernel(const WgradArgs a
 //     the blocks of 32 columns alike, so that a lane needs one address per 16 tokens.
 //   - A workgroup's work is a list of tiles, then a share of the tiles that do not
 //     fill the device a last time: those are cut along the tokens into equal shares
-//     (wgrad_join_kernel adds the pieces in token order).
+//     (wgrad_join_kernel adds the pieces).
 struct WgradPlan {
     int tiles_n, tiles_k;
     int full;          // tiles computed whole, tile t by workgroup t % grid
     int grid;          // workgroups
     int shares;        // workgroups that take a share of the other tiles (0: there are none)
+    int dealt;         // neighbouring shares on different XCDs
     int64_t steps;     // of 64 tokens
     float* pieces;     // [2 shares] partial tiles
 };
@@ -603,8 +604,9 @@ __global__ __launch_bounds__(kWgThreads, WN == 4 ? 1 : 2) void wgrad_kernel(cons
     typedef WgradTile<WN, WK> Tile;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const int wave = uni(threadIdx.x >> 6);
-    // workgroups are dealt to the 8 XCDs in turn: those of one XCD take neighbouring tiles
-    const int per = p.grid / 8, me = p.grid % 8 == 0 ? (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8) : (int)blockIdx.x;
+    // workgroups are dealt to the 8 XCDs in turn: those of one XCD take neighbouring tiles, but the tiles of a round
+    // that not all take part in, and shares where the plan says so, go over the XCDs in turn
+    const int id = (int)blockIdx.x, per = p.grid / 8, me = p.grid % 8 == 0 ? id % 8 * per + id / 8 : id;
     f32x16 acc[WN][WK];
     auto clear = [&]() {
 #pragma unroll
@@ -612,7 +614,9 @@ __global__ __launch_bounds__(kWgThreads, WN == 4 ? 1 : 2) void wgrad_kernel(cons
 #pragma unroll
             for (int j = 0; j < WK; ++j) acc[i][j] = f32x16{};
     };
-    for (int t = me; t < p.full; t += p.grid) {
+    for (int t0 = 0; t0 < p.full; t0 += p.grid) {
+        const int t = t0 + (t0 + p.grid <= p.full ? me : id);
+        if (t >= p.full) break;
         int tn, tk;
         wgrad_tile(p, t, tn, tk);
         clear();
@@ -623,17 +627,18 @@ __global__ __launch_bounds__(kWgThreads, WN == 4 ? 1 : 2) void wgrad_kernel(cons
                                     tk * Tile::kBK + (wave & 1) * 32 * WK, acc[i]);
         __syncthreads();
     }
-    if (me >= p.shares) return;
-    const int64_t end = wgrad_share(p, me + 1);
+    const int share = p.dealt ? id : me;
+    if (share >= p.shares) return;
+    const int64_t end = wgrad_share(p, share + 1);
     int slot = 0;
-    for (int64_t at = wgrad_share(p, me); at < end; ++slot) {
+    for (int64_t at = wgrad_share(p, share); at < end; ++slot) {
         const int64_t t = at / p.steps, stop = (t + 1) * p.steps < end ? (t + 1) * p.steps : end;
         int tn, tk;
         wgrad_tile(p, p.full + (int)t, tn, tk);
         clear();
         WgradRun<T, WN>(a, lds, tn, tk, stop - t * p.steps, acc).run(at - t * p.steps, stop - t * p.steps);
         // in the order of the registers: [block][four accumulators][thread]
-        f32x4* out = reinterpret_cast<f32x4*>(p.pieces + (int64_t)(2 * me + slot) * Tile::kFloats) + threadIdx.x;
+        f32x4* out = reinterpret_cast<f32x4*>(p.pieces + (int64_t)(2 * share + slot) * Tile::kFloats) + threadIdx.x;
 #pragma unroll
         for (int b = 0; b < Tile::kBlocks; ++b)
 #pragma unroll
