@@ -20,17 +20,29 @@ bool wgrad_fast(const gemm_rs_wgrad_args& g)
 // 27 / 20 / 24, 4096 x 512 x 512 23 / 21 / 24, 16384 x 256 x 128 36 / 29 / 28).
 constexpr int kWgMinSteps = 8;
 
-// Whether cutting the tiles of the last round into shares saves time: what a step costs
-// there (small tiles: 0.8 us, 1.3 with two workgroups per CU; big ones 1.1, since fewer
-// of them run at a higher clock), against starting the join and moving a piece for every
-// tile and share.  Measured, us, cut / whole: 1000 x 8192 x 1100 39 / 39, 2000 x 6000 x 1500
-// 61 / 68, 2048 x 8192 x 3584 205 / 183, 3000 x 8192 x 3584 259 / 249, 4096 x 1280 x 8192
-// 111 / 110, 6000 x 4000 x 2000 109 / 146, 32768 x 8192 x 3584 1718 / 1766.
-bool wgrad_cut_pays(bool big, int64_t rest, int64_t shares, int64_t steps)
+// The number of shares that the tiles of the last round are best cut into, or 0 if they are
+// better left whole: by what a step costs there (small tiles: 0.8 us, 1.3 with two
+// workgroups per CU; big ones 1.1, since fewer of them run at a higher clock), and by
+// starting the join and moving a piece for every tile and share.  Measured, us, cut / whole:
+// 1000 x 8192 x 1100 39 / 39, 2000 x 6000 x 1500 61 / 68, 2048 x 8192 x 3584 205 / 183,
+// 3000 x 8192 x 3584 259 / 249, 4096 x 1280 x 8192 111 / 110, 6000 x 4000 x 2000 109 / 146,
+// 32768 x 8192 x 3584 1718 / 1766; with 512 / 256 shares: 16384 x 700 x 300 42 / 36,
+// 3000 x 1500 x 700 33 / 29, 16384 x 512 x 512 32 / 29.
+int wgrad_shares(bool big, int64_t rest, int64_t steps)
 {
-    if (shares <= rest) return false;
     auto ns = [&](int64_t groups) { return big ? 1100 : groups <= kCus ? 800 : 1300; };
-    return rest * steps / shares * ns(shares) + 1500 + (rest + shares) * (big ? 62 : 35) < steps * ns(rest);
+    int64_t best = 0, cost = steps * ns(rest);
+    for (int64_t most = big ? kCus : 2 * kCus; most >= kCus / 2; most /= 2) {
+        int64_t shares = rest * steps / kWgMinSteps;
+        shares = shares < most ? shares : most;
+        if (shares <= rest) continue;
+        const int64_t c = rest * steps / shares * ns(shares) + 1500 + (rest + shares) * (big ? 62 : 35);
+        if (c < cost) {
+            cost = c;
+            best = shares;
+        }
+    }
+    return (int)best;
 }
 
 // Neighbouring shares of one XCD (each reads the tiles' rows of its own tokens) or of all:
@@ -59,13 +71,9 @@ WgradPlan wgrad_plan(const gemm_rs_wgrad_args& g, int& big)
     p.steps = steps;
     const int64_t all = (int64_t)p.tiles_n * p.tiles_k, rest = all % slots;
     p.full = (int)(all - rest);
-    int64_t shares = rest * p.steps / kWgMinSteps;
-    shares = shares < slots ? shares : slots;
-    if (!wgrad_cut_pays(big, rest, shares, p.steps)) {
-        p.full = (int)all;
-        shares = 0;
-    }
-    p.shares = (int)shares;
+    const int shares = wgrad_shares(big, rest, steps);
+    if (shares == 0) p.full = (int)all;
+    p.shares = shares;
     p.grid = (int)(p.full >= slots || shares >= slots ? slots : p.full > shares ? p.full : shares);
     p.dealt = shares > 0 && (shares < p.grid || rest * p.steps / shares >= kWgDealtSteps);
     return p;
