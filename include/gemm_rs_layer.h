@@ -81,7 +81,13 @@ int gemm_rs_w4_pack(const gemm_rs_w4_config *cfg, const void *q, const void *sca
                     void *packed, void *stream);
 
 /* The product, M >= 0 rows.  FP32 accumulation, one rounding to cfg->dtype.
- * An infinity in a row of x gives NaN in that row of y. */
+ * Inputs are multiplied by 16 + q, and (16 + z) times their sum taken off again:
+ *   - before its rounding a result is within (2 ceil(K / 32) + 40) 2^-24 of
+ *     sum_k |x| |s| (32 + q + z), not of sum_k |x| |s| |q - z|;
+ *   - finite inputs of any size give the formula's result, an infinity only where
+ *     that is past the type's range;
+ *   - an infinity in a row of x gives NaN in all of that row of y, since it meets
+ *     itself with the other sign. */
 int gemm_rs_w4_linear(const gemm_rs_w4_config *cfg, const void *packed, int64_t M, const void *x,
                       int64_t x_stride, void *y, int64_t y_stride, void *stream);
 

@@ -5,11 +5,18 @@
 // the waves consume them and read at full rate; from some 16 tokens on the vector
 // instructions that expand weights and apply scales do, beside the MFMAs.
 //   - A nibble becomes a 16-bit float by two bit operations per pair: placed in the
-//     mantissa of 16.0 it reads as 16 + q exactly.
-//   - The MFMA multiplies x by 16 + q; the group's FP32 accumulator starts at
-//     -(16 + z) times the sum of the group's inputs, which is taken once for every
+//     mantissa of 16 o it reads as (16 + q) o exactly, o a power of two.
+//   - The MFMA multiplies x by (16 + q) o; the group's FP32 accumulator starts at
+//     -(16 + z) o times the sum of the group's inputs, which is taken once for every
 //     column.  No weight is rounded, and none has its zero point subtracted by itself.
-//   - The group's accumulator times its scale is added to the result's (FP32).
+//   - The group's accumulator times its scale is added to the result's (FP32), which is
+//     divided by o at the end.
+//   - o is 1 in F16.  In BF16, whose inputs reach FP32's largest value, 31 x summed over
+//     a block's 128 inputs would be an infinity from |x| of some 2^116 on, over groups of
+//     32 from 2^118, even where y is small.  o = 2^-12 keeps every such sum below 2^128 for
+//     any finite x.  Nothing is lost at the other end: inputs are multiples of 2^-133, so
+//     the products are of 2^-145, which FP32 holds down to 2^-149; only the result's own
+//     sum is rounded there, by 2^-138 of y at most, a 32nd of BF16's last place.
 #pragma once
 
 #include <type_traits>
@@ -85,21 +92,24 @@ struct W4Type;
 template <>
 struct W4Type<__bf16> {
     typedef bf16x8 frag;
-    static constexpr uint32_t kMask = 0x00780078u, kMagic = 0x41804180u;  // the nibbles' places; 16.0 in both halves
+    static constexpr float kOne = 0x1p-12f;  // what a weight of 1 is multiplied as
+    static constexpr uint32_t kOnes = 0x39803980u;  // it in both halves
+    static constexpr uint32_t kMask = 0x00780078u, kMagic = 0x3B803B80u;  // the nibbles' places; 16 of it in both halves
     static constexpr bool kBf16 = true;
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
-    static __device__ __forceinline__ float add2(uint32_t v, float c)  // both halves and c
+    static __device__ __forceinline__ float add2(uint32_t v, float c)  // both halves times kOne, and c
     {
-        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v), __builtin_bit_cast(bf16x2, 0x3F803F80u), c, false);
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v), __builtin_bit_cast(bf16x2, kOnes), c, false);
     }
 };
 template <>
 struct W4Type<_Float16> {
     typedef f16x8 frag;
-    static constexpr uint32_t kMask = 0x03C003C0u, kMagic = 0x4C004C00u;
+    static constexpr float kOne = 1.f;
+    static constexpr uint32_t kOnes = 0x3C003C00u, kMask = 0x03C003C0u, kMagic = 0x4C004C00u;
     static constexpr bool kBf16 = false;
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c)
     {
@@ -107,11 +117,11 @@ struct W4Type<_Float16> {
     }
     static __device__ __forceinline__ float add2(uint32_t v, float c)
     {
-        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, v), __builtin_bit_cast(f16x2, 0x3C003C00u), c, false);
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, v), __builtin_bit_cast(f16x2, kOnes), c, false);
     }
 };
 
-// The eight weights of a word as 16 + q.  The constants sit in a scalar and a vector
+// The eight weights of a word as (16 + q) kOne.  The constants sit in a scalar and a vector
 // register: and-or takes neither as a literal, and one scalar.
 template <class T>
 __device__ __forceinline__ typename W4Type<T>::frag w4_expand(uint32_t w)
@@ -146,7 +156,7 @@ __device__ __forceinline__ i32x4 lanes_down(const i32x4& v)
     return r;
 }
 
-// What a sum of inputs is multiplied by: all of -(16 + 8) where every zero point is 8, else the sign.
+// What a sum of inputs times kOne is multiplied by: all of -(16 + 8) where every zero point is 8, else the sign.
 template <bool ZEROS>
 constexpr float w4_unit()
 {
@@ -186,7 +196,7 @@ struct W4Block {
     }
     // g[t][f] += step k (32 inputs) of the block's product with the rows x[f]; after a group's last step acc += its scale
     // times g.  The part of the zero points, -(16 + z) times the sum of a row's inputs, is where g starts: start(u, f)
-    // gives that sum of sub-block u times w4_unit.
+    // gives that sum of sub-block u times kOne w4_unit.
     template <int MF, class F>
     __device__ __forceinline__ void step(const typename W4Type<T>::frag (&x)[MF], int k, f32x4 (&g)[NT][MF],
                                          f32x4 (&acc)[NT][MF], F start) const
@@ -225,7 +235,7 @@ struct W4Block {
     template <int MF>
     __device__ __forceinline__ void multiply(const typename W4Type<T>::frag (&x)[4][MF], f32x4 (&acc)[NT][MF]) const
     {
-        const typename W4Type<T>::frag unit = w4_constant<T>(w4_unit<ZEROS>());
+        const typename W4Type<T>::frag unit = w4_constant<T>(W4Type<T>::kOne * w4_unit<ZEROS>());
         f32x4 g[NT][MF];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -351,7 +361,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(const W4Args a)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int64_t m = m0 + f * 16 + 4 * (l >> 4) + r;
-            if (m < a.M) static_cast<T*>(a.y)[m * a.y_stride + n] = (T)sum[r];
+            if (m < a.M) static_cast<T*>(a.y)[m * a.y_stride + n] = (T)(sum[r] / W4Type<T>::kOne);
         }
     }
 }
@@ -493,7 +503,7 @@ __global__ __launch_bounds__(512, 2) void w4_tile_kernel(const W4Args a)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int64_t m = m0 + f * 16 + 4 * (lane >> 4) + r;
-                if (n < a.l.N && m < a.M) static_cast<T*>(a.y)[m * a.y_stride + n] = (T)y[r];
+                if (n < a.l.N && m < a.M) static_cast<T*>(a.y)[m * a.y_stride + n] = (T)(y[r] / W4Type<T>::kOne);
             }
         }
     }

@@ -243,7 +243,10 @@ def w4_pack(q, scales, zeros=None, *, group, stream=None) -> W4Weight:
 
 
 def w4_linear(x, weight: W4Weight, out=None, *, stream=None):
-    """y = x w^T for x [M][K] (any M; made for few rows), FP32 accumulation, rounded once to x's type."""
+    """y = x w^T for x [M][K] (any M; made for few rows), FP32 accumulation, rounded once to x's type.
+
+    An infinity or a NaN in a row of x makes that row of y NaN.
+    """
     M, _ = _two(x, "x")
     N, dtype = weight.N, weight.dtype
     dev = _device(x, "x")
