@@ -23,7 +23,7 @@ import struct
 import torch
 
 from . import build as _build
-from .gemm_rs import ERR_INVALID_ARG, OK  # noqa: F401
+from .gemm_rs import ERR_INVALID_ARG, ERR_UNSUPPORTED_SHAPE, OK  # noqa: F401
 
 # ---- constants mirrored from include/gemm_rs_layer.h --------------------------
 DTYPE_BF16 = 0
@@ -223,6 +223,8 @@ def w4_pack(q, scales, zeros=None, *, group, stream=None) -> W4Weight:
     N, half = _two(q, "q")
     if scales.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"scales: expected bfloat16 or float16, got {scales.dtype}")
+    if max(N, 2 * half, abs(group)) >= 1 << 31:  # the structure would keep the low bits
+        raise GemmRSLayerError(ERR_UNSUPPORTED_SHAPE, "w4_pack")
     cfg = gemm_rs_w4_config(N, 2 * half, group, _CODES[scales.dtype], int(zeros is not None))
     L = lib()
     _check(L.gemm_rs_w4_validate(ctypes.byref(cfg)), "gemm_rs_w4_validate")
