@@ -9,7 +9,9 @@ Argument checks and marshalling only: every step runs in the HIP kernels of the
 library.  Tensors live on the current device; rows may be strided, elements of a
 row are adjacent.  Work is enqueued on ``stream`` (a torch stream or a raw
 handle; default: torch's current stream) and calls return at once; outputs
-and workspaces come from torch's allocator on that stream.
+and workspaces come from torch's allocator on that stream.  The calls record no
+history for autograd and refuse tensors that require gradients while gradients
+are enabled; inside an autograd.Function they are not.
 
 If the library is missing this module raises ImportError on first use: there is
 no fallback path.
@@ -139,6 +141,14 @@ _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_d
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
+_grad_mode = torch.is_grad_enabled  # looked up only where a tensor asks for gradients
+
+
+def _lost_gradient(name):
+    return RuntimeError(f"{name}: requires gradients, but the call records no history for autograd: pass it detached, or "
+                        "call under torch.no_grad() (as inside an autograd.Function)")
+
+
 def _device(t, name):
     """Index of the current device, which has to be t's."""
     d = t.get_device()
@@ -160,6 +170,8 @@ def _rows(t, name, rows, width, dtype, dev):
         raise ValueError(f"{name}: rows must hold their elements side by side, strides are {(s0, s1)}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, not on the current device")
+    if t.requires_grad and _grad_mode():
+        raise _lost_gradient(name)
     return s0 if rows > 1 else max(s0, width)
 
 
@@ -172,6 +184,8 @@ def _flat(t, name, shape, dtype, dev):
         raise ValueError(f"{name}: must be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, not on the current device")
+    if t.requires_grad and _grad_mode():
+        raise _lost_gradient(name)
 
 
 def _two(t, name):
@@ -321,6 +335,8 @@ def _parts(parts, dev):
         s0, s1, s2 = parts.stride()
         if s2 != 1 and N != 1 or s1 < N and S > 1:
             raise ValueError(f"parts: rows must hold their elements side by side, strides are {(s0, s1, s2)}")
+        if parts.requires_grad and _grad_mode():
+            raise _lost_gradient("parts")
         step, base = s0 * parts.element_size(), parts.data_ptr()
         return parts, S, N, range(base, base + P * step, step) if step > 0 else [base] * P, s1 if S > 1 else max(s1, N)
     if not 1 <= len(parts) <= NORM_MAX_PARTS:
