@@ -422,12 +422,14 @@ def block_norm_backward(dz, dh, h, y, rstd, *, pre_weight=None, post_weight=None
     """Gradients of block_norm's inputs from dz (None without a pre weight) and dh (None: zero).
 
     h, y, rstd: what block_norm(save=True) returned; h is only read with a pre weight, y only with a post weight or a
-    gate (either may then be None).  Every part's gradient is .y.  Weight and [N]-gate gradients are float32, sums over
+    gate (either may then be None, but dz or y is needed for the parts' type).  Every part's gradient is .y.  Weight and [N]-gate gradients are float32, sums over
     rows in a fixed order; .residual has the residual's type.
     """
     like = dz if dz is not None else y
     if like is None:
         raise ValueError("dz or y is needed")
+    if dz is not None and pre_weight is None:
+        raise ValueError("dz: needs a pre_weight")
     name = "dz" if dz is not None else "y"
     S, N = _two(like, name)
     dev = _device(like, name)

@@ -65,3 +65,14 @@ def test_inside_an_autograd_function():
     x, w = ones(4, 64).requires_grad_(), ones(8, 64).requires_grad_()
     Linear.apply(x, w).backward(ones(4, 8))
     assert torch.equal(w.grad, torch.full_like(w, 4)) and torch.equal(x.grad, torch.full_like(x, 8))
+
+
+@pytest.mark.parametrize("post", [False, True])
+def test_backward_refuses_a_gradient_of_no_output(post):
+    """Without a pre weight the forward pass has no z, so a gradient of it has nowhere to go."""
+    t = ones(2, 8)
+    kw = dict(post_weight=ones(8)) if post else {}
+    rstd = ones(2, 2, dtype=torch.float32)
+    with pytest.raises(ValueError, match="dz"):
+        layer.block_norm_backward(t, t, None, t, rstd, **kw)
+    assert torch.equal(layer.block_norm_backward(None, t, None, t, rstd, **kw).residual, t)

@@ -15,3 +15,10 @@ def test_w4_pack_refuses_sizes_past_31_bits(N, half, group):
     with pytest.raises(layer.GemmRSLayerError) as e:
         layer.w4_pack(q, scales, group=group)
     assert e.value.code in (gr.ERR_UNSUPPORTED_SHAPE, gr.ERR_INVALID_ARG)
+
+
+def test_backward_refuses_a_gradient_of_no_output():
+    """Without a pre weight the forward pass has no z, so a gradient of it has nowhere to go."""
+    t = torch.ones(2, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="dz: needs a pre_weight"):
+        layer.block_norm_backward(t, t, None, None, None)
