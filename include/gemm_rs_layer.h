@@ -171,7 +171,8 @@ typedef struct gemm_rs_norm_grad_args {
 } gemm_rs_norm_grad_args;
 
 /* Bytes of workspace the backward pass needs (16-byte aligned; its contents
- * need not be set). */
+ * need not be set): a row of FP32 sums for each of pre_norm, post_norm and a
+ * CHANNEL gate, per workgroup of rows; at most 96 MiB, 24 MiB up to 8192 columns. */
 size_t gemm_rs_block_norm_workspace(const gemm_rs_norm_config *cfg, int64_t rows);
 int gemm_rs_block_norm_backward(const gemm_rs_norm_config *cfg, int64_t rows,
                                 const gemm_rs_norm_grad_args *args, void *workspace,
@@ -215,6 +216,9 @@ typedef struct gemm_rs_wgrad_args {
     int64_t dw_stride;
 } gemm_rs_wgrad_args;
 
+/* Bytes of workspace (16-byte aligned; its contents need not be set): a 64 or
+ * 256 KiB partial tile for every share and every tile that is cut into shares;
+ * less than 64 MiB with tiles of 128 x 128, 128 MiB with tiles of 256 x 256. */
 size_t gemm_rs_ckpt_wgrad_workspace(const gemm_rs_wgrad_args *args);
 int gemm_rs_ckpt_wgrad(const gemm_rs_wgrad_args *args, void *workspace, size_t workspace_bytes,
                        void *stream);

@@ -197,7 +197,9 @@ size_t gemm_rs_ckpt_wgrad_workspace(const gemm_rs_wgrad_args* g)
     if (wgrad_check(g) != GEMM_RS_OK || !wgrad_fast(*g)) return 0;
     int big;
     const WgradPlan p = wgrad_plan(*g, big);
-    return (size_t)p.shares * 2 * (big ? WgradTile<4, 4>::kFloats : WgradTile<2, 2>::kFloats) * sizeof(float);
+    if (p.shares == 0) return 0;
+    const int64_t cut = (int64_t)p.tiles_n * p.tiles_k - p.full;
+    return (size_t)(p.shares + cut - 1) * (big ? WgradTile<4, 4>::kFloats : WgradTile<2, 2>::kFloats) * sizeof(float);
 }
 
 int gemm_rs_ckpt_wgrad(const gemm_rs_wgrad_args* g, void* workspace, size_t workspace_bytes, void* stream)

@@ -297,7 +297,7 @@ struct WgradPlan {
     int shares;        // workgroups that take a share of the other tiles (0: there are none)
     int dealt;         // neighbouring shares on different XCDs
     int64_t steps;     // of 64 tokens
-    float* pieces;     // [2 shares] partial tiles
+    float* pieces;     // [shares + cut tiles - 1] partial tiles, that of share s in cut tile t at s + t
 };
 
 // Tile t in the order of computation: groups of eight tile rows, column by column, so
@@ -630,15 +630,15 @@ __global__ __launch_bounds__(kWgThreads, WN == 4 ? 1 : 2) void wgrad_kernel(cons
     const int share = p.dealt ? id : me;
     if (share >= p.shares) return;
     const int64_t end = wgrad_share(p, share + 1);
-    int slot = 0;
-    for (int64_t at = wgrad_share(p, share); at < end; ++slot) {
+    for (int64_t at = wgrad_share(p, share); at < end;) {
         const int64_t t = at / p.steps, stop = (t + 1) * p.steps < end ? (t + 1) * p.steps : end;
         int tn, tk;
         wgrad_tile(p, p.full + (int)t, tn, tk);
         clear();
         WgradRun<T, WN>(a, lds, tn, tk, stop - t * p.steps, acc).run(at - t * p.steps, stop - t * p.steps);
-        // in the order of the registers: [block][four accumulators][thread]
-        f32x4* out = reinterpret_cast<f32x4*>(p.pieces + (int64_t)(2 * share + slot) * Tile::kFloats) + threadIdx.x;
+        // In the order of the registers: [block][four accumulators][thread].  From one piece to the next the share, the
+        // tile or both go up by one, so their sum tells pieces apart.
+        f32x4* out = reinterpret_cast<f32x4*>(p.pieces + (share + t) * Tile::kFloats) + threadIdx.x;
 #pragma unroll
         for (int b = 0; b < Tile::kBlocks; ++b)
 #pragma unroll
@@ -672,10 +672,10 @@ __global__ __launch_bounds__(64 * WAVES) void wgrad_join_kernel(const WgradArgs 
     constexpr int kAhead = WK == 4 || WAVES > 1 ? 1 : 4;
     f32x4 piece[kAhead][4 * WK];
     auto load = [&](f32x4 (&v)[4 * WK], int64_t s) {
-        // the tile is the second one of a share that begins before it
-        const f32x4* from = in + (2 * s + (s == s0 && wgrad_share(p, s) < first ? 1 : 0)) * kPiece;
+        const f32x4* from = in + (s + t) * kPiece;
 #pragma unroll
         for (int g = 0; g < 4 * WK; ++g) v[g] = from[g * kWgThreads];
+        __builtin_amdgcn_sched_barrier(0);  // all on their way before one is waited for
     };
     f32x16 acc[WK];
 #pragma unroll
