@@ -216,6 +216,23 @@ typedef struct gemm_rs_wgrad_args {
     int64_t dw_stride;
 } gemm_rs_wgrad_args;
 
+/* How gemm_rs_ckpt_wgrad splits the work of these arguments (their sizes, strides
+ * and alignment; host only).  Tiles are squares of dw; those that do not fill the
+ * device a last time may be cut along the tokens into equal shares, whose partial
+ * tiles a second kernel joins. */
+typedef struct gemm_rs_wgrad_info {
+    int32_t words;      /* dy is read in 4-byte words: even N and row stride, aligned to 4;
+                           else by elements, every tile whole                        */
+    int32_t tile;       /* edge of a tile: 128 or 256                                */
+    int32_t whole, cut; /* tiles computed by one workgroup each; tiles cut           */
+    int32_t shares;     /* the cut tiles' shares of tokens (0: none are cut)         */
+    int32_t workgroups; /* of the first kernel                                       */
+    int32_t dealt;      /* 1: neighbouring shares run on different XCDs              */
+    int32_t join_waves; /* waves per workgroup of the join (0: there is none)        */
+} gemm_rs_wgrad_info;
+
+int gemm_rs_ckpt_wgrad_plan(const gemm_rs_wgrad_args *args, gemm_rs_wgrad_info *info);
+
 /* Bytes of workspace (16-byte aligned; its contents need not be set): a 64 or
  * 256 KiB partial tile for every share and every tile that is cut into shares;
  * less than 64 MiB with tiles of 128 x 128, 128 MiB with tiles of 256 x 256. */

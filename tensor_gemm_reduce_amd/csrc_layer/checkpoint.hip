@@ -79,6 +79,11 @@ WgradPlan wgrad_plan(const gemm_rs_wgrad_args& g, int& big)
     return p;
 }
 
+int64_t wgrad_cut(const WgradPlan& p) { return (int64_t)p.tiles_n * p.tiles_k - p.full; }
+
+// Waves per workgroup of the join: by the pieces a tile has (wgrad_join_kernel).
+int wgrad_join_waves(const WgradPlan& p) { return p.shares > 6 * wgrad_cut(p) ? 4 : 1; }
+
 template <class A, class B>
 int launch2(void (*kernel)(A, B), dim3 grid, int threads, int lds, const A& a, const B& b, void* stream)
 {
@@ -101,10 +106,9 @@ int wgrad_run(const WgradArgs& a, const WgradPlan& p, int device, void* stream)
     }
     int rc = launch2(wgrad_kernel<T, WN, WK>, dim3((unsigned)p.grid), kWgThreads, kLds, a, p, stream);
     if (rc != GEMM_RS_OK || p.shares == 0) return rc;
-    const int64_t rest = (int64_t)p.tiles_n * p.tiles_k - p.full;
-    const dim3 grid((unsigned)rest, 4 * WN);
-    return p.shares > 6 * rest ? launch2(wgrad_join_kernel<T, WN, WK, 4>, grid, 256, 0, a, p, stream)
-                               : launch2(wgrad_join_kernel<T, WN, WK, 1>, grid, 64, 0, a, p, stream);
+    const dim3 grid((unsigned)wgrad_cut(p), 4 * WN);
+    return wgrad_join_waves(p) == 4 ? launch2(wgrad_join_kernel<T, WN, WK, 4>, grid, 256, 0, a, p, stream)
+                                    : launch2(wgrad_join_kernel<T, WN, WK, 1>, grid, 64, 0, a, p, stream);
 }
 
 }  // namespace
@@ -192,14 +196,29 @@ static int wgrad_check(const gemm_rs_wgrad_args* g)
     return GEMM_RS_OK;
 }
 
+int gemm_rs_ckpt_wgrad_plan(const gemm_rs_wgrad_args* g, gemm_rs_wgrad_info* info)
+{
+    const int rc = wgrad_check(g);
+    if (rc != GEMM_RS_OK) return rc;
+    if (!info) return GEMM_RS_ERR_INVALID_ARG;
+    if (!wgrad_fast(*g)) {
+        const int64_t tiles = ceil_div(g->N, kWgTile) * ceil_div(g->K, kWgTile);
+        *info = {0, kWgTile, (int32_t)tiles, 0, 0, (int32_t)tiles, 0, 0};
+        return GEMM_RS_OK;
+    }
+    int big;
+    const WgradPlan p = wgrad_plan(*g, big);
+    *info = {1, big ? 256 : 128, p.full, (int32_t)wgrad_cut(p), p.shares, p.grid, p.dealt, p.shares ? wgrad_join_waves(p) : 0};
+    return GEMM_RS_OK;
+}
+
 size_t gemm_rs_ckpt_wgrad_workspace(const gemm_rs_wgrad_args* g)
 {
     if (wgrad_check(g) != GEMM_RS_OK || !wgrad_fast(*g)) return 0;
     int big;
     const WgradPlan p = wgrad_plan(*g, big);
     if (p.shares == 0) return 0;
-    const int64_t cut = (int64_t)p.tiles_n * p.tiles_k - p.full;
-    return (size_t)(p.shares + cut - 1) * (big ? WgradTile<4, 4>::kFloats : WgradTile<2, 2>::kFloats) * sizeof(float);
+    return (size_t)(p.shares + wgrad_cut(p) - 1) * (big ? WgradTile<4, 4>::kFloats : WgradTile<2, 2>::kFloats) * sizeof(float);
 }
 
 int gemm_rs_ckpt_wgrad(const gemm_rs_wgrad_args* g, void* workspace, size_t workspace_bytes, void* stream)

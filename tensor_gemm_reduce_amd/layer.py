@@ -43,7 +43,7 @@ CKPT_NAN = 127
 EXPORTS = ("gemm_rs_layer_strerror", "gemm_rs_w4_validate", "gemm_rs_w4_packed_bytes", "gemm_rs_w4_pack",
            "gemm_rs_w4_linear", "gemm_rs_norm_validate", "gemm_rs_block_norm", "gemm_rs_block_norm_workspace",
            "gemm_rs_block_norm_backward", "gemm_rs_ckpt_pack", "gemm_rs_ckpt_unpack",
-           "gemm_rs_ckpt_wgrad_workspace", "gemm_rs_ckpt_wgrad")
+           "gemm_rs_ckpt_wgrad_plan", "gemm_rs_ckpt_wgrad_workspace", "gemm_rs_ckpt_wgrad")
 
 _CODES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
 
@@ -86,6 +86,10 @@ class gemm_rs_wgrad_args(ctypes.Structure):
                 ("dw_stride", _i64)]
 
 
+class gemm_rs_wgrad_info(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("words", "tile", "whole", "cut", "shares", "workgroups", "dealt", "join_waves")]
+
+
 _LIB = None
 
 
@@ -116,6 +120,7 @@ def lib():
         L.gemm_rs_block_norm_backward.argtypes = [norm, _i64, _vp, _vp, _size, _vp]
         L.gemm_rs_ckpt_pack.argtypes = [_i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp]
         L.gemm_rs_ckpt_unpack.argtypes = [_i32, _i64, _i64, _vp, _vp, _vp, _i64, _vp]
+        L.gemm_rs_ckpt_wgrad_plan.argtypes = [wg, ctypes.POINTER(gemm_rs_wgrad_info)]
         L.gemm_rs_ckpt_wgrad_workspace.argtypes = [wg]
         L.gemm_rs_ckpt_wgrad.argtypes = [wg, _vp, _size, _vp]
         for name in EXPORTS[1:]:

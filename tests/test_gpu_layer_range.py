@@ -8,7 +8,8 @@ import torch
 
 import layer_ref as ref
 from tensor_gemm_reduce_amd import layer
-from test_gpu_layer import BF16, F16, W4_WIDTHS, w4_case
+from test_gpu_layer import BF16, F16, F32, W4_WIDTHS, gen, w4_case, wgrad_case, wgrad_exact
+from test_layer_plan import WGRAD_PLANS
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +99,32 @@ def test_w4_rows_do_not_depend_on_the_number_of_rows():
         assert_within(got, xd[:M] @ w.T, np.abs(xd[:M]) @ terms.T, 2 * 16 + 40, f"M={M}")
         far = (got.double() - whole[:M].double()).abs().cpu().numpy()
         assert np.all(far <= 2 * ref.UNIT[F16] * np.abs(xd[:M] @ w.T) + 2.0 ** -24 + 2 * 72 * ref.U32 * (np.abs(xd[:M]) @ terms.T))
+
+
+# ---- weight gradient -----------------------------------------------------------------
+
+PLANS = [shape for shape, _ in WGRAD_PLANS]
+
+
+@pytest.mark.parametrize("M,N,K", PLANS)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_wgrad_of_every_plan(M, N, K, dtype):
+    """Integers: sums of at most 72 M, multiples of 1/2, below 2^23, so exact in FP32 whatever their order, and the only
+    rounding is the output's.  Every way the work is cut, with either output and with and without a running sum."""
+    dy, kept = wgrad_case(M, N, K, dtype, seed=M, integer=True)
+    add = torch.randint(-50, 50, (N, K), generator=gen(1)).float().cuda()
+    sums = dy.double().t().contiguous() @ layer.ckpt_unpack(kept).double()
+    for a in (None, add):
+        want = sums if a is None else sums + a
+        assert torch.equal(layer.ckpt_wgrad(dy, kept, add=a).double(), want)
+        assert torch.equal(layer.ckpt_wgrad(dy, kept, add=a, dtype=dtype), want.to(dtype))
+    main = add.clone()
+    assert torch.equal(layer.ckpt_wgrad(dy, kept, add=main, out=main).double(), sums + add)
+
+
+@pytest.mark.parametrize("M,N,K", [s for s in PLANS if s[1] * s[2] <= 1 << 21])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_wgrad_of_every_plan_random(M, N, K, dtype):
+    dy, kept = wgrad_case(M, N, K, dtype, seed=N)
+    for out in (F32, dtype):
+        assert_within(layer.ckpt_wgrad(dy, kept, dtype=out), *wgrad_exact(dy, kept), -(-M // 16) + 40, f"{out}")
