@@ -107,7 +107,9 @@ int gemm_rs_w4_linear(const gemm_rs_w4_config *cfg, const void *packed, int64_t 
  *   u = y, r_y = 1                                           without
  *   h = residual_scale residual + block_scale gate u
  *   z = h r_h pre_weight,  r_h = 1 / sqrt(mean(h^2) + eps)   with pre_norm
- * post_norm closes the block whose output is y; pre_norm opens the next one. */
+ * post_norm closes the block whose output is y; pre_norm opens the next one.
+ * The squares are FP32's too: a row whose mean square is past its range (values of
+ * some 2^64) has r = 0, a norm of 0, and changes no other row. */
 typedef struct gemm_rs_norm_config {
     int32_t width;          /* 1 .. GEMM_RS_NORM_MAX_WIDTH                       */
     int32_t dtype;          /* of parts, weights, gate, y, z: BF16, F16 or F32   */

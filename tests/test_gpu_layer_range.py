@@ -8,7 +8,8 @@ import torch
 
 import layer_ref as ref
 from tensor_gemm_reduce_amd import layer
-from test_gpu_layer import BF16, F16, F32, W4_WIDTHS, gen, w4_case, wgrad_case, wgrad_exact
+from test_gpu_layer import (BF16, F16, F32, GRAD_ROUNDINGS, NORM_ROUNDINGS, W4_WIDTHS, gen, grad_case, norm_case, run_grad,
+                            run_norm, w4_case, wgrad_case, wgrad_exact)
 from test_layer_plan import WGRAD_PLANS
 
 pytestmark = pytest.mark.gpu
@@ -128,3 +129,89 @@ def test_wgrad_of_every_plan_random(M, N, K, dtype):
     dy, kept = wgrad_case(M, N, K, dtype, seed=N)
     for out in (F32, dtype):
         assert_within(layer.ckpt_wgrad(dy, kept, dtype=out), *wgrad_exact(dy, kept), -(-M // 16) + 40, f"{out}")
+
+
+# ---- block norm -----------------------------------------------------------------------
+
+PER_ROW = ("residual", "y")
+
+
+def check_grad_rows(got, c, a=0.7, b=-0.9):
+    """As check_grad, but only what is summed over rows carries a row's roundings."""
+    want = ref.block_norm_backward(c["dz"], c["dh"], c["h"], c["y"], c["rstd"], c["pre"], c["post"], c["gate"], a, b)
+    rows = c["y"].shape[0]
+    for k, (value, mag) in want.items():
+        t = getattr(got, k)
+        summed = k not in PER_ROW and (k != "gate" or c["gate"].dim() == 1)
+        assert_within(t, value, mag, GRAD_ROUNDINGS + (rows if summed else 0), k)
+
+
+# Rows wider than a workgroup's registers, with one to three rows per workgroup (256 of them): two and four chunks of
+# columns per thread, the last one ragged or whole
+@pytest.mark.parametrize("S,N", [(600, 8200), (700, 16384), (600, 20001), (290, 32768)])
+@pytest.mark.parametrize("dtype,rdtype,post,gate", [(BF16, F32, True, "channel"), (F16, F16, False, "channel"), (F32, F32, True, "token"),
+                                                    (BF16, BF16, True, "full"), (F16, F32, False, "none")])
+def test_wide_rows_repeat(S, N, dtype, rdtype, post, gate):
+    c = grad_case(S, N, dtype, rdtype, post, gate, seed=S + N)
+    got = run_grad(c)
+    check_grad_rows(got, c)
+    again = run_grad(c)
+    for k in got.__slots__:
+        t = getattr(got, k)
+        assert t is None or torch.equal(t, getattr(again, k)), k
+
+
+@pytest.mark.parametrize("S,N", [(700, 264), (513, 2050), (1300, 1000), (64, 8192)])
+@pytest.mark.parametrize("dtype,rdtype,post,gate", [(F16, F16, True, "full"), (BF16, F32, True, "token"), (F32, F32, False, "channel")])
+def test_block_norm_rows_by_themselves(S, N, dtype, rdtype, post, gate):
+    c = grad_case(S, N, dtype, rdtype, post, gate, seed=S * N)
+    check_grad_rows(run_grad(c), c)
+
+
+def check_norm_within(out, c, a, b):
+    want = ref.block_norm(c["parts"], c["residual"], c["pre"], c["post"], c["gate"], a, b, 1e-5)
+    for k in ("y", "h", "z"):
+        assert_within(getattr(out, k), *want[k], NORM_ROUNDINGS[k], k)
+
+
+@pytest.mark.parametrize("N", [100, 2056, 8192, 9000, 20001])
+def test_block_norm_results_past_the_largest(N):
+    """A sum or a residual past half precision's range is an infinity in y or h, while z comes from the FP32 values."""
+    c = norm_case(3, 6, N, F16, F16, False, "none", seed=N)
+    c["parts"][:, 1] *= 2.0 ** 15
+    c["parts"][:, 4] *= 2.0 ** 13
+    c["residual"][2] *= 2.0 ** 14
+    out = run_norm(c, a=3.0, b=-2.0, save=True)
+    check_norm_within(out, c, 3.0, -2.0)
+    # (some inputs are infinities at the larger widths)
+    finite = torch.isfinite(c["parts"]).all(2).all(0) & torch.isfinite(c["residual"]).all(1)
+    assert torch.isinf(out.y[1]).any() and torch.isinf(out.h[2]).any() and torch.isfinite(out.z[finite]).all()
+
+
+@pytest.mark.parametrize("N", [100, 2056, 8192, 9000, 20001])
+@pytest.mark.parametrize("scale", [2.0 ** 40, 2.0 ** -40])
+def test_block_norm_small_and_large_results(N, scale):
+    """Values far from one whose squares FP32 still holds."""
+    for dtype in (BF16, F32):
+        c = norm_case(2, 5, N, dtype, F32, True, "channel", seed=N)
+        c["parts"] *= scale
+        c["residual"] *= scale
+        check_norm_within(run_norm(c, save=True), c, 0.7, -0.9)
+    c = norm_case(2, 5, N, F16, F16, False, "full", seed=N)   # results below half precision's normal range
+    c["parts"] *= 2.0 ** -13
+    c["residual"] *= 2.0 ** -14
+    check_norm_within(run_norm(c, save=True), c, 0.7, -0.9)
+
+
+@pytest.mark.parametrize("N", [72, 2056, 8192, 9000, 20001])
+def test_block_norm_rows_whose_squares_overflow(N):
+    """Statistics are FP32: a row of values from 2^64 on has a mean square of infinity, so 1 / rms is 0, its norm 0, and
+    nothing of another row changes.  h keeps the values."""
+    c = norm_case(2, 6, N, BF16, F32, False, "none", seed=N)
+    clean = run_norm(c, save=True)
+    c["residual"][3] = 2.0 ** 100
+    out = run_norm(c, save=True)
+    keep = [0, 1, 2, 4, 5]
+    assert torch.equal(out.h[keep], clean.h[keep]) and torch.equal(out.z[keep], clean.z[keep])
+    assert torch.allclose(out.h[3], torch.full_like(out.h[3], -0.9 * 2.0 ** 100), rtol=2.0 ** -22)
+    assert torch.all(out.z[3] == 0) and out.rstd[1, 3] == 0
