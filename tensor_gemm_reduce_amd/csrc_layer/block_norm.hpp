@@ -27,7 +27,9 @@ struct NormArgs {
 // all of a row's loads are on their way at once, the weights and the gate too, so that
 // nothing is waited for after a sum over the row.  1 x 8192, eight parts, takes 4.3 us so,
 // 7.0 with four chunks per thread; 4096 x 8192, one part, 93 and 102; 4096 x 256 8.4 with
-// 128 threads, 12.6 with 256.
+// 128 threads, 12.6 with 256.  Rows past 8192 columns take four chunks per thread (us, bytes
+// at 5 TB/s in brackets, BF16, one part: 1024 x 8200 40 (17), 1024 x 16384 45 (34), 1024 x
+// 32768 83 (67); 1024 x 8192 23 (17)).
 template <class T, class R, int THREADS, int ITEMS, int MAXP>
 __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
 {
@@ -313,7 +315,11 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormGradAr
 
 // Rows wider than 8 x 1024: ITEMS chunks of eight columns per thread.  The inputs are read
 // again where they are needed again, from cache, and the sums over rows are kept in the
-// workgroup's partial row.
+// workgroup's partial row.  Scratch memory bounds it: d and the chunks' inputs pass the 128
+// registers of 1024 threads (56 .. 91 of them in scratch with two chunks, 289 .. 369 with
+// four; 59% of the waves' cycles are waits).  With the sums over rows, BF16, us (bytes at 5
+// TB/s): 1024 x 8200 86 (20), 1024 x 16384 138 (40), 1024 x 20480 391 (50), 1024 x 32768 515
+// (81); 1024 x 8192, by the kernel above, 39 (20).
 template <class T, class R, int ITEMS>
 __global__ __launch_bounds__(1024) void norm_backward_wide_kernel(const NormGradArgs a)
 {

@@ -17,17 +17,19 @@ bool wgrad_fast(const gemm_rs_wgrad_args& g)
 
 // A share of a cut tile is at least this many steps of 64 tokens: shorter ones cost more
 // in starts and in joining than they spread (us with 6 / 8 / 12 steps: 2048 x 1024 x 1024
-// 27 / 20 / 24, 4096 x 512 x 512 23 / 21 / 24, 16384 x 256 x 128 36 / 29 / 28).
+// 19.9 / 19.8 / 24.3, 4096 x 512 x 512 20.2 / 19.5 / 23.4, 16384 x 256 x 128 21.8 / 19.3 /
+// 21.7, 1000 x 300 x 200 15.0 / 14.0 / 19.2).
 constexpr int kWgMinSteps = 8;
 
 // The number of shares that the tiles of the last round are best cut into, or 0 if they are
 // better left whole: by what a step costs there (small tiles: 0.8 us, 1.3 with two
 // workgroups per CU; big ones 1.1, since fewer of them run at a higher clock), and by
-// starting the join and moving a piece for every tile and share.  Measured, us, cut / whole:
-// 1000 x 8192 x 1100 39 / 39, 2000 x 6000 x 1500 61 / 68, 2048 x 8192 x 3584 205 / 183,
-// 3000 x 8192 x 3584 259 / 249, 4096 x 1280 x 8192 111 / 110, 6000 x 4000 x 2000 109 / 146,
-// 32768 x 8192 x 3584 1718 / 1766; with 512 / 256 shares: 16384 x 700 x 300 42 / 36,
-// 3000 x 1500 x 700 33 / 29, 16384 x 512 x 512 32 / 29.
+// starting the join and moving a piece for every tile and share.  Measured, us, BF16
+// results, cut / whole: 1000 x 8192 x 1100 39 / 40, 2000 x 6000 x 1500 61 / 69,
+// 2048 x 8192 x 3584 172 / 160, 3000 x 8192 x 3584 198 / 180, 4096 x 1280 x 8192 107 / 107,
+// 4096 x 8192 x 1024 85 / 105, 6000 x 4000 x 2000 112 / 146, 32768 x 8192 x 3584 1697 / 1726;
+// with 512 / 256 shares: 16384 x 700 x 300 40 / 34, 3000 x 1500 x 700 33 / 28,
+// 16384 x 512 x 512 30 / 27.
 int wgrad_shares(bool big, int64_t rest, int64_t steps)
 {
     auto ns = [&](int64_t groups) { return big ? 1100 : groups <= kCus ? 800 : 1300; };
@@ -46,17 +48,26 @@ int wgrad_shares(bool big, int64_t rest, int64_t steps)
 }
 
 // Neighbouring shares of one XCD (each reads the tiles' rows of its own tokens) or of all:
-// short shares are better the first way (2048 x 1024 x 1024, 8 steps, 20 us against 24;
-// 8000 x 2300 x 2300, 40 steps, 114 / 118), long ones the second (10000 x 2000 x 3500, 69 steps,
-// 165 / 160; 16384 x 3000 x 2500, 120 steps, 314 / 263).
+// short shares are mostly better the first way (us, first / second: 2048 x 1024 x 1024,
+// 8 steps, 19.8 / 23.4; 8000 x 2300 x 2300, 40 steps, 113 / 118; but 3000 x 1500 x 700,
+// 13 steps, 28.8 / 27.1, and 12300 x 1030 x 1000, 15 steps, 61.5 / 58.5), long ones the
+// second (10000 x 2000 x 3500, 69 steps, 167 / 158; 16384 x 3000 x 2500, 120 steps, 313 / 261).
 constexpr int kWgDealtSteps = 48;
 
 // The 256 x 256 tile reads and turns its operands half as often for the same outputs, but
 // starts and ends slower: for products of at least kWgBigSteps steps, and kWgBigWork of
-// its steps per CU.  Measured, us (256 / 128): 2048 x 8192 x 3584 214 / 208 (32 steps),
-// 2600 x 8192 x 1024 66 / 62 (41), 3000 x 8192 x 3584 260 / 274 (47), 4096 x 1280 x 8192 110 / 131 (64), 32768 x 8192 x 3584
-// 1786 / 2657 (512); 8192 x 1024 x 1024 47 / 42 (8 a CU), 5000 x 1024 x 2048 47 / 46 (10),
-// 16384 x 2048 x 512 59 / 64 (16), 4096 x 2048 x 2048 59 / 63 (16).
+// its steps per CU.  Where the two meet depends on how the tiles fill the CUs and on the
+// bytes of a result; the thresholds are those from which the big tile is at most some 8%
+// behind with either result.  Measured, us (256 / 128), FP32 results added to a running sum:
+// 2048 x 8192 x 3584 194 / 187 (32 steps), 2560 x 8192 x 3584 228 / 228 (40),
+// 3008 x 8192 x 3584 257 / 265 (47), 3008 x 8192 x 1024 77 / 74, 3008 x 2048 x 3584 78 / 73,
+// 4096 x 7168 x 1280 112 / 112 (64), 10000 x 8192 x 3584 592 / 754 (157); BF16 results:
+// 2560 x 8192 x 1024 72 / 61 (40), 3008 x 8192 x 1024 71 / 69, 4096 x 1280 x 8192 105 / 117,
+// 32768 x 8192 x 3584 1700 / 2556 (512); 8192 x 1024 x 1024 46 / 40 (8 a CU), 5000 x 1024 x
+// 2048 47 / 45 (10), 16384 x 2048 x 512 58 / 61 (16), 3500 x 3000 x 1500 66 / 86 (16).
+// What that gives away: with BF16 results, tiles that leave few CUs idle in their last round
+// are faster big from 12 or 16 steps on (1024 x 8192 x 2048, 256 tiles, 43 / 53; 2560 x 8192 x
+// 2048 85 / 116; 2048 x 6144 x 2048, 192 tiles, 62 / 72; 2048 x 8192 x 3584, 448, 130 / 161).
 constexpr int kWgBigSteps = 44, kWgBigWork = 12;
 
 WgradPlan wgrad_plan(const gemm_rs_wgrad_args& g, int& big)

@@ -208,7 +208,10 @@ constexpr int kWgThreads = 256;
 // 128 x 128 outputs per workgroup, four waves of 64 x 64, 32 tokens a step.  Both operands
 // are token-major in memory, the MFMA wants eight tokens of a column in a lane: the tiles
 // go into LDS as they are and are read transposed.  The checkpoint is expanded to T between
-// its load and LDS.  4096 x 4096 x 1024 takes 127 us, 57 with the kernel below.
+// its load and LDS.  An odd N or row stride leaves every other row off the words, so rows
+// are loaded at two-byte alignment, and no tile is cut: 4096 x 4095 x 1024 takes 360 us (65
+// with 4096 columns and the kernel below), 512 x 8191 x 1024 55 (21), and 16384 x 511 x 256,
+// eight workgroups, 1404 (23).
 constexpr int kWgTile = 128, kWgStep = 32;
 constexpr int kWgPitch = kWgTile * 2 + 64;  // rows 16 banks apart: the four rows of a transposed read differ
 
@@ -654,8 +657,9 @@ __global__ __launch_bounds__(kWgThreads, WN == 4 ? 1 : 2) void wgrad_kernel(cons
 // and row of its blocks.  Its WAVES waves take equal parts of the pieces, in token order,
 // and add up in that order.  The latency of the pieces bounds it: where tiles have many,
 // four waves read them at once (16384 x 512 x 256, 32 pieces a tile: 22 us, 32 with one
-// wave); where they have few, three waves would stand idle (4096 x 1280 x 8192: 119 us,
-// 109 with one wave).
+// wave; 4100 x 300 x 200, 8 pieces: 16.9, 18.5); where they have few, three waves would stand
+// idle (6000 x 4000 x 2000, 2 pieces: 121 us, 111 with one wave; 4096 x 4096 x 1024, 4 pieces:
+// 61, 58).
 template <class T, int WN, int WK, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void wgrad_join_kernel(const WgradArgs a, const WgradPlan p)
 {

@@ -67,10 +67,15 @@ int w4_tile_launch(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
 //
 // More rows: whichever of six kernels costs least, as rounds of workgroups over the CUs
 // times a round's cost.  A round takes a time that grows with the columns per workgroup,
-// though not from zero (all run the whole of K).  Measured at K = 8192, us for groups of
-// 128 and of 32: the kernel above with 64 rows and 16 columns 19, 20; with 32 columns 29,
-// 37; the kernel whose workgroups keep 64 rows in LDS with 64 columns 36, 40; 128: 44, 52;
-// 192: 55, 68; 256: 66, 84.
+// though not from zero (all run the whole of K).  Measured at K = 8192 with 64 rows, us for
+// groups of 128 and of 32: the kernel above with 16 columns 19, 20; with 32 columns 29, 37;
+// the kernel whose workgroups keep 64 rows in LDS with 64 columns 36, 40; 128: 44, 52; 192:
+// 55, 68; 256: 66, 84.  The table has no entry for the group, zero points or K, which move
+// the six alike: with 2048 rows 42, 43, 38, 50, 62, 76 for groups of 128, 42, 45, 42, 55, 74,
+// 88 for groups of 32, 48, 57, 56, 78, 99, 132 with zero points too, and 16, 21, 15, 22, 29,
+// 40 at K = 2048.  It takes the fastest of the six, or one within 2%, for 500 x 7168 x 8192,
+// 500 x 6144 x 2048 and 2000 x 8192 x 3584 with groups of 128, of 32, and of 64 and 32 with
+// zero points: 500 x 7168 x 8192, groups of 32 with zero points, 192 / 256 columns 196 / 139.
 template <class T>
 int w4_run(const gemm_rs_w4_config& c, const W4Args& a, void* stream)
 {

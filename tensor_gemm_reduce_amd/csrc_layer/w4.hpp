@@ -372,9 +372,14 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(const W4Args a)
 // registers; each wave expands its own weights, once for its 64 rows.  Whoever writes a
 // row's inputs also sums them for the zero points: sums by MFMA, as the kernel above takes
 // them, would repeat in every wave and cost 1 / NT of the product.
-// Vector instructions bound it, above all the scales' multiply-add per output and group:
-// 7168 x 8192, 500 rows, 71 us (823 TFLOP/s) with groups of 128 and 90 with groups of 32;
-// 6144 x 2048, 500 rows, groups of 32, 22.6 us (557 TFLOP/s).
+// MFMAs and vector instructions bound it together: two waves share a SIMD, and a pair of
+// tiles is scaled right behind its MFMAs, so that the two kinds run after each other more
+// than side by side.  7168 x 8192, 500 rows: 71 us (823 TFLOP/s) with groups of 128, when
+// MFMAs take 42% of the busy cycles and the rest of the vector instructions 41%; 87 with
+// groups of 32 (34% and 60%: four times the scales' multiply-adds); 139 with groups of 32 and
+// zero points (21% and 62%: a multiply per start of a group as well, and NT = 4 keeps 32
+// registers in scratch; 15 with groups of 64).  6144 x 2048, 500 rows, groups of 32: 22.8 us
+// (552 TFLOP/s; 25% and 50%).
 constexpr int kW4Rows = 64;
 
 // Adds another lane's value, within 16 lanes.
