@@ -9,7 +9,8 @@ The C ABI is ``include/gemm_rs.h`` (``libgemm_rs.so``); ``gemm_rs`` is its
 ctypes binding.  The operators around that layer (4-bit weights for decode, the
 norms, gate and residual after it with their gradients, 8-bit checkpoints and the
 weight gradient) are in ``layer`` (``include/gemm_rs_layer.h``,
-``libgemm_rs_layer.so``).
+``libgemm_rs_layer.so``); the router, the experts' products and the 8-bit
+floating-point product in ``experts`` (``include/gemm_rs_experts.h``, the same library).
 """
 from .gemm_rs import (  # noqa: F401
     GemmRS, GemmRSError, gemm_rs_config, gemm_rs_info, make_config,

@@ -33,7 +33,7 @@ def sources():
 
 
 def layer_sources():
-    return [os.path.join(CSRC_LAYER, n) for n in ("w4.hip", "block_norm.hip", "checkpoint.hip")]
+    return [os.path.join(CSRC_LAYER, n) for n in ("w4.hip", "block_norm.hip", "checkpoint.hip", "route.hip", "fp8.hip")]
 
 
 def compile_flags(csrc=CSRC):

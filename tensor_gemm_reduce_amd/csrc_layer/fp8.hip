@@ -1,0 +1,376 @@
+// fp8.hip -- C entry points of the 8-bit floating-point matrices and their products
+// (gemm_rs_experts.h).
+#include "host.hpp"
+
+#include "gemm_rs_experts.h"
+#include "fp8.hpp"
+
+using namespace gemm_rs_layer;
+
+namespace {
+
+constexpr int64_t kMaxWidth = 1 << 22;
+constexpr int64_t kMaxResource = (int64_t(1) << 31) - 1;  // bytes of a buffer resource below kOob
+
+int64_t blocks_of(int64_t n) { return ceil_div(n, kFp8Block); }
+int64_t pitch_of(int64_t rows) { return ceil_div(rows + 3, 4) * 4; }  // bytes from a block's scales to the next one's
+int64_t scale_bytes(int64_t rows, int64_t cols) { return pitch_of(rows) * blocks_of(cols); }
+int64_t up16(int64_t n) { return ceil_div(n, 16) * 16; }
+bool is_float(int dtype) { return dtype >= GEMM_RS_DTYPE_BF16 && dtype <= GEMM_RS_DTYPE_F32; }
+
+template <class A>
+using Kernel = void (*)(A);
+
+template <class A>
+Kernel<A> pick(int dtype, Kernel<A> bf16, Kernel<A> f16, Kernel<A> f32)
+{
+    return dtype == GEMM_RS_DTYPE_BF16 ? bf16 : dtype == GEMM_RS_DTYPE_F16 ? f16 : f32;
+}
+
+int quant_rows(int dtype, int64_t M, int64_t K, const void* x, int64_t stride, void* q, void* s, void* stream)
+{
+    Fp8QuantArgs a = {};
+    a.x = x;
+    a.q = static_cast<uint8_t*>(q);
+    a.s = static_cast<uint8_t*>(s);
+    a.M = M;
+    a.stride = stride;
+    a.K = (int)K;
+    a.blocks = (int)blocks_of(K);
+    a.pitch = (int)pitch_of(M);
+    a.q_pitch = a.blocks * kFp8Block;
+    return launch(pick(dtype, fp8_quant_kernel<__bf16>, fp8_quant_kernel<_Float16>, fp8_quant_kernel<float>),
+                  dim3((unsigned)ceil_div(ceil_div(M, 16) * a.blocks, 4)), 256, a, stream, "gemm_rs_fp8_quant");
+}
+
+// blocks: of 128 rows of x, those of all experts where there are any
+int quant_columns(int dtype, int64_t M, int64_t K, int64_t x_rows, const void* x, int64_t stride, const int32_t* offsets,
+                  const int32_t* tokens, int64_t E, int64_t blocks, void* q, void* s, void* stream)
+{
+    Fp8QuantArgs a = {};
+    a.x = x;
+    a.q = static_cast<uint8_t*>(q);
+    a.s = static_cast<uint8_t*>(s);
+    a.M = M;
+    a.stride = stride;
+    a.K = (int)K;
+    a.pitch = (int)pitch_of(K);
+    a.q_pitch = blocks * kFp8Block;
+    a.offsets = offsets;
+    a.tokens = tokens;
+    a.E = (int)E;
+    a.x_rows = x_rows;
+    return launch(pick(dtype, fp8_quant_t_kernel<__bf16>, fp8_quant_t_kernel<_Float16>, fp8_quant_t_kernel<float>),
+                  dim3((unsigned)blocks, (unsigned)ceil_div(K, 64)), 256, a, stream, "gemm_rs_fp8_quant_transposed");
+}
+
+int quant_check(int32_t dtype, int64_t M, int64_t K, const void* x, int64_t stride, const void* q, const void* s)
+{
+    if (!is_float(dtype) || M < 0 || K < 1) return GEMM_RS_ERR_INVALID_ARG;
+    if (M >= kMaxRows || K > kMaxWidth || ceil_div(M, 16) * blocks_of(K) > kMaxThreads / 64 - 4) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return GEMM_RS_OK;
+    Checker c;
+    c.need(x, elem_bytes(dtype));
+    c.stride(stride, K);
+    c.need(q, 16);
+    c.need(s, 16);
+    return c.code;
+}
+
+// A workgroup's LDS past 64 KB, allowed once per device.
+template <class K>
+int allow_lds(K kernel, int bytes, int device, std::atomic<bool>* allowed)
+{
+    if (allowed[device].load(std::memory_order_relaxed)) return GEMM_RS_OK;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return hip_fail(e, "hipFuncSetAttribute");
+    allowed[device].store(true, std::memory_order_relaxed);
+    return GEMM_RS_OK;
+}
+
+template <int W, int MODE, class T>
+int tile_launch(Fp8Args& a, int device, void* stream)
+{
+    constexpr int kRows = Fp8Tile<W>::kRows, kLds = Fp8Tile<W>::kLds;
+    static std::atomic<bool> allowed[kMaxDevices];
+    const int rc = allow_lds(fp8_kernel<W, MODE, T>, kLds, device, allowed);
+    if (rc != GEMM_RS_OK) return rc;
+    a.tiles_n = (int)ceil_div(a.N, kRows);
+    int64_t tiles = ceil_div(a.M, kRows);
+    if (MODE == kByExpert || MODE == kGather) tiles = a.M / kRows + (a.E < a.M ? a.E : a.M);  // at most one ragged tile an expert
+    a.tiles_m = (int)tiles;
+    tiles *= a.tiles_n;
+    if (MODE == kSums) tiles *= a.E;
+    if (tiles * 256 > kMaxThreads) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    void* p[] = {&a};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fp8_kernel<W, MODE, T>), dim3((unsigned)tiles), dim3(256), p,
+                                         kLds, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? GEMM_RS_OK : hip_fail(e, "fp8_kernel");
+}
+
+template <int MF, int MODE, class T>
+int few_launch(const Fp8Args& a, void* stream)
+{
+    constexpr int kWaves = 8;
+    int64_t tiles = ceil_div(a.M, 16 * MF);
+    if (MODE != kDense) tiles = a.M / (16 * MF) + (a.E < a.M ? a.E : a.M);
+    return launch(fp8_few_kernel<kWaves, MF, MODE, T>, dim3((unsigned)ceil_div(a.N, kFewTile), (unsigned)tiles), 64 * kWaves, a,
+                  stream, "fp8_few_kernel");
+}
+
+template <int MODE, class T>
+int product(Fp8Args& a, int device, void* stream)
+{
+    if constexpr (MODE != kSums) {
+        const int64_t rows = MODE == kDense ? a.M : ceil_div(a.M, a.E);  // of an expert, if all have as many
+        if (rows <= 16) return few_launch<1, MODE, T>(a, stream);
+        if (rows <= 32) return few_launch<2, MODE, T>(a, stream);
+        if (rows <= 64) return few_launch<4, MODE, T>(a, stream);
+    }
+    const int64_t tiles = ceil_div(a.M, 256) * ceil_div(a.N, 256) * (MODE == kSums ? a.E : 1);
+    return tiles >= kCus ? tile_launch<4, MODE, T>(a, device, stream) : tile_launch<2, MODE, T>(a, device, stream);
+}
+
+template <int MODE>
+int product_of(int out_dtype, Fp8Args& a, int device, void* stream)
+{
+    return out_dtype == GEMM_RS_DTYPE_BF16  ? product<MODE, __bf16>(a, device, stream)
+           : out_dtype == GEMM_RS_DTYPE_F16 ? product<MODE, _Float16>(a, device, stream)
+                                            : product<MODE, float>(a, device, stream);
+}
+
+bool fp8_args_ok(const gemm_rs_fp8_args* g)
+{
+    return g && (is_float(g->x_dtype) || g->x_dtype == GEMM_RS_DTYPE_FP8) && is_float(g->out_dtype) && g->M >= 0 && g->N >= 1 &&
+           g->K >= 1 && g->x_rows >= 0 && g->E >= 0;
+}
+
+// q and scales of x in the workspace
+size_t quant_bytes(int64_t rows, int64_t K) { return (size_t)(up16(rows * blocks_of(K) * kFp8Block) + up16(scale_bytes(rows, K))); }
+
+int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!fp8_args_ok(g)) return GEMM_RS_ERR_INVALID_ARG;
+    if (experts ? g->E < 1 || !g->offsets : g->E != 0 || g->offsets || g->tokens) return GEMM_RS_ERR_INVALID_ARG;
+    if (!g->tokens && g->x_rows != g->M) return GEMM_RS_ERR_INVALID_ARG;
+    const int64_t blocks = blocks_of(g->K), pitch = blocks * kFp8Block;
+    if (g->M >= kMaxRows || g->x_rows >= kMaxRows || g->N > kMaxWidth || g->K > kMaxWidth || g->E > (1 << 20) ||
+        scale_bytes(g->x_rows, g->K) > kMaxResource || scale_bytes(g->N, g->K) > kMaxResource ||
+        (g->tokens && g->x_rows * pitch > kMaxResource) || g->M / 16 + g->E > 65535 * 16)
+        return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (g->M == 0) return GEMM_RS_OK;
+    const bool raw = g->x_dtype != GEMM_RS_DTYPE_FP8;
+    Checker c;
+    if (g->x_rows > 0) {
+        c.need(g->x, raw ? elem_bytes(g->x_dtype) : 16);
+        if (raw) c.stride(g->x_stride, g->K);
+        else c.need(g->x_scales, 16);
+    }
+    c.need(g->w, 16);
+    c.need(g->w_scales, 16);
+    c.maybe(g->offsets, 4);
+    c.maybe(g->tokens, 4);
+    c.maybe(g->add, 4);
+    if (g->add) c.stride(g->add_stride, g->N);
+    c.need(g->out, elem_bytes(g->out_dtype));
+    c.stride(g->out_stride, g->N);
+    if (g->add && g->add == g->out && (g->out_dtype != GEMM_RS_DTYPE_F32 || g->add_stride != g->out_stride))
+        c.fail(GEMM_RS_ERR_INVALID_ARG);
+    const size_t ws = gemm_rs_fp8_workspace(g);
+    if (ws > 0) {
+        if (!workspace || workspace_bytes < ws) c.fail(GEMM_RS_ERR_SCRATCH);
+        else c.need(workspace, 16);
+    }
+    if (c.code != GEMM_RS_OK) return c.code;
+    int device = 0, rc = check_device(&device);
+    if (rc != GEMM_RS_OK) return rc;
+    if (g->x_rows == 0) return GEMM_RS_OK;  // no row can have an input
+    Fp8Args a = {};
+    a.x = static_cast<const uint8_t*>(g->x);
+    a.xs = static_cast<const uint8_t*>(g->x_scales);
+    if (raw) {
+        rc = quant_check(g->x_dtype, g->x_rows, g->K, g->x, g->x_stride, workspace, workspace);
+        if (rc != GEMM_RS_OK) return rc;
+        uint8_t* q = static_cast<uint8_t*>(workspace);
+        uint8_t* s = q + up16(g->x_rows * pitch);
+        rc = quant_rows(g->x_dtype, g->x_rows, g->K, g->x, g->x_stride, q, s, stream);
+        if (rc != GEMM_RS_OK) return rc;
+        a.x = q;
+        a.xs = s;
+    }
+    a.w = static_cast<const uint8_t*>(g->w);
+    a.ws = static_cast<const uint8_t*>(g->w_scales);
+    a.offsets = g->offsets;
+    a.tokens = g->tokens;
+    a.add = g->add;
+    a.out = g->out;
+    a.M = g->M;
+    a.x_rows = g->x_rows;
+    a.x_pitch = a.w_pitch = pitch;
+    a.w_expert = g->N * pitch;
+    a.ws_expert = scale_bytes(g->N, g->K);
+    a.add_stride = g->add_stride;
+    a.out_stride = g->out_stride;
+    a.xs_bytes = scale_bytes(g->x_rows, g->K);
+    a.ws_bytes = a.ws_expert;
+    a.N = (int)g->N;
+    a.E = (int)g->E;
+    a.steps = (int)blocks;
+    a.xs_pitch = (int)pitch_of(g->x_rows);
+    a.ws_pitch = (int)pitch_of(g->N);
+    if (!experts) return product_of<kDense>(g->out_dtype, a, device, stream);
+    return g->tokens ? product_of<kGather>(g->out_dtype, a, device, stream) : product_of<kByExpert>(g->out_dtype, a, device, stream);
+}
+
+bool wgrad_ok(const gemm_rs_experts_wgrad_args* g)
+{
+    return g && is_float(g->dtype) && (g->out_dtype == g->dtype || g->out_dtype == GEMM_RS_DTYPE_F32) && g->M >= 0 && g->N >= 1 &&
+           g->K >= 1 && g->E >= 1 && g->x_rows >= 0;
+}
+
+// Blocks of 128 rows that the experts' rows make at most.
+int64_t wgrad_blocks(const gemm_rs_experts_wgrad_args& g) { return g.M / kFp8Block + (g.E < g.M ? g.E : g.M); }
+
+bool wgrad_fits(const gemm_rs_experts_wgrad_args& g)
+{
+    return g.M < kMaxRows && g.x_rows < kMaxRows && g.N <= kMaxWidth && g.K <= kMaxWidth && g.E <= (1 << 20) &&
+           wgrad_blocks(g) * kFp8Block <= kMaxResource / 256 && pitch_of(g.N) * wgrad_blocks(g) <= kMaxResource &&
+           pitch_of(g.K) * wgrad_blocks(g) <= kMaxResource && ceil_div(g.N, 64) <= 65535 && ceil_div(g.K, 64) <= 65535;
+}
+
+int64_t wgrad_operand(int64_t rows, int64_t blocks) { return up16(rows * blocks * kFp8Block) + up16(pitch_of(rows) * blocks); }
+
+}  // namespace
+
+extern "C" {
+
+int gemm_rs_fp8_quant(int32_t dtype, int64_t M, int64_t K, const void* x, int64_t x_stride, void* q, void* scales, void* stream)
+{
+    int rc = quant_check(dtype, M, K, x, x_stride, q, scales);
+    if (rc != GEMM_RS_OK || M == 0) return rc;
+    if ((rc = check_device()) != GEMM_RS_OK) return rc;
+    return quant_rows(dtype, M, K, x, x_stride, q, scales, stream);
+}
+
+int gemm_rs_fp8_quant_transposed(int32_t dtype, int64_t M, int64_t K, const void* x, int64_t x_stride, void* q, void* scales,
+                                 void* stream)
+{
+    int rc = quant_check(dtype, M, K, x, x_stride, q, scales);
+    if (rc != GEMM_RS_OK || M == 0) return rc;
+    if (ceil_div(K, 64) > 65535) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if ((rc = check_device()) != GEMM_RS_OK) return rc;
+    return quant_columns(dtype, M, K, M, x, x_stride, nullptr, nullptr, 0, blocks_of(M), q, scales, stream);
+}
+
+int gemm_rs_fp8_pack(int32_t dtype, int64_t E, int64_t N, int64_t K, int32_t transpose, const void* w, void* q, void* scales,
+                     void* stream)
+{
+    if (!is_float(dtype) || E < 1 || N < 1 || K < 1 || (transpose != 0 && transpose != 1)) return GEMM_RS_ERR_INVALID_ARG;
+    if (E > 65535 || N > kMaxWidth || K > kMaxWidth) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    Checker c;
+    c.need(w, elem_bytes(dtype));
+    c.need(q, 16);
+    c.need(scales, 16);
+    if (c.code != GEMM_RS_OK) return c.code;
+    const int rc = check_device();
+    if (rc != GEMM_RS_OK) return rc;
+    Fp8PackArgs a = {};
+    const int64_t rows = transpose ? K : N, cols = transpose ? N : K;
+    a.w = w;
+    a.q = static_cast<uint8_t*>(q);
+    a.s = static_cast<uint8_t*>(scales);
+    a.N = (int)N;
+    a.K = (int)K;
+    a.transpose = transpose;
+    a.w_expert = N * K;
+    a.q_pitch = blocks_of(cols) * kFp8Block;
+    a.q_expert = rows * a.q_pitch;
+    a.s_expert = scale_bytes(rows, cols);
+    a.pitch = (int)pitch_of(rows);
+    return launch(pick(dtype, fp8_pack_kernel<__bf16>, fp8_pack_kernel<_Float16>, fp8_pack_kernel<float>),
+                  dim3((unsigned)blocks_of(K), (unsigned)blocks_of(N), (unsigned)E), 256, a, stream, "gemm_rs_fp8_pack");
+}
+
+size_t gemm_rs_fp8_workspace(const gemm_rs_fp8_args* g)
+{
+    if (!fp8_args_ok(g) || g->M == 0 || g->x_dtype == GEMM_RS_DTYPE_FP8 || g->x_rows >= kMaxRows || g->K > kMaxWidth) return 0;
+    return quant_bytes(g->x_rows, g->K);
+}
+
+int gemm_rs_fp8_linear(const gemm_rs_fp8_args* g, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return fp8_product(g, false, workspace, workspace_bytes, stream);
+}
+
+int gemm_rs_experts_linear(const gemm_rs_fp8_args* g, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return fp8_product(g, true, workspace, workspace_bytes, stream);
+}
+
+size_t gemm_rs_experts_wgrad_workspace(const gemm_rs_experts_wgrad_args* g)
+{
+    if (!wgrad_ok(g) || !wgrad_fits(*g) || g->M == 0 || g->x_rows == 0) return 0;
+    const int64_t blocks = wgrad_blocks(*g);
+    return (size_t)(wgrad_operand(g->N, blocks) + wgrad_operand(g->K, blocks));
+}
+
+int gemm_rs_experts_wgrad(const gemm_rs_experts_wgrad_args* g, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!wgrad_ok(g) || (!g->tokens && g->x_rows != g->M)) return GEMM_RS_ERR_INVALID_ARG;
+    if (!wgrad_fits(*g)) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    const bool any = g->M > 0 && g->x_rows > 0;
+    Checker c;
+    c.need(g->offsets, 4);
+    c.maybe(g->tokens, 4);
+    if (any) {
+        c.need(g->dy, elem_bytes(g->dtype));
+        c.stride(g->dy_stride, g->N);
+        c.need(g->x, elem_bytes(g->dtype));
+        c.stride(g->x_stride, g->K);
+    }
+    c.maybe(g->add, 4);
+    c.need(g->dw, elem_bytes(g->out_dtype));
+    if (g->add && g->add == g->dw && g->out_dtype != GEMM_RS_DTYPE_F32) c.fail(GEMM_RS_ERR_INVALID_ARG);
+    const size_t need = gemm_rs_experts_wgrad_workspace(g);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) c.fail(GEMM_RS_ERR_SCRATCH);
+        else c.need(workspace, 16);
+    }
+    if (c.code != GEMM_RS_OK) return c.code;
+    int device = 0, rc = check_device(&device);
+    if (rc != GEMM_RS_OK) return rc;
+    Fp8Args a = {};
+    const int64_t blocks = any ? wgrad_blocks(*g) : 0;
+    if (any) {
+        uint8_t* y = static_cast<uint8_t*>(workspace);
+        uint8_t* ys = y + up16(g->N * blocks * kFp8Block);
+        uint8_t* x = y + wgrad_operand(g->N, blocks);
+        uint8_t* xs = x + up16(g->K * blocks * kFp8Block);
+        rc = quant_columns(g->dtype, g->M, g->N, g->M, g->dy, g->dy_stride, g->offsets, nullptr, g->E, blocks, y, ys, stream);
+        if (rc == GEMM_RS_OK)
+            rc = quant_columns(g->dtype, g->M, g->K, g->x_rows, g->x, g->x_stride, g->offsets, g->tokens, g->E, blocks, x, xs, stream);
+        if (rc != GEMM_RS_OK) return rc;
+        a.x = y;
+        a.xs = ys;
+        a.w = x;
+        a.ws = xs;
+    }
+    a.offsets = g->offsets;
+    a.add = g->add;
+    a.out = g->dw;
+    a.M = g->N;
+    a.x_rows = g->N;
+    a.rows = any ? g->M : 0;
+    a.x_pitch = a.w_pitch = blocks * kFp8Block;
+    a.out_expert = g->N * g->K;
+    a.add_stride = a.out_stride = g->K;
+    a.xs_bytes = pitch_of(g->N) * blocks;
+    a.ws_bytes = pitch_of(g->K) * blocks;
+    a.N = (int)g->K;
+    a.E = (int)g->E;
+    a.xs_pitch = (int)pitch_of(g->N);
+    a.ws_pitch = (int)pitch_of(g->K);
+    return product_of<kSums>(g->out_dtype, a, device, stream);
+}
+
+}  // extern "C"

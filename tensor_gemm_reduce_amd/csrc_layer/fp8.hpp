@@ -1,0 +1,725 @@
+// fp8.hpp -- matrices in e4m3 with a power-of-two scale for each block of 128 inputs,
+// and their products, dense and by expert.
+//
+// The scale is the smallest power of two that brings a block to at most 448, e4m3's
+// largest value: quantising then has one rounding, to e4m3, which no reciprocal can
+// turn, and the scale is an E8M0 byte, which the scaled MFMA takes beside its operands.
+// So the products of a block of 128 are scaled where they are summed, in FP32, without
+// a vector instruction, and the matrix instructions alone bound a large product.
+// How the instruction orders its inputs inside a block does not matter: both operands
+// are read in the same order, and all of a block has one scale.
+#pragma once
+
+#include <type_traits>
+#include <utility>
+
+#include "common.hpp"
+
+namespace gemm_rs_layer {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kFp8Block = 128;
+constexpr int kFp8MinExp = -126;
+
+// The exponent of a block from the bits of its largest magnitude: E - 8 for 2^E .. 1.75 2^E,
+// else E - 7, since 448 = 1.75 2^8.
+__device__ __forceinline__ int fp8_exponent(uint32_t top)
+{
+    const int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return e > kFp8MinExp ? e : kFp8MinExp;
+}
+
+// Four values times 2^-e as e4m3 bytes; all NaN in a block with an infinity or a NaN.
+__device__ __forceinline__ uint32_t fp8_word(float a, float b, float c, float d)
+{
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+constexpr uint32_t kFp8Nan4 = 0x7F7F7F7Fu;
+
+__device__ __forceinline__ float fp8_inverse(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
+
+struct Fp8QuantArgs {
+    const void* x;
+    uint8_t *q, *s;
+    int64_t M, stride;  // rows of x
+    int K, blocks;      // columns; blocks of 128 of the result's rows
+    int pitch;          // bytes from a block's scales to the next one's
+    int64_t q_pitch;    // bytes of a row of q
+    // transposed: the rows of each expert by themselves
+    const int32_t *offsets, *tokens;
+    int E;
+    int64_t x_rows;
+};
+
+// A wave takes 16 rows of one block, 16 lanes and 16 bytes a lane (BF16) for each row.
+template <class T>
+__global__ __launch_bounds__(256) void fp8_quant_kernel(const Fp8QuantArgs a)
+{
+    const int lane = threadIdx.x & 63, l16 = lane & 15;
+    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t r0 = id / a.blocks * 16;
+    const int kb = (int)(id % a.blocks), col = kb * kFp8Block + l16 * 8;
+    vec8<T> v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = r0 + 4 * i + lane / 16;
+        v[i] = vec8<T>{};
+        if (r < a.M) v[i] = load8(static_cast<const T*>(a.x) + r * a.stride, col, a.K);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = r0 + 4 * i + lane / 16;
+        float f[8];
+        widen<T>(v[i], f);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+        const bool bad = top >= 0x7F800000u;
+        const int e = bad ? 0 : fp8_exponent(top);
+        const float inv = fp8_inverse(e);
+        u32x2 w = {fp8_word(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                   fp8_word(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
+        if (bad) w = u32x2{kFp8Nan4, kFp8Nan4};
+        if (r < a.M) {
+            *reinterpret_cast<u32x2*>(a.q + r * a.q_pitch + col) = w;
+            if (l16 == 0) a.s[(int64_t)kb * a.pitch + r] = (uint8_t)(e + 127);
+        }
+    }
+}
+
+// The lane's expert among e0 .. e0 + 63: rows a .. b - 1, within 0 .. M.
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int E, int64_t M, int e, int& a, int& b)
+{
+    a = b = 0;
+    if (e < E) {
+        const int m = (int)M;
+        a = min(max(offsets[e], 0), m);
+        b = min(max(offsets[e + 1], a), m);
+    }
+}
+
+struct RowTile {
+    int e, m0, m1;  // expert, first row, end of the expert's rows
+};
+
+// Tile `id` of the experts' rows, `rows` rows a tile, expert by expert; false if there are
+// fewer.  For a whole wave, with uniform results.
+__device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int64_t M, int rows, int id, RowTile& t)
+{
+    const int lane = threadIdx.x & 63;
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        int a, b;
+        expert_rows(offsets, E, M, e0 + lane, a, b);
+        const int n = (b - a + rows - 1) / rows;
+        int s = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(s, d);
+            if (lane >= d) s += o;
+        }
+        const uint64_t past = __ballot(carry + s > id);
+        if (past) {
+            const int at = __ffsll((unsigned long long)past) - 1;
+            const int before = carry + __builtin_amdgcn_readlane(s, at) - __builtin_amdgcn_readlane(n, at);
+            t.e = e0 + at;
+            t.m0 = __builtin_amdgcn_readlane(a, at) + (uni(id) - before) * rows;
+            t.m1 = __builtin_amdgcn_readlane(b, at);
+            return true;
+        }
+        carry += __builtin_amdgcn_readlane(s, 63);
+    }
+    return false;
+}
+
+// Tiles of `rows` rows of the experts before `last`.
+__device__ __forceinline__ int tiles_before(const int32_t* offsets, int E, int64_t M, int rows, int last)
+{
+    int n = 0;
+    for (int e0 = 0; e0 < last; e0 += 64) {
+        int a, b;
+        const int e = e0 + (threadIdx.x & 63);
+        expert_rows(offsets, E, M, e < last ? e : E, a, b);
+        n += (b - a + rows - 1) / rows;
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
+    return uni(n);
+}
+
+// 128 rows x 64 columns of x as 64 rows of one block: a thread holds 4 rows x 8 columns, the
+// columns' maxima meet in LDS, and a column's four bytes go there as one word, from where
+// whole rows of the result are written.
+template <class T>
+__global__ __launch_bounds__(256) void fp8_quant_t_kernel(const Fp8QuantArgs a)
+{
+    constexpr int kCols = 64, kPitch = kFp8Block + 16;
+    __shared__ uint32_t top[kCols];
+    __shared__ __attribute__((aligned(16))) uint8_t out[kCols * kPitch];
+    const int tid = threadIdx.x, cg = tid % 8, rg = tid / 8, c0 = blockIdx.y * kCols, col = c0 + cg * 8;
+    int64_t m0 = (int64_t)blockIdx.x * kFp8Block, m1 = a.M;
+    if (a.offsets) {
+        RowTile t;
+        if (!find_tile(a.offsets, a.E, a.M, kFp8Block, blockIdx.x, t)) return;
+        m0 = t.m0;
+        m1 = t.m1;
+    }
+    if (tid < kCols) top[tid] = 0;
+    vec8<T> v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int64_t r = m0 + rg * 4 + i;
+        v[i] = vec8<T>{};
+        if (r >= m1) continue;
+        if (a.tokens) r = a.tokens[r];
+        if (r >= 0 && r < a.x_rows) v[i] = load8(static_cast<const T*>(a.x) + r * a.stride, col, a.K);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint((float)v[i][j]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int d = 8; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+        if ((tid & 63) < 8) atomicMax(&top[cg * 8 + j], m);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t m = top[cg * 8 + j];
+        const bool bad = m >= 0x7F800000u;
+        const float inv = fp8_inverse(bad ? 0 : fp8_exponent(m));
+        const uint32_t w = fp8_word((float)v[0][j] * inv, (float)v[1][j] * inv, (float)v[2][j] * inv, (float)v[3][j] * inv);
+        *reinterpret_cast<uint32_t*>(out + (cg * 8 + j) * kPitch + rg * 4) = bad ? kFp8Nan4 : w;
+    }
+    __syncthreads();
+    const int64_t kb = blockIdx.x;
+    if (tid < kCols && c0 + tid < a.K) {
+        const uint32_t m = top[tid];
+        a.s[kb * a.pitch + c0 + tid] = (uint8_t)((m >= 0x7F800000u ? 0 : fp8_exponent(m)) + 127);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = tid / 8 + 32 * i;
+        if (c0 + c < a.K)
+            *reinterpret_cast<u32x4*>(a.q + (c0 + c) * a.q_pitch + kb * kFp8Block + tid % 8 * 16) =
+                *reinterpret_cast<const u32x4*>(out + c * kPitch + tid % 8 * 16);
+    }
+}
+
+struct Fp8PackArgs {
+    const void* w;
+    uint8_t *q, *s;
+    int N, K, transpose;
+    int64_t w_expert, q_expert, s_expert;  // elements, bytes and bytes of an expert
+    int64_t q_pitch;
+    int pitch;
+};
+
+// A workgroup takes a block of 128 x 128: a thread holds eight columns of eight rows 16 apart.
+template <class T>
+__global__ __launch_bounds__(256) void fp8_pack_kernel(const Fp8PackArgs a)
+{
+    constexpr int kPitch = kFp8Block + 16;
+    __shared__ uint32_t top;
+    __shared__ __attribute__((aligned(16))) uint8_t out[kFp8Block * kPitch];
+    const int tid = threadIdx.x, cg = tid % 16, rg = tid / 16, n0 = blockIdx.y * kFp8Block, k0 = blockIdx.x * kFp8Block;
+    const T* w = static_cast<const T*>(a.w) + blockIdx.z * a.w_expert;
+    uint8_t *q = a.q + blockIdx.z * a.q_expert, *s = a.s + blockIdx.z * a.s_expert;
+    if (tid == 0) top = 0;
+    vec8<T> v[8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int n = n0 + rg + 16 * i;
+        v[i] = vec8<T>{};
+        if (n < a.N) v[i] = load8(w + (int64_t)n * a.K, k0 + cg * 8, a.K);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint((float)v[i][j]) & 0x7FFFFFFFu);
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    __syncthreads();
+    if ((tid & 63) == 0) atomicMax(&top, m);
+    __syncthreads();
+    m = top;
+    const bool bad = m >= 0x7F800000u;
+    const int e = bad ? 0 : fp8_exponent(m);
+    const float inv = fp8_inverse(e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float f[8];
+        widen<T>(v[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= inv;
+        u32x2 b = {fp8_word(f[0], f[1], f[2], f[3]), fp8_word(f[4], f[5], f[6], f[7])};
+        if (bad) b = u32x2{kFp8Nan4, kFp8Nan4};
+        const int r = rg + 16 * i;
+        if (a.transpose) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[(cg * 8 + j) * kPitch + r] = (uint8_t)(b[j / 4] >> (8 * (j % 4)));
+        } else
+            *reinterpret_cast<u32x2*>(out + r * kPitch + cg * 8) = b;
+    }
+    __syncthreads();
+    // rows of the result: n, or k where transposed; padding rows of it are not kept, its padding columns are zeros
+    const int rows = a.transpose ? a.K : a.N, r0 = a.transpose ? k0 : n0, kb = a.transpose ? blockIdx.y : blockIdx.x;
+    if (tid < kFp8Block && r0 + tid < rows) s[(int64_t)kb * a.pitch + r0 + tid] = (uint8_t)(e + 127);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = tid / 8 + 32 * i;
+        u32x4 b = *reinterpret_cast<const u32x4*>(out + r * kPitch + tid % 8 * 16);
+        if (r0 + r < rows) *reinterpret_cast<u32x4*>(q + (int64_t)(r0 + r) * a.q_pitch + kb * kFp8Block + tid % 8 * 16) = b;
+    }
+}
+
+// ---- the products -----------------------------------------------------------------------
+
+enum Fp8Mode { kDense = 0, kByExpert = 1, kGather = 2, kSums = 3 };
+
+// out[m][n] = add + sum_k x[m][k] w[n][k].
+//   kDense   all rows with one w
+//   kByExpert   the rows of each expert with its own; kGather: the row of x is tokens[m]
+//   kSums    a result for each expert, the sum over its own blocks of the columns of x and w
+struct Fp8Args {
+    const uint8_t *x, *w, *xs, *ws;
+    const int32_t *offsets, *tokens;
+    const float* add;
+    void* out;
+    int64_t M, x_rows, rows;  // rows of the result; of x; of the experts (kSums)
+    int64_t x_pitch, w_pitch, w_expert, ws_expert, out_expert, add_stride, out_stride;
+    int64_t xs_bytes, ws_bytes;
+    int N, E, steps;          // steps of 128 inputs
+    int xs_pitch, ws_pitch;
+    int tiles_m, tiles_n;
+};
+
+// Results in FP32 take every product whole: the scaled MFMA lines the products of e4m3 up with the largest of a group and
+// drops what lies below its 2^-13 (the sums with the accumulator are FP32's).  That is within BF16's and F16's rounding
+// of a result, not within FP32's, so there the operands are multiplied in BF16, at half the rate.
+template <class T>
+constexpr bool fp8_exact = std::is_same<T, float>::value;
+
+__device__ __forceinline__ float fp8_scale(uint32_t byte) { return __uint_as_float((byte & 255u) << 23); }
+
+// Quarter q (eight values) of a fragment times its scale.
+__device__ __forceinline__ bf16x8 fp8_to_bf16(const i32x8& f, int q, float scale)
+{
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bf16x2 p = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * q + i / 2], scale, true)
+                               : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * q + i / 2], scale, false);
+        v[i] = __builtin_bit_cast(uint32_t, p);
+    }
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+template <int... I, class F>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f)
+{
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F f)
+{
+    each_of(std::make_integer_sequence<int, N>(), f);
+}
+
+// Stores eight results of a row from column n on, with what is added to them.
+template <class T>
+__device__ __forceinline__ void fp8_store(const Fp8Args& a, T* out, const float* add, int n, float (&f)[8])
+{
+    if (add) {
+        float g[8];
+        widen<float>(load8(add, n, a.N), g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] += g[j];
+    }
+    store8(out, n, a.N, f);
+}
+
+// Tiles of 64 W x 64 W results by 2 x 2 waves of 32 W x 32 W, steps of 128 inputs, two stages in LDS.
+//   - Stages are loaded into LDS directly, 16-byte chunk c of row r at chunk c ^ (r / 2) % 8:
+//     16 consecutive rows, as the fragments are read, lie in different banks.
+//   - A wave's LDS row 32 i + r holds matrix row W r + i: the W fragments of a lane then
+//     belong to W neighbouring rows, whose scales are one load, and the MFMA picks the byte.
+//     w is the MFMA's first operand, so a lane ends with 4 W neighbouring columns of a row.
+//   - A step has two halves of 64 inputs.  While the first is multiplied, the second's
+//     fragments are read; then the next stage has to have come, and a barrier frees this one;
+//     while the second is multiplied, the stage is filled again (a step's time to arrive) and
+//     the next step's first fragments are read.
+template <int W>
+struct Fp8Tile {
+    static constexpr int kRows = 64 * W;
+    static constexpr int kOperand = kRows * kFp8Block;
+    static constexpr int kStage = 2 * kOperand;
+    static constexpr int kLds = 2 * kStage;
+};
+
+template <int W, int MODE, bool EXACT>
+struct Fp8Run {
+    typedef Fp8Tile<W> Tile;
+    static constexpr int kLoads = 2 * W;  // a thread's, of an operand and stage
+    static constexpr int kMf = W * W;     // MFMAs of a half step, or (EXACT) of a quarter of it
+
+    const Fp8Args& a;
+    char* const lds;
+    f32x16 (&acc)[W][W];  // [row of x][row of w]
+    i32x8 fx[2][W], fw[2][W];
+    bf16x8 wide[2][EXACT ? 2 * W : 1];  // a quarter of a half step: w's, then x's
+    int sx[2][MODE == kGather ? W : 1], sw[2];
+    uint32_t xo[MODE == kGather ? kLoads : 1], wo;  // a thread's chunk of a stage, first or of each load
+    uint32_t sxo[MODE == kGather ? W : 1], swo;
+    uint32_t get[2][4];  // LDS offsets of the lane's chunks: operand, chunk (of the first stage)
+    __amdgpu_buffer_rsrc_t rx, rw, rsx, rsw;
+    int step0, step1;
+
+    // rows m0 .. m1 - 1 of x, columns n0 .. of the result, steps s0 .. s1 - 1
+    __device__ __forceinline__ Fp8Run(const Fp8Args& args, char* l, f32x16 (&c)[W][W], int e, int64_t m0, int64_t m1, int n0,
+                                      int s0, int s1)
+        : a(args), lds(l), acc(c), step0(s0), step1(s1)
+    {
+        const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+        const int wm = wave >> 1, wn = wave & 1;
+        const int chunk = (tid % 8) ^ (tid / 16 % 8), row = W * (tid / 8);
+        const int nrows = (int)(a.N - n0 < Tile::kRows ? a.N - n0 : Tile::kRows);
+        const int mrows = (int)(m1 - m0 < Tile::kRows ? m1 - m0 : Tile::kRows);
+        rw = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + e * a.w_expert + n0 * a.w_pitch), 0, (int)(nrows * a.w_pitch),
+                                               kRsrcFlags);
+        wo = (uint32_t)row * (uint32_t)a.w_pitch + chunk * 16;
+        const uint8_t* ws = a.ws + e * a.ws_expert;
+        rsw = __builtin_amdgcn_make_buffer_rsrc((void*)ws, 0, (int)a.ws_bytes, kRsrcFlags);
+        swo = n0 + wn * 32 * W + W * (lane & 31);
+        if constexpr (MODE == kGather) {
+            rx = __builtin_amdgcn_make_buffer_rsrc((void*)a.x, 0, (int)(a.x_rows * a.x_pitch), kRsrcFlags);
+            auto token = [&](int r) {
+                const int t = r < mrows ? a.tokens[m0 + r] : -1;
+                return t < a.x_rows ? t : -1;
+            };
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int t = token(row + j / W * 32 * W + j % W);
+                xo[j] = t >= 0 ? (uint32_t)t * (uint32_t)a.x_pitch + chunk * 16 : kOob;
+            }
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const int t = token(wm * 32 * W + W * (lane & 31) + i);
+                sxo[i] = t >= 0 ? t : kOob;
+            }
+        } else {
+            rx = __builtin_amdgcn_make_buffer_rsrc((void*)(a.x + m0 * a.x_pitch), 0, (int)(mrows * a.x_pitch), kRsrcFlags);
+            xo[0] = (uint32_t)row * (uint32_t)a.x_pitch + chunk * 16;
+            sxo[0] = (uint32_t)m0 + wm * 32 * W + W * (lane & 31);
+        }
+        rsx = __builtin_amdgcn_make_buffer_rsrc((void*)a.xs, 0, (int)a.xs_bytes, kRsrcFlags);
+        const int r = lane & 31, h = lane >> 5, turn = r / 2 % 8;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // chunks of the half c / 2 of a step: 2 h + c % 2
+            const int at = (4 * (c / 2) + 2 * h + c % 2) ^ turn;
+            get[0][c] = (wm * 32 * W + r) * kFp8Block + at * 16;
+            get[1][c] = Tile::kOperand + (wn * 32 * W + r) * kFp8Block + at * 16;
+        }
+    }
+    // Load j of the 2 kLoads of step s into stage P.
+    template <int P>
+    __device__ __forceinline__ void load(int j, int s) const
+    {
+        const bool w = j >= kLoads;
+        const int i = w ? j - kLoads : j;
+        const uint32_t at = (uint32_t)(i / W * 32 * W + i % W);  // rows from the thread's first
+        const uint32_t off = (w ? wo + at * (uint32_t)a.w_pitch : MODE == kGather ? xo[i % (MODE == kGather ? kLoads : 1)]
+                                                                                  : xo[0] + at * (uint32_t)a.x_pitch) | past(s);
+        const int wave = uni(threadIdx.x >> 6);
+        lds_void_t* to = (lds_void_t*)(lds + P * Tile::kStage + (w ? Tile::kOperand : 0) + (i * 256 + wave * 64) * 16);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(w ? rw : rx, to, 16, off, s * kFp8Block, 0, 0);
+    }
+    // an offset past every resource for steps past the last, which then read zeros: a mask, no select that might
+    // become one per lane
+    __device__ __forceinline__ uint32_t past(int s) const { return ~(uint32_t)uni((s - step1) >> 31) & kOob; }
+    template <int P>
+    __device__ __forceinline__ void load_scales(int s)
+    {
+        auto get_w = [&](const __amdgpu_buffer_rsrc_t& r, uint32_t off, int pitch) -> int {
+            if constexpr (W == 4) return (int)__builtin_amdgcn_raw_buffer_load_b32(r, off | past(s), s * pitch, 0);
+            else return (int)__builtin_amdgcn_raw_buffer_load_b16(r, off | past(s), s * pitch, 0);
+        };
+        sw[P] = get_w(rsw, swo, a.ws_pitch);
+        if constexpr (MODE == kGather) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) sx[P][i] = __builtin_amdgcn_raw_buffer_load_b8(rsx, sxo[i] | past(s), s * a.xs_pitch, 0);
+        } else
+            sx[P][0] = get_w(rsx, sxo[0], a.xs_pitch);
+    }
+    // fragment i of half u of the stage P
+    template <int P>
+    __device__ __forceinline__ i32x8 read(int u, int i, bool w) const
+    {
+        const char* p = lds + P * Tile::kStage + i * 32 * kFp8Block;
+        const i32x4 lo = *reinterpret_cast<const i32x4*>(p + get[w][2 * u]);
+        const i32x4 hi = *reinterpret_cast<const i32x4*>(p + get[w][2 * u + 1]);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    // piece i (w's, then x's) of quarter q of half U in BF16, scaled
+    template <int U, int P>
+    __device__ __forceinline__ void widen_piece(int q, int i)
+    {
+        const bool w = i < W;
+        const int t = w ? i : i - W;
+        const uint32_t s = w ? (uint32_t)sw[P] >> (8 * t) : MODE == kGather ? (uint32_t)sx[P][MODE == kGather ? t : 0]
+                                                                            : (uint32_t)sx[P][0] >> (8 * t);
+        wide[q & 1][i] = fp8_to_bf16(w ? fw[U][t] : fx[U][t], q, fp8_scale(s));
+    }
+    // MFMA M of half U of a step on stage P
+    template <int U, int P, int M>
+    __device__ __forceinline__ void multiply()
+    {
+        constexpr int i = M % kMf / W, j = M % W;
+        if constexpr (EXACT) {
+            constexpr int q = M / kMf, piece = M % kMf;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wide[q & 1][j], wide[q & 1][W + i], acc[i][j], 0, 0, 0);
+            if constexpr (kMf >= 2 * W) {
+                if constexpr (piece < 2 * W) widen_next<U, P>(q, piece);
+            } else {
+                widen_next<U, P>(q, piece);
+            }
+        } else if constexpr (MODE == kGather)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[U][j], fx[U][i], acc[i][j], 0, 0, j, sw[P], 0,
+                                                                         sx[P][i]);
+        else
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[U][j], fx[U][i], acc[i][j], 0, 0, j, sw[P], i,
+                                                                         sx[P][0]);
+    }
+    // the same piece of the quarter after q
+    template <int U, int P>
+    __device__ __forceinline__ void widen_next(int q, int piece)
+    {
+        if (q < 3) widen_piece<U, P>(q + 1, piece);
+        else if (U == 0) widen_piece<1, P>(0, piece);
+        else widen_piece<0, P ^ 1>(0, piece);
+    }
+    // this wave's LDS reads and loads have ended, then everybody's
+    static __device__ __forceinline__ void barrier()
+    {
+        __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0), as a builtin: the compiler then knows
+        __asm__ __volatile__("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // Takes the constancy of these from the compiler, which would give every sum with them a register of its own.
+    __device__ __forceinline__ void hide()
+    {
+        __asm__ __volatile__("" : "+v"(wo));
+        if constexpr (MODE != kGather) __asm__ __volatile__("" : "+v"(xo[0]));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) __asm__ __volatile__("" : "+v"(get[0][c]), "+v"(get[1][c]));
+    }
+    template <int P>
+    __device__ __forceinline__ void step(int s)
+    {
+        constexpr int kAll = EXACT ? 4 * kMf : kMf, kPer = 4 * W / kMf;  // loads beside an MFMA
+        hide();
+        each<kAll>([&](auto m) {
+            constexpr int M = decltype(m)::value;
+            multiply<0, P, M>();
+            if constexpr (M < W) fw[1][M] = read<P>(1, M, true);
+            else if constexpr (M < 2 * W) fx[1][M - W] = read<P>(1, M - W, false);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        barrier();
+        each<kAll>([&](auto m) {
+            constexpr int M = decltype(m)::value;
+            multiply<1, P, M>();
+#pragma unroll
+            for (int j = kPer * M; j < kPer * (M + 1) && j < 4 * W; ++j) load<P>(j, s + 2);
+            if constexpr (M < W) fw[0][M] = read<P ^ 1>(0, M, true);
+            else if constexpr (M < 2 * W) fx[0][M - W] = read<P ^ 1>(0, M - W, false);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        load_scales<P>(s + 2);
+    }
+    __device__ __forceinline__ void run()
+    {
+#pragma unroll
+        for (int j = 0; j < 2 * kLoads; ++j) load<0>(j, step0);
+        load_scales<0>(step0);
+#pragma unroll
+        for (int j = 0; j < 2 * kLoads; ++j) load<1>(j, step0 + 1);
+        load_scales<1>(step0 + 1);
+        barrier();
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            fw[0][i] = read<0>(0, i, true);
+            fx[0][i] = read<0>(0, i, false);
+        }
+        if constexpr (EXACT)
+#pragma unroll
+            for (int i = 0; i < 2 * W; ++i) widen_piece<0, 0>(0, i);
+        for (int s = step0; s < step1; s += 2) {
+            step<0>(s);
+            step<1>(s + 1);
+        }
+        barrier();
+    }
+};
+
+// EXACT: quarters of the fragments are turned to BF16, which holds every scaled value, beside the MFMAs of the quarter before.
+template <int W, int MODE, class T>
+__global__ __launch_bounds__(256, W == 4 ? 1 : 2) void fp8_kernel(const Fp8Args a)
+{
+    typedef Fp8Tile<W> Tile;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+    int e = 0, n0, s0 = 0, s1 = a.steps;
+    int64_t m0, m1 = a.M;
+    const int id = blockIdx.x;
+    if constexpr (MODE == kByExpert || MODE == kGather) {
+        const int tn = id % a.tiles_n;
+        RowTile t;
+        if (!find_tile(a.offsets, a.E, a.M, Tile::kRows, id / a.tiles_n, t)) return;
+        e = t.e;
+        m0 = t.m0;
+        m1 = t.m1;
+        n0 = tn * Tile::kRows;
+    } else {
+        int t = id;
+        if constexpr (MODE == kSums) {
+            e = id / (a.tiles_m * a.tiles_n);
+            t = id % (a.tiles_m * a.tiles_n);
+            s0 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, e);
+            s1 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, e + 1);
+        }
+        m0 = (int64_t)(t / a.tiles_n) * Tile::kRows;
+        n0 = t % a.tiles_n * Tile::kRows;
+    }
+    f32x16 acc[W][W];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[i][j] = f32x16{};
+    Fp8Run<W, MODE, fp8_exact<T>>(a, lds, acc, MODE == kSums ? 0 : e, m0, m1, n0, s0, s1).run();
+    const int r = lane & 31, h = lane >> 5;
+    const int64_t shift = MODE == kSums ? e * a.out_expert : 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const int64_t m = m0 + (wave >> 1) * 32 * W + W * r + i;
+        if (m >= m1) continue;
+        T* out = static_cast<T*>(a.out) + shift + m * a.out_stride;
+        const float* add = a.add ? a.add + shift + m * a.add_stride : nullptr;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int n = n0 + (wave & 1) * 32 * W + W * (8 * g + 4 * h);  // 4 W columns: W e + j
+#pragma unroll
+            for (int p = 0; p < 4 * W; p += 8) {
+                float f[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) f[q] = acc[i][(p + q) % W][4 * g + (p + q) / W];
+                fp8_store<T>(a, out, add, n + p, f);
+            }
+        }
+    }
+}
+
+// Few rows: a workgroup computes 16 columns for up to 16 MF rows, its waves split the blocks of
+// 128 inputs and add up through LDS in wave order.  The weights' bytes bound it: each wave
+// keeps kAhead blocks of them in flight, straight into the MFMA's registers (16 rows x 64
+// bytes an instruction).
+constexpr int kFewTile = 16;
+
+template <int WAVES, int MF, int MODE, class T>
+__global__ __launch_bounds__(64 * WAVES) void fp8_few_kernel(const Fp8Args a)
+{
+    constexpr int kAhead = MF > 2 ? 2 : 4;
+    __shared__ __attribute__((aligned(16))) f32x4 part[WAVES][MF][64];
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+    const int n0 = blockIdx.x * kFewTile;
+    int e = 0;
+    int64_t m0 = (int64_t)blockIdx.y * (16 * MF), m1 = a.M;
+    if constexpr (MODE != kDense) {
+        RowTile t;
+        if (!find_tile(a.offsets, a.E, a.M, 16 * MF, blockIdx.y, t)) return;
+        e = t.e;
+        m0 = t.m0;
+        m1 = t.m1;
+    }
+    const int n = min(n0 + r, a.N - 1);  // columns and rows past the last are read again, and not stored
+    const uint8_t* w = a.w + e * a.w_expert + n * a.w_pitch + q * 16;
+    const uint8_t* ws = a.ws + e * a.ws_expert + n;
+    const uint8_t *x[MF], *xs[MF];
+#pragma unroll
+    for (int f = 0; f < MF; ++f) {
+        int64_t m = m0 + 16 * f + r;
+        m = m < m1 ? m : m1 - 1;
+        if constexpr (MODE == kGather) {
+            const int64_t t = a.tokens[m];
+            m = t < 0 ? 0 : t < a.x_rows ? t : a.x_rows - 1;
+        }
+        x[f] = a.x + m * a.x_pitch + q * 16;
+        xs[f] = a.xs + m;
+    }
+    struct Block {
+        i32x4 w[2], x[MF][2];
+        int ws, xs[MF];
+    } b[kAhead];
+    auto load = [&](Block& c, int kb) {
+        const int64_t at = (int64_t)kb * kFp8Block;
+        c.w[0] = *reinterpret_cast<const i32x4*>(w + at);
+        c.w[1] = *reinterpret_cast<const i32x4*>(w + at + 64);
+        c.ws = ws[(int64_t)kb * a.ws_pitch];
+#pragma unroll
+        for (int f = 0; f < MF; ++f) {
+            c.x[f][0] = *reinterpret_cast<const i32x4*>(x[f] + at);
+            c.x[f][1] = *reinterpret_cast<const i32x4*>(x[f] + at + 64);
+            c.xs[f] = xs[f][(int64_t)kb * a.xs_pitch];
+        }
+    };
+    f32x4 acc[MF] = {};
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (wave + i * WAVES < a.steps) load(b[i], wave + i * WAVES);
+    for (int kb = wave; kb < a.steps; kb += kAhead * WAVES) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int at = kb + i * WAVES;
+            if (at >= a.steps) break;
+            const i32x8 fw = __builtin_shufflevector(b[i].w[0], b[i].w[1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+            for (int f = 0; f < MF; ++f) {
+                const i32x8 fx = __builtin_shufflevector(b[i].x[f][0], b[i].x[f][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                if constexpr (fp8_exact<T>) {
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_to_bf16(fw, p, fp8_scale(b[i].ws)),
+                                                                         fp8_to_bf16(fx, p, fp8_scale(b[i].xs[f])), acc[f], 0, 0, 0);
+                } else
+                    acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fx, acc[f], 0, 0, 0, b[i].ws, 0, b[i].xs[f]);
+            }
+            if (at + kAhead * WAVES < a.steps) load(b[i], at + kAhead * WAVES);
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < MF; ++f) part[wave][f][lane] = acc[f];
+    __syncthreads();
+    for (int i = threadIdx.x; i < MF * 64; i += 64 * WAVES) {
+        f32x4 s = part[0][i / 64][lane];
+#pragma unroll
+        for (int v = 1; v < WAVES; ++v) s += part[v][i / 64][lane];
+        const int64_t m = m0 + 16 * (i / 64) + r;
+        if (m >= m1) continue;
+        T* out = static_cast<T*>(a.out) + m * a.out_stride;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int at = n0 + 4 * q + c;
+            if (at >= a.N) break;
+            float v = s[c];
+            if (a.add) v += a.add[m * a.add_stride + at];
+            out[at] = (T)v;
+        }
+    }
+}
+
+}  // namespace gemm_rs_layer

@@ -1,0 +1,582 @@
+// route.hpp -- the router: scores, the choice of k experts for each token, the
+// plan of every expert's rows, the gradient of the logits; and a token's rows
+// back into one.
+//
+// A wave takes a token (or 64 / SEG tokens where the experts fit SEG lanes): lane l
+// holds experts l, l + 64, ..  Choices have to come out as the formula says, not as
+// FP32 rounds it: without a bias and groups scores order as the logits do, which are
+// compared as they are; else in 64 bits.  Either way as unsigned keys that order like
+// the values, so that a maximum over the lanes and the lowest lane that has it are the
+// choice.  Bytes are few (8192 x 256 logits in FP32: 8 MB, 1.7 us); the k maxima over
+// the lanes, six exchanges each, are what takes time.
+#pragma once
+
+#include <type_traits>
+
+#include "common.hpp"
+
+namespace gemm_rs_layer {
+
+constexpr int kPlanIds = 1024;    // choices per workgroup of the plan's kernels, one per thread
+constexpr int kRouteTokens = 128; // at most so many tokens per workgroup
+
+// Workgroups count their choices per expert (hist), a second kernel adds the counts up over
+// the workgroups before each, and a third gives each choice its row.  One workgroup does
+// all by itself.
+struct PlanArgs {
+    const int32_t* experts;
+    int32_t *offsets, *tokens, *slots;
+    int32_t* hist;    // [chunks][E]: counts, then the counts before
+    int32_t* totals;  // [E]
+    int64_t ids;      // T k
+    int E, k, chunk, chunks;  // choices per workgroup; workgroups
+};
+
+// An unsigned number that orders like v; 1 for a NaN, and never 0.
+__device__ __forceinline__ uint32_t route_key(float v)
+{
+    if (v != v) return 1u;
+    const uint32_t b = __float_as_uint(v + 0.f);  // -0 as 0
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t route_key(double v)
+{
+    if (v != v) return 1u;
+    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+    return b >> 63 ? ~b : b | (uint64_t(1) << 63);
+}
+
+template <int SEG>
+__device__ __forceinline__ uint32_t seg_max(uint32_t v)
+{
+#pragma unroll
+    for (int d = SEG / 2; d > 0; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+    return v;
+}
+template <int SEG>
+__device__ __forceinline__ uint64_t seg_max(uint64_t v)
+{
+#pragma unroll
+    for (int d = SEG / 2; d > 0; d >>= 1) {
+        const uint64_t o = (uint64_t)__shfl_xor((long long)v, d);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+template <int SEG>
+__device__ __forceinline__ float seg_max(float v)
+{
+#pragma unroll
+    for (int d = SEG / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+template <int SEG, class F>
+__device__ __forceinline__ F seg_sum(F v)
+{
+#pragma unroll
+    for (int d = SEG / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+__device__ __forceinline__ float route_exp(float v) { return expf(v); }
+__device__ __forceinline__ double route_exp(double v) { return exp(v); }
+
+// s = softmax (over the SEG lanes and NV values each) or sigmoid; values of experts that are off are 0.
+template <class F, int SEG, int NV>
+__device__ __forceinline__ void route_scores(const float (&l)[NV], bool sigmoid, F (&s)[NV])
+{
+    if (sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s[i] = l[i] == -INFINITY ? F(0) : F(1) / (F(1) + route_exp(-(F)l[i]));
+        return;
+    }
+    float top = l[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) top = fmaxf(top, l[i]);
+    top = seg_max<SEG>(top);
+    if (top == -INFINITY) top = 0.f;  // nothing is on: all zeros
+    F sum = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        s[i] = route_exp((F)l[i] - (F)top);
+        sum += s[i];
+    }
+    sum = seg_sum<SEG>(sum);
+    const F inv = sum == F(0) ? F(0) : F(1) / sum;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] *= inv;
+}
+
+struct RouteArgs {
+    const void* logits;
+    const float* bias;
+    float* weights;
+    int32_t* experts;
+    int64_t T, stride;
+    int dtype, E, k, sigmoid, renormalise, groups, keep;
+    float scale;
+    int tokens;  // per workgroup
+    PlanArgs plan;
+};
+
+__device__ __forceinline__ float route_load(const void* p, int dtype, int64_t at)
+{
+    if (dtype == 0) return (float)static_cast<const __bf16*>(p)[at];
+    if (dtype == 1) return (float)static_cast<const _Float16*>(p)[at];
+    return static_cast<const float*>(p)[at];
+}
+
+// Where the choices of a workgroup go: thread i has choice i of the workgroup's (its expert,
+// -1 for none).  Rows count up over the waves' choices in order: a wave finds a choice's
+// rank among the same expert's in the wave by comparing indices bit by bit, and the waves'
+// counts stand in LDS.  before[e]: the expert's first row of this workgroup.  count:
+// [waves][E + 1] 16-bit, and room for E + 1 more words behind it.
+__device__ __forceinline__ int plan_rank(int e, bool in, int E, uint16_t* count, int& wave_rank)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    uint32_t* words = reinterpret_cast<uint32_t*>(count);
+    const int pitch = (E + 1) & ~1;
+    for (int i = threadIdx.x; i < waves * pitch / 2; i += blockDim.x) words[i] = 0;
+    __syncthreads();
+    uint64_t same = __ballot(in);
+    for (int b = 1; b < E; b <<= 1) {
+        const uint64_t m = __ballot((e & b) != 0);
+        same &= e & b ? m : ~m;
+    }
+    const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+    if (in && rank == 0) count[wave * pitch + e] = (uint16_t)__popcll(same);
+    wave_rank = rank;
+    __syncthreads();
+    int r = rank;
+    if (in)
+        for (int w = 0; w < wave; ++w) r += count[w * pitch + e];
+    return r;
+}
+
+// Exclusive sums over E values v[e] (one per thread, more for small workgroups) in LDS, and the total at E.
+__device__ __forceinline__ void scan_experts(int* v, int E, int* part)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+        const int e = e0 + threadIdx.x, own = e < E ? v[e] : 0;
+        int s = own;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(s, d);
+            if (lane >= d) s += o;
+        }
+        if (lane == 63) part[wave] = s;
+        __syncthreads();
+        int base = carry, all = 0;
+        for (int w = 0; w < waves; ++w) {
+            if (w < wave) base += part[w];
+            all += part[w];
+        }
+        carry += all;
+        if (e < E) v[e] = base + s - own;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) v[E] = carry;
+    __syncthreads();
+}
+
+constexpr int kMaxExperts = 1024;
+
+struct PlanLds {
+    uint16_t count[16 * kMaxExperts];
+    int before[kMaxExperts + 1];
+    int part[16];
+};
+
+__device__ __forceinline__ void plan_store(const PlanArgs& a, int64_t id, bool in, int row, int total)
+{
+    if (id < a.ids) {
+        a.slots[id] = in ? row : -1;
+        if (in) a.tokens[row] = (int32_t)(id / a.k);
+        if (id >= total) a.tokens[id] = -1;
+    }
+}
+
+// The plan of at most 1024 choices by one workgroup: choice i = thread i.
+__device__ __forceinline__ void plan_alone(const PlanArgs& a, PlanLds& s, int e, bool in)
+{
+    for (int i = threadIdx.x; i < a.E; i += blockDim.x) s.before[i] = 0;
+    int wave_rank;
+    const int r = plan_rank(e, in, a.E, s.count, wave_rank);
+    // the last wave that has an expert knows its number of rows, so each raises the count to its own last rank
+    if (in) atomicMax(&s.before[e], r + 1);
+    __syncthreads();
+    scan_experts(s.before, a.E, s.part);
+    for (int i = threadIdx.x; i <= a.E; i += blockDim.x) a.offsets[i] = s.before[i];
+    plan_store(a, threadIdx.x, in, in ? s.before[e] + r : 0, s.before[a.E]);
+}
+
+// Threads of the router's workgroups, and so choices that one may make: the scores of WIDE take LDS.
+constexpr int route_threads(int nv) { return nv > 4 ? 256 : kPlanIds; }
+
+template <int SEG, int NV, bool WIDE>
+__global__ __launch_bounds__(route_threads(NV)) void route_kernel(const RouteArgs a)
+{
+    typedef typename std::conditional<WIDE, uint64_t, uint32_t>::type key_t;
+    constexpr int kPer = 64 / SEG;  // tokens of a wave at a time
+    constexpr int kThreads = route_threads(NV);
+    __shared__ union {
+        PlanLds plan;
+        double c[WIDE && SEG == 64 ? kThreads / 64 : 1][WIDE && SEG == 64 ? 64 * NV : 1];
+    } lds;
+    __shared__ int32_t ids[kThreads], hist[kMaxExperts];
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), waves = kThreads / 64;
+    const int sub = lane & (SEG - 1), part = lane / SEG;
+    const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+    ids[threadIdx.x] = -1;
+    for (int i = threadIdx.x; i < a.E; i += kThreads) hist[i] = 0;
+    __syncthreads();
+    for (int g = wave * kPer; g < a.tokens; g += waves * kPer) {
+        const int64_t t = t0 + g + part;
+        const bool live = g + part < a.tokens && t < a.T;
+        float l[NV], p[NV];
+        key_t key[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = i * 64 + sub;
+            l[i] = live && e < a.E ? route_load(a.logits, a.dtype, t * a.stride + e) : -INFINITY;
+        }
+        route_scores<float, SEG, NV>(l, a.sigmoid, p);
+        if constexpr (WIDE) {
+            double c[NV];
+            route_scores<double, SEG, NV>(l, a.sigmoid, c);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = i * 64 + sub;
+                if (a.bias && e < a.E) c[i] += (double)a.bias[e];
+                key[i] = l[i] == -INFINITY ? 0 : route_key(c[i]);
+            }
+            if constexpr (SEG == 64) if (a.groups > 1) {
+                // the lanes of the wave share the groups; each group's two largest
+                double* mine = lds.c[wave];
+#pragma unroll
+                for (int i = 0; i < NV; ++i) mine[i * 64 + lane] = l[i] == -INFINITY ? -INFINITY : c[i] != c[i] ? -1e300 : c[i];
+                __asm__ __volatile__("" ::: "memory");  // the LDS operations of a wave complete in order
+                const int size = a.E / a.groups;
+                int per = 64;  // lanes of a group
+                while (per * a.groups > 64) per >>= 1;
+                const int group = lane / per;
+                double hi = -INFINITY, lo = -INFINITY;
+                if (group < a.groups)
+                    for (int i = lane % per; i < size; i += per) {
+                        const double v = mine[group * size + i];
+                        if (v > hi) {
+                            lo = hi;
+                            hi = v;
+                        } else if (v > lo)
+                            lo = v;
+                    }
+                for (int d = per / 2; d > 0; d >>= 1) {
+                    const double oh = __shfl_xor(hi, d), ol = __shfl_xor(lo, d);
+                    const double third = hi < oh ? hi : oh;  // the smaller of the two largest
+                    lo = lo > ol ? lo : ol;
+                    if (third > lo) lo = third;
+                    if (oh > hi) hi = oh;
+                }
+                const double total = lo == -INFINITY ? hi : hi + lo;
+                // how many groups come before this one
+                int rank = 0;
+                for (int o = 0; o < a.groups; ++o) {
+                    const double v = __shfl(total, o * per);
+                    rank += v > total || (v == total && o < group) ? 1 : 0;
+                }
+                const uint64_t kept = __ballot(group < a.groups && rank < a.keep);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int e = i * 64 + lane;
+                    if (e < a.E && !(kept >> (e / size * per) & 1)) key[i] = 0;
+                }
+                __asm__ __volatile__("" ::: "memory");
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) key[i] = l[i] == -INFINITY ? 0 : route_key(l[i]);
+        }
+        int chosen = -1;
+        float score = 0.f, sum = 0.f;
+        for (int j = 0; j < a.k; ++j) {
+            key_t top = key[0];
+#pragma unroll
+            for (int i = 1; i < NV; ++i) top = key[i] > top ? key[i] : top;
+            top = seg_max<SEG>(top);
+            int e = -1;
+            float v = 0.f;
+#pragma unroll
+            for (int i = NV - 1; i >= 0; --i) {
+                uint64_t m = __ballot(top != 0 && key[i] == top);
+                if constexpr (SEG < 64) m = m >> (part * SEG) & ((uint64_t(1) << SEG) - 1);
+                if (m) {
+                    const int at = __ffsll((unsigned long long)m) - 1;
+                    e = i * 64 + at;
+                    v = __shfl(p[i], part * SEG + at);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (e == i * 64 + sub) key[i] = 0;
+            sum += v;
+            if (sub == j % SEG) {
+                chosen = e;
+                score = v;
+            }
+        }
+        // lane j of the token has choice j (k <= SEG)
+        if (live && sub < a.k) {
+            const float w = a.renormalise ? score / (sum + 1e-20f) : score;
+            a.weights[t * a.k + sub] = a.scale * w;
+            a.experts[t * a.k + sub] = chosen;
+            ids[(g + part) * a.k + sub] = chosen;
+            if (a.plan.chunks > 1 && chosen >= 0) atomicAdd(&hist[chosen], 1);
+        }
+    }
+    __syncthreads();
+    if (a.plan.chunks > 1) {
+        for (int i = threadIdx.x; i < a.E; i += kThreads) a.plan.hist[(int64_t)blockIdx.x * a.E + i] = hist[i];
+        return;
+    }
+    const int e = ids[threadIdx.x];
+    plan_alone(a.plan, lds.plan, e, e >= 0);
+}
+
+// Counts of given choices; all of the plan if one workgroup holds them.
+__global__ __launch_bounds__(kPlanIds) void plan_count_kernel(const PlanArgs a)
+{
+    __shared__ PlanLds s;
+    const int64_t id = (int64_t)blockIdx.x * a.chunk + threadIdx.x;
+    int e = threadIdx.x < a.chunk && id < a.ids ? a.experts[id] : -1;
+    if (e >= a.E) e = -1;
+    const bool in = e >= 0;
+    if (a.chunks == 1) {
+        plan_alone(a, s, e, in);
+        return;
+    }
+    for (int i = threadIdx.x; i < a.E; i += blockDim.x) s.before[i] = 0;
+    __syncthreads();
+    if (in) atomicAdd(&s.before[e], 1);
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.E; i += blockDim.x) a.hist[(int64_t)blockIdx.x * a.E + i] = s.before[i];
+}
+
+// hist[c][e] becomes the sum over the workgroups before c: 8 experts x 32 workgroups at a time.
+__global__ __launch_bounds__(256) void plan_scan_kernel(const PlanArgs a)
+{
+    __shared__ int part[8][33];
+    const int col = threadIdx.x & 7, row = threadIdx.x >> 3, e = blockIdx.x * 8 + col;
+    int carry = 0;
+    for (int c0 = 0; c0 < a.chunks; c0 += 32) {
+        const int c = c0 + row;
+        const bool in = c < a.chunks && e < a.E;
+        const int own = in ? a.hist[(int64_t)c * a.E + e] : 0;
+        part[col][row] = own;
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            const int v = part[col][r];
+            before += r < row ? v : 0;
+            all += v;
+        }
+        if (in) a.hist[(int64_t)c * a.E + e] = carry + before;
+        carry += all;
+        __syncthreads();
+    }
+    if (row == 0 && e < a.E) a.totals[e] = carry;
+}
+
+__global__ __launch_bounds__(kPlanIds) void plan_place_kernel(const PlanArgs a)
+{
+    __shared__ PlanLds s;
+    for (int i = threadIdx.x; i < a.E; i += blockDim.x) s.before[i] = a.totals[i];
+    __syncthreads();
+    scan_experts(s.before, a.E, s.part);
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i <= a.E; i += blockDim.x) a.offsets[i] = s.before[i];
+    const int64_t id = (int64_t)blockIdx.x * a.chunk + threadIdx.x;
+    const bool mine = threadIdx.x < a.chunk && id < a.ids;
+    int e = mine ? a.experts[id] : -1;
+    if (e >= a.E) e = -1;
+    const bool in = e >= 0;
+    int wave_rank;
+    const int r = plan_rank(e, in, a.E, s.count, wave_rank);
+    if (mine) plan_store(a, id, in, in ? s.before[e] + a.hist[(int64_t)blockIdx.x * a.E + e] + r : 0, s.before[a.E]);
+}
+
+struct RouteGradArgs {
+    const void* logits;
+    const int32_t* experts;
+    const float* dweights;
+    void* dlogits;
+    int64_t T, stride, dstride;
+    int dtype, E, k, sigmoid, renormalise;
+    float scale;
+};
+
+// Scores are computed again.  ds is what the weights pass to the scores that were chosen;
+// softmax: dl = s (ds - sum ds s), sigmoid: dl = ds s (1 - s).
+template <int SEG, int NV>
+__global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs a)
+{
+    constexpr int kPer = 64 / SEG;
+    const int lane = threadIdx.x & 63, sub = lane & (SEG - 1), part = lane / SEG;
+    const int64_t t = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * kPer + part;
+    const bool live = t < a.T;
+    float l[NV], p[NV], ds[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = i * 64 + sub;
+        l[i] = live && e < a.E ? route_load(a.logits, a.dtype, t * a.stride + e) : -INFINITY;
+        ds[i] = 0.f;
+    }
+    int e = -1;
+    float dw = 0.f;
+    if (live && sub < a.k) {
+        e = a.experts[t * a.k + sub];
+        if (e < 0 || e >= a.E) e = -1;
+        else dw = a.scale * a.dweights[t * a.k + sub];
+    }
+    route_scores<float, SEG, NV>(l, a.sigmoid, p);
+    float s = 0.f;  // the score of this lane's choice
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const float v = __shfl(p[i], part * SEG + (e & (SEG - 1)));
+        if (e >= 0 && e / 64 == i) s = v;
+    }
+    if (a.renormalise) {
+        const float inv = 1.f / (seg_sum<SEG>(s) + 1e-20f);
+        dw = (dw - seg_sum<SEG>(dw * s) * inv) * inv;
+        if (e < 0) dw = 0.f;
+    }
+    float dot = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+        const int ej = __shfl(e, part * SEG + j);
+        const float dj = __shfl(dw, part * SEG + j);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ej == i * 64 + sub) ds[i] += dj;
+    }
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) dot += ds[i] * p[i];
+        dot = seg_sum<SEG>(dot);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int at = i * 64 + sub;
+        if (!live || at >= a.E) continue;
+        const float d = a.sigmoid ? ds[i] * p[i] * (1.f - p[i]) : p[i] * (ds[i] - dot);
+        const int64_t to = t * a.dstride + at;
+        if (a.dtype == 0) static_cast<__bf16*>(a.dlogits)[to] = (__bf16)d;
+        else if (a.dtype == 1) static_cast<_Float16*>(a.dlogits)[to] = (_Float16)d;
+        else static_cast<float*>(a.dlogits)[to] = d;
+    }
+}
+
+// ---- rows back to tokens -----------------------------------------------------------
+
+struct CombineArgs {
+    const void *y, *dout;
+    const int32_t* slots;
+    const float* weights;
+    void *out, *dy;
+    float* dweights;
+    int64_t T, R, y_stride, out_stride, dout_stride, dy_stride;
+    int N, k;
+};
+
+constexpr int kCombineThreads = 256;
+constexpr int kCombineAhead = 8;  // rows of a token in flight
+
+// A thread sums eight columns of a token's rows; bytes bound it.
+template <class T>
+__global__ __launch_bounds__(kCombineThreads) void combine_kernel(const CombineArgs a)
+{
+    const int64_t t = blockIdx.x;
+    const int col = (blockIdx.y * kCombineThreads + threadIdx.x) * 8;
+    if (col >= a.N) return;
+    float acc[8] = {};
+    for (int j0 = 0; j0 < a.k; j0 += kCombineAhead) {
+        vec8<T> v[kCombineAhead];
+        float w[kCombineAhead];
+        bool has[kCombineAhead];
+#pragma unroll
+        for (int j = 0; j < kCombineAhead; ++j) {
+            const int64_t at = t * a.k + j0 + j;
+            const int slot = j0 + j < a.k ? a.slots[at] : -1;
+            has[j] = slot >= 0 && slot < a.R;
+            w[j] = has[j] && a.weights ? a.weights[at] : 1.f;
+            v[j] = has[j] ? load8(static_cast<const T*>(a.y) + slot * a.y_stride, col, a.N) : vec8<T>{};
+        }
+#pragma unroll
+        for (int j = 0; j < kCombineAhead; ++j)
+            if (has[j]) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w[j], (float)v[j][i], acc[i]);
+            }
+    }
+    store8(static_cast<T*>(a.out) + t * a.out_stride, col, a.N, acc);
+}
+
+// A workgroup takes a token, so that dout is read once for kCombineAhead rows: each is
+// multiplied with it (the weight's gradient) and written as the weight times it.
+template <class T>
+__global__ __launch_bounds__(kCombineThreads) void combine_backward_kernel(const CombineArgs a)
+{
+    __shared__ float part[kCombineThreads / 64][kCombineAhead];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int j0 = 0; j0 < a.k; j0 += kCombineAhead) {
+        int slot[kCombineAhead];
+        float w[kCombineAhead], dot[kCombineAhead];
+#pragma unroll
+        for (int j = 0; j < kCombineAhead; ++j) {
+            const int64_t at = t * a.k + j0 + j;
+            slot[j] = j0 + j < a.k ? a.slots[at] : -1;
+            if (slot[j] >= a.R) slot[j] = -1;
+            w[j] = slot[j] >= 0 && a.weights ? a.weights[at] : 1.f;
+            dot[j] = 0.f;
+        }
+        for (int col = threadIdx.x * 8; col < a.N; col += kCombineThreads * 8) {
+            float d[8];
+            widen<T>(load8(static_cast<const T*>(a.dout) + t * a.dout_stride, col, a.N), d);
+            vec8<T> v[kCombineAhead];
+            if (a.dweights)
+#pragma unroll
+                for (int j = 0; j < kCombineAhead; ++j)
+                    if (slot[j] >= 0) v[j] = load8(static_cast<const T*>(a.y) + slot[j] * a.y_stride, col, a.N);
+#pragma unroll
+            for (int j = 0; j < kCombineAhead; ++j)
+                if (slot[j] >= 0) {
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (a.dweights) dot[j] = __builtin_fmaf(d[i], (float)v[j][i], dot[j]);
+                        f[i] = w[j] * d[i];
+                    }
+                    store8(static_cast<T*>(a.dy) + slot[j] * a.dy_stride, col, a.N, f);
+                }
+        }
+        if (!a.dweights) continue;
+#pragma unroll
+        for (int j = 0; j < kCombineAhead; ++j) {
+            const float sum = wave_sum(dot[j]);
+            if (lane == 0) part[wave][j] = sum;
+        }
+        __syncthreads();
+        const int j = threadIdx.x;
+        if (j < kCombineAhead && j0 + j < a.k) {
+            float sum = 0.f;
+#pragma unroll
+            for (int v = 0; v < kCombineThreads / 64; ++v) sum += part[v][j];
+            a.dweights[t * a.k + j0 + j] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace gemm_rs_layer
