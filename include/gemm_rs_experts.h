@@ -73,7 +73,8 @@ typedef struct gemm_rs_fp8_args {
     const void *w, *w_scales; /* [N][K] in FP8; E of them                            */
     const int32_t *offsets;  /* [E + 1], ascending from 0                            */
     const int32_t *tokens;   /* [M] or NULL                                          */
-    const float *add;        /* [M][N] FP32 or NULL; may be out (F32, same stride)   */
+    const float *add;        /* [M][N] or NULL; with an F32 out, and may be it (of
+                                the same stride)                                     */
     int64_t add_stride;
     void *out;               /* [M][N] */
     int64_t out_stride;
@@ -99,7 +100,7 @@ typedef struct gemm_rs_experts_wgrad_args {
     int64_t x_stride;
     const int32_t *offsets; /* [E + 1]     */
     const int32_t *tokens;  /* [M] or NULL: row m of x */
-    const float *add;       /* [E][N][K] contiguous FP32 or NULL; may be dw (F32) */
+    const float *add;       /* [E][N][K] contiguous or NULL; with an F32 dw, and may be it */
     void *dw;               /* [E][N][K] contiguous */
 } gemm_rs_experts_wgrad_args;
 

@@ -101,6 +101,7 @@ int tile_launch(Fp8Args& a, int device, void* stream)
     a.tiles_m = (int)tiles;
     tiles *= a.tiles_n;
     if (MODE == kSums) tiles *= a.E;
+    tiles = ceil_div(tiles, 8) * 8;
     if (tiles * 256 > kMaxThreads) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     void* p[] = {&a};
     const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fp8_kernel<W, MODE, T>), dim3((unsigned)tiles), dim3(256), p,
@@ -174,7 +175,7 @@ int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t
     if (g->add) c.stride(g->add_stride, g->N);
     c.need(g->out, elem_bytes(g->out_dtype));
     c.stride(g->out_stride, g->N);
-    if (g->add && g->add == g->out && (g->out_dtype != GEMM_RS_DTYPE_F32 || g->add_stride != g->out_stride))
+    if (g->add && (g->out_dtype != GEMM_RS_DTYPE_F32 || (g->add == g->out && g->add_stride != g->out_stride)))
         c.fail(GEMM_RS_ERR_INVALID_ARG);
     const size_t ws = gemm_rs_fp8_workspace(g);
     if (ws > 0) {
@@ -330,7 +331,7 @@ int gemm_rs_experts_wgrad(const gemm_rs_experts_wgrad_args* g, void* workspace, 
     }
     c.maybe(g->add, 4);
     c.need(g->dw, elem_bytes(g->out_dtype));
-    if (g->add && g->add == g->dw && g->out_dtype != GEMM_RS_DTYPE_F32) c.fail(GEMM_RS_ERR_INVALID_ARG);
+    if (g->add && g->out_dtype != GEMM_RS_DTYPE_F32) c.fail(GEMM_RS_ERR_INVALID_ARG);
     const size_t need = gemm_rs_experts_wgrad_workspace(g);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) c.fail(GEMM_RS_ERR_SCRATCH);

@@ -331,19 +331,6 @@ __device__ __forceinline__ void each(F f)
     each_of(std::make_integer_sequence<int, N>(), f);
 }
 
-// Stores eight results of a row from column n on, with what is added to them.
-template <class T>
-__device__ __forceinline__ void fp8_store(const Fp8Args& a, T* out, const float* add, int n, float (&f)[8])
-{
-    if (add) {
-        float g[8];
-        widen<float>(load8(add, n, a.N), g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] += g[j];
-    }
-    store8(out, n, a.N, f);
-}
-
 // Tiles of 64 W x 64 W results by 2 x 2 waves of 32 W x 32 W, steps of 128 inputs, two stages in LDS.
 //   - Stages are loaded into LDS directly, 16-byte chunk c of row r at chunk c ^ (r / 2) % 8:
 //     16 consecutive rows, as the fragments are read, lie in different banks.
@@ -559,6 +546,7 @@ struct Fp8Run {
         if constexpr (EXACT)
 #pragma unroll
             for (int i = 0; i < 2 * W; ++i) widen_piece<0, 0>(0, i);
+        // in twos: a step past the last multiplies the zeros its loads gave
         for (int s = step0; s < step1; s += 2) {
             step<0>(s);
             step<1>(s + 1);
@@ -567,61 +555,111 @@ struct Fp8Run {
     }
 };
 
+// The results of a wave leave through LDS, so that whole lines are stored: 32 rows at a time, 16-byte chunk c of a row at
+// chunk c ^ r.  A lane has 4 W neighbouring columns of a row for each g.  Direct stores of those, 16 bytes in each of 64
+// lines an instruction, took 25 us of a tile's 55.
+// area: the wave's own 32 rows; m0, n0: the wave's first row and column.
+template <int W, class T>
+__device__ __forceinline__ void fp8_store_tile(const Fp8Args& a, char* area, int64_t shift, int64_t m0, int64_t m1, int n0,
+                                               const f32x16 (&acc)[W][W])
+{
+    constexpr int kPer = 16 / sizeof(T);         // elements of a chunk
+    constexpr int kChunks = 32 * W / kPer;       // chunks of a row
+    constexpr int kRows = 64 / kChunks;          // rows of an instruction
+    typedef T chunk_t __attribute__((ext_vector_type(kPer)));
+    typedef T out_t __attribute__((ext_vector_type(kPer), aligned(sizeof(T))));
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5, c = lane % kChunks, n = n0 + c * kPer;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        __asm__ __volatile__("" ::: "memory");  // the LDS operations of a wave complete in order
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int p = 0; p < 4 * W; p += kPer) {
+                chunk_t v;
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) v[q] = (T)acc[i][(p + q) % W][4 * g + (p + q) / W];
+                const int at = (W * (8 * g + 4 * h) + p) / kPer;
+                *reinterpret_cast<chunk_t*>(area + (r * kChunks + (at ^ (r & (kChunks - 1)))) * 16) = v;
+            }
+        __asm__ __volatile__("" ::: "memory");
+#pragma unroll 4
+        for (int k = 0; k < 32 / kRows; ++k) {
+            const int row = k * kRows + lane / kChunks;
+            const int64_t m = m0 + W * row + i;
+            out_t v = *reinterpret_cast<const chunk_t*>(area + (row * kChunks + (c ^ (row & (kChunks - 1)))) * 16);
+            if (m >= m1 || n >= a.N) continue;
+            T* out = static_cast<T*>(a.out) + shift + m * a.out_stride + n;
+            if (n + kPer <= a.N) {
+                if constexpr (fp8_exact<T>)
+                    if (a.add) v += *reinterpret_cast<const out_t*>(a.add + shift + m * a.add_stride + n);
+                *reinterpret_cast<out_t*>(out) = v;
+            } else {
+#pragma unroll
+                for (int q = 0; q < kPer - 1; ++q)
+                    if (n + q < a.N) {
+                        if constexpr (fp8_exact<T>)
+                            if (a.add) v[q] += a.add[shift + m * a.add_stride + n + q];
+                        out[q] = v[q];
+                    }
+            }
+        }
+    }
+    __asm__ __volatile__("" ::: "memory");
+}
+
+// Where tile `id` of tiles_m x tiles_n is: groups of eight tile rows, column by column, so that the 32 tiles an XCD works on
+// at a time share rows of x and of w.
+__device__ __forceinline__ void fp8_place(int id, int tiles_m, int tiles_n, int& tm, int& tn)
+{
+    const int per = 8 * tiles_n, g = id / per, left = tiles_m - 8 * g, rows = left < 8 ? left : 8, r = id - g * per;
+    tm = 8 * g + r % rows;
+    tn = r / rows;
+}
+
 // EXACT: quarters of the fragments are turned to BF16, which holds every scaled value, beside the MFMAs of the quarter before.
 template <int W, int MODE, class T>
 __global__ __launch_bounds__(256, W == 4 ? 1 : 2) void fp8_kernel(const Fp8Args a)
 {
     typedef Fp8Tile<W> Tile;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
-    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+    const int wave = uni(threadIdx.x >> 6);
     int e = 0, n0, s0 = 0, s1 = a.steps;
     int64_t m0, m1 = a.M;
-    const int id = blockIdx.x;
-    if constexpr (MODE == kByExpert || MODE == kGather) {
-        const int tn = id % a.tiles_n;
+    constexpr bool kGrouped = MODE == kByExpert || MODE == kGather;
+    const int tiles_m = kGrouped ? tiles_before(a.offsets, a.E, a.M, Tile::kRows, a.E) : a.tiles_m;
+    // workgroups are dealt to the 8 XCDs in turn: those of one XCD take neighbouring tiles
+    const int all = tiles_m * a.tiles_n * (MODE == kSums ? a.E : 1), per = (all + 7) / 8;
+    int id = (int)blockIdx.x % 8 * per + (int)blockIdx.x / 8;
+    if ((int)blockIdx.x / 8 >= per || id >= all) return;  // the grid is a bound
+    if constexpr (MODE == kSums) {
+        e = id / (tiles_m * a.tiles_n);
+        id %= tiles_m * a.tiles_n;
+        s0 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, e);
+        s1 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, e + 1);
+    }
+    int tm, tn;
+    fp8_place(id, tiles_m, a.tiles_n, tm, tn);
+    n0 = tn * Tile::kRows;
+    if constexpr (kGrouped) {
         RowTile t;
-        if (!find_tile(a.offsets, a.E, a.M, Tile::kRows, id / a.tiles_n, t)) return;
+        if (!find_tile(a.offsets, a.E, a.M, Tile::kRows, tm, t)) return;
         e = t.e;
         m0 = t.m0;
         m1 = t.m1;
-        n0 = tn * Tile::kRows;
-    } else {
-        int t = id;
-        if constexpr (MODE == kSums) {
-            e = id / (a.tiles_m * a.tiles_n);
-            t = id % (a.tiles_m * a.tiles_n);
-            s0 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, e);
-            s1 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, e + 1);
-        }
-        m0 = (int64_t)(t / a.tiles_n) * Tile::kRows;
-        n0 = t % a.tiles_n * Tile::kRows;
-    }
+    } else
+        m0 = (int64_t)tm * Tile::kRows;
     f32x16 acc[W][W];
 #pragma unroll
     for (int i = 0; i < W; ++i)
 #pragma unroll
         for (int j = 0; j < W; ++j) acc[i][j] = f32x16{};
     Fp8Run<W, MODE, fp8_exact<T>>(a, lds, acc, MODE == kSums ? 0 : e, m0, m1, n0, s0, s1).run();
-    const int r = lane & 31, h = lane >> 5;
     const int64_t shift = MODE == kSums ? e * a.out_expert : 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const int64_t m = m0 + (wave >> 1) * 32 * W + W * r + i;
-        if (m >= m1) continue;
-        T* out = static_cast<T*>(a.out) + shift + m * a.out_stride;
-        const float* add = a.add ? a.add + shift + m * a.add_stride : nullptr;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int n = n0 + (wave & 1) * 32 * W + W * (8 * g + 4 * h);  // 4 W columns: W e + j
-#pragma unroll
-            for (int p = 0; p < 4 * W; p += 8) {
-                float f[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) f[q] = acc[i][(p + q) % W][4 * g + (p + q) / W];
-                fp8_store<T>(a, out, add, n + p, f);
-            }
-        }
-    }
+    char* area = lds + wave * (32 * 32 * W * 4);
+    m0 += (wave >> 1) * 32 * W;
+    n0 += (wave & 1) * 32 * W;
+    fp8_store_tile<W, T>(a, area, shift, m0, m1, n0, acc);
 }
 
 // Few rows: a workgroup computes 16 columns for up to 16 MF rows, its waves split the blocks of
@@ -716,7 +754,8 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_few_kernel(const Fp8Args a)
             const int at = n0 + 4 * q + c;
             if (at >= a.N) break;
             float v = s[c];
-            if (a.add) v += a.add[m * a.add_stride + at];
+            if constexpr (fp8_exact<T>)
+                if (a.add) v += a.add[m * a.add_stride + at];
             out[at] = (T)v;
         }
     }

@@ -238,6 +238,8 @@ def _product(name, x, weight, routing, rows, add, out, dtype, stream):
         dtype = x.dtype if raw else torch.bfloat16
     if dtype not in _CODES:
         raise TypeError(f"dtype: expected bfloat16, float16 or float32, got {dtype}")
+    if add is not None and dtype is not torch.float32:
+        raise TypeError(f"add: needs a float32 out, not {dtype}")
     add_stride = 0 if add is None else _rows(add, "add", M, N, torch.float32, dev)
     out_stride = N if out is None else _rows(out, "out", M, N, dtype, dev)
     if stream is not None:
@@ -262,7 +264,7 @@ def fp8_linear(x, weight: Fp8, *, add=None, out=None, dtype=None, stream=None):
     """out [M][N] = x w^T (+ add), FP32 accumulation, rounded once.
 
     x: [M][K] bfloat16, float16 or float32, quantised by the call as fp8_quant does, or an Fp8.  weight: an Fp8 [N][K].
-    add: float32 [M][N] or None.  dtype: of out (default: x's; bfloat16 for an Fp8).  out may be `add` (float32).
+    dtype: of out (default: x's; bfloat16 for an Fp8).  add: float32 [M][N] or None, with a float32 out, which may be it.
     The gradients of y = x w^T: fp8_linear(dy, fp8_pack(w, transpose=True)) and
     fp8_linear(fp8_quant(dy, transpose=True), fp8_quant(x, transpose=True), dtype=torch.float32).
     """
@@ -400,8 +402,8 @@ def experts_linear(x, weight: Fp8, routing: Routing, *, rows=False, add=None, ou
 def experts_wgrad(dy, x, routing: Routing, *, rows=False, add=None, out=None, dtype=torch.float32, stream=None):
     """The weights' gradients [E][N][K] = dy^T x (+ add) of every expert, both in 8 bits in blocks of 128 of its rows.
 
-    dy: [R][N], x: [T][K] or with rows=True [R][K], of one type.  add: float32 [E][N][K], contiguous, or None.
-    dtype: float32 or dy's (out's, if given).  out may be `add` (float32).
+    dy: [R][N], x: [T][K] or with rows=True [R][K], of one type.  dtype: float32 or dy's (out's, if given).
+    add: float32 [E][N][K], contiguous, or None, with a float32 out, which may be it.
     """
     M, N = _two(dy, "dy")
     x_rows, K = _two(x, "x")
@@ -415,6 +417,8 @@ def experts_wgrad(dy, x, routing: Routing, *, rows=False, add=None, out=None, dt
         dtype = out.dtype
     if dtype is not torch.float32 and dtype is not dy.dtype:
         raise TypeError(f"dtype: expected float32 or {dy.dtype}, got {dtype}")
+    if add is not None and dtype is not torch.float32:
+        raise TypeError(f"add: needs a float32 out, not {dtype}")
     if min(N, K) < 1:
         raise ValueError(f"dy, x: no columns in shapes {tuple(dy.shape)}, {tuple(x.shape)}")
     for t, name, kind in ((add, "add", torch.float32), (out, "out", dtype)):

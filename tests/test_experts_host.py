@@ -108,7 +108,8 @@ def test_fp8_workspace():
     (dict(w_scales=0), gr.ERR_INVALID_ARG),
     (dict(x_stride=129), gr.ERR_INVALID_ARG),
     (dict(out_stride=15), gr.ERR_INVALID_ARG),
-    (dict(add=256, add_stride=16), gr.ERR_INVALID_ARG),       # in place needs FP32
+    (dict(add=512, add_stride=16), gr.ERR_INVALID_ARG),       # needs an FP32 result
+    (dict(add=256, add_stride=17, out_dtype=2), gr.ERR_INVALID_ARG),  # in place, of another stride
     (dict(), gr.ERR_SCRATCH),
 ])
 def test_fp8_linear_refuses(kw, code):

@@ -183,8 +183,8 @@ def test_linear_strides_add_and_out(M, N, K):
     assert ex.fp8_linear(x.cuda(), weight, add=main, out=main) is main
     assert torch.equal(f64(main), exact + f64(add))
     base = torch.full((M, N + 9), 99.0, dtype=BF16, device="cuda")
-    ex.fp8_linear(x.bfloat16().cuda(), weight, add=add.cuda(), out=base[:, 1:N + 1])
-    assert torch.equal(base[:, 1:N + 1].cpu(), (exact + f64(add)).to(BF16))
+    ex.fp8_linear(x.bfloat16().cuda(), weight, out=base[:, 1:N + 1])
+    assert torch.equal(base[:, 1:N + 1].cpu(), exact.to(BF16))
     assert (base[:, 0] == 99).all() and (base[:, N + 1:] == 99).all()
 
 
@@ -660,7 +660,11 @@ def test_refusals():
     with pytest.raises(TypeError, match="dtype"):
         ex.fp8_linear(one(4, 16), w, dtype=torch.float64)
     with pytest.raises(TypeError, match="add"):
-        ex.fp8_linear(one(4, 16), w, add=one(4, 8))
+        ex.fp8_linear(one(4, 16), w, add=one(4, 8), dtype=F32)
+    with pytest.raises(TypeError, match="add: needs"):
+        ex.fp8_linear(one(4, 16), w, add=one(4, 8, dtype=F32))
+    with pytest.raises(TypeError, match="add: needs"):
+        ex.experts_wgrad(one(8, 8), one(4, 16), plan, add=one(3, 8, 16, dtype=F32), dtype=BF16)
     with pytest.raises(ValueError, match="side by side"):
         ex.fp8_linear(one(16, 4).t(), w)
     with pytest.raises(ValueError, match="0 experts"):
@@ -700,7 +704,7 @@ def test_gradients_are_not_lost_without_a_word(call):
         "fp8_quant": (lambda x: ex.fp8_quant(x), dict(x=one(4, 16))),
         "fp8_pack": (lambda w: ex.fp8_pack(w), dict(w=one(4, 16))),
         "fp8_linear": (lambda x, add, out: ex.fp8_linear(x, ex.fp8_pack(one(8, 16)), add=add, out=out),
-                       dict(x=one(4, 16), add=one(4, 8, dtype=F32), out=one(4, 8))),
+                       dict(x=one(4, 16), add=one(4, 8, dtype=F32), out=one(4, 8, dtype=F32))),
         "route": (lambda logits, bias: ex.route(logits, 2, bias=bias), dict(logits=one(4, 8), bias=one(8, dtype=F32))),
         "route_backward": (lambda dweights, logits: ex.route_backward(dweights, logits, plan.experts),
                            dict(dweights=one(4, 2, dtype=F32), logits=one(4, 8))),
