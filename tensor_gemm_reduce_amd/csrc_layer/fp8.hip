@@ -88,24 +88,23 @@ int allow_lds(K kernel, int bytes, int device, std::atomic<bool>* allowed)
     return GEMM_RS_OK;
 }
 
-template <int W, int MODE, class T>
-int tile_launch(Fp8Args& a, int device, void* stream)
+template <int W, int NS, int MODE, class T>
+int tile_launch(Fp8Args& a, int64_t tiles_m, int device, void* stream)
 {
-    constexpr int kRows = Fp8Tile<W>::kRows, kLds = Fp8Tile<W>::kLds;
+    typedef Fp8Tile<W, NS, MODE> Tile;
+    constexpr int kRows = Tile::kRows;
     static std::atomic<bool> allowed[kMaxDevices];
-    const int rc = allow_lds(fp8_kernel<W, MODE, T>, kLds, device, allowed);
+    const int rc = allow_lds(fp8_kernel<W, NS, MODE, T>, Tile::kLds, device, allowed);
     if (rc != GEMM_RS_OK) return rc;
     a.tiles_n = (int)ceil_div(a.N, kRows);
-    int64_t tiles = ceil_div(a.M, kRows);
-    if (MODE == kByExpert || MODE == kGather) tiles = a.M / kRows + (a.E < a.M ? a.E : a.M);  // at most one ragged tile an expert
-    a.tiles_m = (int)tiles;
-    tiles *= a.tiles_n;
-    if (MODE == kSums) tiles *= a.E;
-    tiles = ceil_div(tiles, 8) * 8;
-    if (tiles * 256 > kMaxThreads) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    a.tiles_m = (int)tiles_m;
+    int64_t grid = ceil_div(tiles_m * a.tiles_n * (MODE == kSums ? a.E : 1), 8) * 8;
+    if (grid >= int64_t(1) << 31) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;  // tiles are counted in 32 bits
+    if (Tile::kKeeps && grid > kCus) grid = kCus;
+    if (grid * 256 > kMaxThreads) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     void* p[] = {&a};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fp8_kernel<W, MODE, T>), dim3((unsigned)tiles), dim3(256), p,
-                                         kLds, static_cast<hipStream_t>(stream));
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fp8_kernel<W, NS, MODE, T>), dim3((unsigned)grid), dim3(256), p,
+                                         Tile::kLds, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? GEMM_RS_OK : hip_fail(e, "fp8_kernel");
 }
 
@@ -128,8 +127,14 @@ int product(Fp8Args& a, int device, void* stream)
         if (rows <= 32) return few_launch<2, MODE, T>(a, stream);
         if (rows <= 64) return few_launch<4, MODE, T>(a, stream);
     }
-    const int64_t tiles = ceil_div(a.M, 256) * ceil_div(a.N, 256) * (MODE == kSums ? a.E : 1);
-    return tiles >= kCus ? tile_launch<4, MODE, T>(a, device, stream) : tile_launch<2, MODE, T>(a, device, stream);
+    // rows of tiles: exact, or at most one ragged tile an expert
+    auto rows_of = [&](int64_t edge) {
+        return MODE == kByExpert || MODE == kGather ? a.M / edge + (a.E < a.M ? a.E : a.M) : ceil_div(a.M, edge);
+    };
+    auto tiles = [&](int64_t edge) { return rows_of(edge) * ceil_div(a.N, edge) * (MODE == kSums ? a.E : 1); };
+    if (tiles(256) >= kCus) return tile_launch<4, 2, MODE, T>(a, rows_of(256), device, stream);
+    return tiles(128) > kCus ? tile_launch<2, 2, MODE, T>(a, rows_of(128), device, stream)
+                             : tile_launch<2, 4, MODE, T>(a, rows_of(128), device, stream);
 }
 
 template <int MODE>

@@ -331,67 +331,98 @@ __device__ __forceinline__ void each(F f)
     each_of(std::make_integer_sequence<int, N>(), f);
 }
 
-// Tiles of 64 W x 64 W results by 2 x 2 waves of 32 W x 32 W, steps of 128 inputs, two stages in LDS.
-//   - Stages are loaded into LDS directly, 16-byte chunk c of row r at chunk c ^ (r / 2) % 8:
-//     16 consecutive rows, as the fragments are read, lie in different banks.
-//   - A wave's LDS row 32 i + r holds matrix row W r + i: the W fragments of a lane then
-//     belong to W neighbouring rows, whose scales are one load, and the MFMA picks the byte.
-//     w is the MFMA's first operand, so a lane ends with 4 W neighbouring columns of a row.
-//   - A step has two halves of 64 inputs.  While the first is multiplied, the second's
-//     fragments are read; then the next stage has to have come, and a barrier frees this one;
-//     while the second is multiplied, the stage is filled again (a step's time to arrive) and
-//     the next step's first fragments are read.
-template <int W>
+// Tiles of 64 W x 64 W results by 2 x 2 waves of 32 W x 32 W, in steps of 128 inputs, NS stages in LDS.
+//   - Stages are loaded into LDS directly, 16-byte chunk c of row r at chunk c ^ r / 2 % 8: 16 consecutive rows, as the
+//     fragments are read, lie in different banks.
+//   - A wave's LDS row 32 i + r holds matrix row W r + i: the W fragments of a lane then belong to W neighbouring rows,
+//     whose scales are one load, and the MFMA picks the byte.  w is the MFMA's first operand, so a lane ends with 4 W
+//     neighbouring columns of a row.
+//   - A step has two halves of 64 inputs.  While the first is multiplied, the second's fragments are read; then the next
+//     step's stage has to have come, and a barrier frees this one; while the second is multiplied, this stage is filled
+//     for step s + NS and the next step's first fragments are read.
+// W = 4, NS = 2: one workgroup per CU, whose waves have 256 accumulators each.  What bounds it is the matrix instructions
+//   at the clock that the power limit leaves (79% of the cycles at 1.8 GHz in 8192^3).  Half steps in four stages, with
+//   more time for a load to arrive, but half lines a request, are 6% slower (8192^3: 393 / 417 us).  It keeps its
+//   workgroups for all tiles: the next tile's first stages are on their way before a tile's results are stored.
+// W = 2, NS = 2: two workgroups per CU.  LDS bounds it (96 KB a step against 256 cycles of MFMAs).
+// W = 2, NS = 4: for products of no more tiles than CUs, where a workgroup has the CU to itself and its loads' latency
+//   would bound it (501 x 7168 x 8192: 48 us with two stages).
+template <int W, int NS, int MODE>
 struct Fp8Tile {
     static constexpr int kRows = 64 * W;
     static constexpr int kOperand = kRows * kFp8Block;
     static constexpr int kStage = 2 * kOperand;
-    static constexpr int kLds = 2 * kStage;
+    static constexpr bool kKeeps = W == 4;       // workgroups stay for all tiles
+    static constexpr int kArea = 4096;           // of a wave's results on their way out
+    static constexpr int kOut = kKeeps ? NS * kStage : 0;              // where the areas begin
+    static constexpr int kScale = NS * kStage + (kKeeps ? 4 * kArea : 0);  // and the scales: [wave][stage][1 + W][64 lanes]
+    static constexpr int kScaleStage = 256 * (MODE == kGather ? 1 + W : 2);
+    static constexpr int kLds = kScale + 4 * NS * kScaleStage;
 };
 
-template <int W, int MODE, bool EXACT>
+struct Fp8Place {
+    int e, n0, s0, s1;  // expert, first column, steps
+    int64_t m0, m1;     // first row, end of rows
+};
+
+template <int W, int NS, int MODE, bool EXACT>
 struct Fp8Run {
-    typedef Fp8Tile<W> Tile;
+    typedef Fp8Tile<W, NS, MODE> Tile;
     static constexpr int kLoads = 2 * W;  // a thread's, of an operand and stage
+    static constexpr int kScales = MODE == kGather ? 1 + W : 2;  // loads of a step's scales
+    static constexpr int kStep = 2 * kLoads + kScales;
     static constexpr int kMf = W * W;     // MFMAs of a half step, or (EXACT) of a quarter of it
 
     const Fp8Args& a;
-    char* const lds;
+    char *const lds, *put, *put_scales;  // where the wave's loads of a stage begin, and of its scales
     f32x16 (&acc)[W][W];  // [row of x][row of w]
-    i32x8 fx[2][W], fw[2][W];
+    i32x4 f[2][2 * W][2];  // fragments of w, then of x, in two chunks
     bf16x8 wide[2][EXACT ? 2 * W : 1];  // a quarter of a half step: w's, then x's
-    int sx[2][MODE == kGather ? W : 1], sw[2];
+    int sx[2][MODE == kGather ? W : 1], sw[2];  // scales of an even and an odd step
     uint32_t xo[MODE == kGather ? kLoads : 1], wo;  // a thread's chunk of a stage, first or of each load
     uint32_t sxo[MODE == kGather ? W : 1], swo;
-    uint32_t get[2][4];  // LDS offsets of the lane's chunks: operand, chunk (of the first stage)
+    uint32_t get[2][4];  // LDS offsets of the lane's chunks of the first stage: operand, chunk
     __amdgpu_buffer_rsrc_t rx, rw, rsx, rsw;
     int step0, step1;
 
-    // rows m0 .. m1 - 1 of x, columns n0 .. of the result, steps s0 .. s1 - 1
-    __device__ __forceinline__ Fp8Run(const Fp8Args& args, char* l, f32x16 (&c)[W][W], int e, int64_t m0, int64_t m1, int n0,
-                                      int s0, int s1)
-        : a(args), lds(l), acc(c), step0(s0), step1(s1)
+    __device__ __forceinline__ Fp8Run(const Fp8Args& args, char* l, f32x16 (&c)[W][W]) : a(args), lds(l), acc(c)
     {
-        const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
-        const int wm = wave >> 1, wn = wave & 1;
+        const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), r = lane & 31, h = lane >> 5;
+        put = l + wave * 1024;
+        put_scales = l + Tile::kScale + wave * NS * Tile::kScaleStage;
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {  // chunks of half c4 / 2 of a step: 2 h + c4 % 2
+            const int at = (4 * (c4 / 2) + 2 * h + c4 % 2) ^ (r / 2 % 8);
+            get[0][c4] = ((wave >> 1) * 32 * W + r) * kFp8Block + at * 16;
+            get[1][c4] = Tile::kOperand + ((wave & 1) * 32 * W + r) * kFp8Block + at * 16;
+        }
+    }
+    __device__ __forceinline__ void setup(const Fp8Place& p)
+    {
+        int tid = threadIdx.x;
+        __asm__ __volatile__("" : "+v"(tid));  // keeps what follows from being held in registers over all tiles
+        const int lane = tid & 63, wave = uni(tid >> 6), wm = wave >> 1, wn = wave & 1;
+        // load j: LDS row 32 j + tid / 8, so matrix row `row` + rows_of(j)
         const int chunk = (tid % 8) ^ (tid / 16 % 8), row = W * (tid / 8);
-        const int nrows = (int)(a.N - n0 < Tile::kRows ? a.N - n0 : Tile::kRows);
-        const int mrows = (int)(m1 - m0 < Tile::kRows ? m1 - m0 : Tile::kRows);
-        rw = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + e * a.w_expert + n0 * a.w_pitch), 0, (int)(nrows * a.w_pitch),
+        const int nrows = (int)(a.N - p.n0 < Tile::kRows ? a.N - p.n0 : Tile::kRows);
+        const int mrows = (int)(p.m1 - p.m0 < Tile::kRows ? p.m1 - p.m0 : Tile::kRows);
+        const int e = MODE == kSums ? 0 : p.e;
+        step0 = p.s0;
+        step1 = p.s1;
+        rw = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + e * a.w_expert + p.n0 * a.w_pitch), 0, (int)(nrows * a.w_pitch),
                                                kRsrcFlags);
         wo = (uint32_t)row * (uint32_t)a.w_pitch + chunk * 16;
-        const uint8_t* ws = a.ws + e * a.ws_expert;
-        rsw = __builtin_amdgcn_make_buffer_rsrc((void*)ws, 0, (int)a.ws_bytes, kRsrcFlags);
-        swo = n0 + wn * 32 * W + W * (lane & 31);
+        rsw = __builtin_amdgcn_make_buffer_rsrc((void*)(a.ws + e * a.ws_expert), 0, (int)a.ws_bytes, kRsrcFlags);
+        swo = p.n0 + wn * 32 * W + W * (lane & 31);
         if constexpr (MODE == kGather) {
             rx = __builtin_amdgcn_make_buffer_rsrc((void*)a.x, 0, (int)(a.x_rows * a.x_pitch), kRsrcFlags);
             auto token = [&](int r) {
-                const int t = r < mrows ? a.tokens[m0 + r] : -1;
+                const int t = r < mrows ? a.tokens[p.m0 + r] : -1;
                 return t < a.x_rows ? t : -1;
             };
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
-                const int t = token(row + j / W * 32 * W + j % W);
+                const int t = token(row + rows_of(j));
                 xo[j] = t >= 0 ? (uint32_t)t * (uint32_t)a.x_pitch + chunk * 16 : kOob;
             }
 #pragma unroll
@@ -400,57 +431,70 @@ struct Fp8Run {
                 sxo[i] = t >= 0 ? t : kOob;
             }
         } else {
-            rx = __builtin_amdgcn_make_buffer_rsrc((void*)(a.x + m0 * a.x_pitch), 0, (int)(mrows * a.x_pitch), kRsrcFlags);
+            rx = __builtin_amdgcn_make_buffer_rsrc((void*)(a.x + p.m0 * a.x_pitch), 0, (int)(mrows * a.x_pitch), kRsrcFlags);
             xo[0] = (uint32_t)row * (uint32_t)a.x_pitch + chunk * 16;
-            sxo[0] = (uint32_t)m0 + wm * 32 * W + W * (lane & 31);
+            sxo[0] = (uint32_t)p.m0 + wm * 32 * W + W * (lane & 31);
         }
         rsx = __builtin_amdgcn_make_buffer_rsrc((void*)a.xs, 0, (int)a.xs_bytes, kRsrcFlags);
-        const int r = lane & 31, h = lane >> 5, turn = r / 2 % 8;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {  // chunks of the half c / 2 of a step: 2 h + c % 2
-            const int at = (4 * (c / 2) + 2 * h + c % 2) ^ turn;
-            get[0][c] = (wm * 32 * W + r) * kFp8Block + at * 16;
-            get[1][c] = Tile::kOperand + (wn * 32 * W + r) * kFp8Block + at * 16;
-        }
     }
-    // Load j of the 2 kLoads of step s into stage P.
-    template <int P>
-    __device__ __forceinline__ void load(int j, int s) const
+    static constexpr __device__ int rows_of(int j) { return j / W * 32 * W + j % W; }
+    // Load j of the 2 kLoads of inputs k .. k + 127 into stage Q; skip: past() of the step.
+    template <int Q>
+    __device__ __forceinline__ void load(int j, int k, uint32_t skip) const
     {
         const bool w = j >= kLoads;
         const int i = w ? j - kLoads : j;
-        const uint32_t at = (uint32_t)(i / W * 32 * W + i % W);  // rows from the thread's first
-        const uint32_t off = (w ? wo + at * (uint32_t)a.w_pitch : MODE == kGather ? xo[i % (MODE == kGather ? kLoads : 1)]
-                                                                                  : xo[0] + at * (uint32_t)a.x_pitch) | past(s);
-        const int wave = uni(threadIdx.x >> 6);
-        lds_void_t* to = (lds_void_t*)(lds + P * Tile::kStage + (w ? Tile::kOperand : 0) + (i * 256 + wave * 64) * 16);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(w ? rw : rx, to, 16, off, s * kFp8Block, 0, 0);
+        const uint32_t off = (w ? wo + (uint32_t)rows_of(i) * (uint32_t)a.w_pitch
+                              : MODE == kGather ? xo[i % (MODE == kGather ? kLoads : 1)]
+                                                : xo[0] + (uint32_t)rows_of(i) * (uint32_t)a.x_pitch) | skip;
+        lds_void_t* to = (lds_void_t*)(put + Q * Tile::kStage + (w ? Tile::kOperand : 0) + i * 4096);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(w ? rw : rx, to, 16, off, k, 0, 0);
     }
     // an offset past every resource for steps past the last, which then read zeros: a mask, no select that might
     // become one per lane
     __device__ __forceinline__ uint32_t past(int s) const { return ~(uint32_t)uni((s - step1) >> 31) & kOob; }
-    template <int P>
-    __device__ __forceinline__ void load_scales(int s)
+    // The scales go through LDS too, a dword for each lane: in registers, the compiler would wait for them, and so for
+    // everything before them, by its own count.
+    template <int Q>
+    __device__ __forceinline__ void load_scales(int s) const
     {
-        auto get_w = [&](const __amdgpu_buffer_rsrc_t& r, uint32_t off, int pitch) -> int {
-            if constexpr (W == 4) return (int)__builtin_amdgcn_raw_buffer_load_b32(r, off | past(s), s * pitch, 0);
-            else return (int)__builtin_amdgcn_raw_buffer_load_b16(r, off | past(s), s * pitch, 0);
+        const uint32_t skip = past(s);
+        const int kw = s * a.ws_pitch, kx = s * a.xs_pitch;
+        auto load = [&](const __amdgpu_buffer_rsrc_t& r, uint32_t off, int k, int slot) {
+            lds_void_t* to = (lds_void_t*)(put_scales + Q * Tile::kScaleStage + slot * 256);
+            if constexpr (W == 4) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 4, off, k, 0, 0);
+            else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 2, off, k, 0, 0);
         };
-        sw[P] = get_w(rsw, swo, a.ws_pitch);
+        load(rsw, swo | skip, kw, 0);
         if constexpr (MODE == kGather) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) sx[P][i] = __builtin_amdgcn_raw_buffer_load_b8(rsx, sxo[i] | past(s), s * a.xs_pitch, 0);
+            for (int i = 0; i < W; ++i) {
+                lds_void_t* to = (lds_void_t*)(put_scales + Q * Tile::kScaleStage + (1 + i) * 256);
+                const uint32_t off = sxo[i] | skip;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsx, to, 1, off, kx, 0, 0);
+            }
         } else
-            sx[P][0] = get_w(rsx, sxo[0], a.xs_pitch);
+            load(rsx, sxo[0] | skip, kx, 1);
+        __builtin_amdgcn_sched_barrier(0);  // the waits count them
     }
-    // fragment i of half u of the stage P
-    template <int P>
-    __device__ __forceinline__ i32x8 read(int u, int i, bool w) const
+    template <int Q>
+    __device__ __forceinline__ void read_scales()
     {
-        const char* p = lds + P * Tile::kStage + i * 32 * kFp8Block;
-        const i32x4 lo = *reinterpret_cast<const i32x4*>(p + get[w][2 * u]);
-        const i32x4 hi = *reinterpret_cast<const i32x4*>(p + get[w][2 * u + 1]);
-        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        const char* p = put_scales + Q * Tile::kScaleStage + (threadIdx.x & 63) * 4;
+        sw[Q & 1] = *reinterpret_cast<const int*>(p);
+#pragma unroll
+        for (int i = 0; i < (MODE == kGather ? W : 1); ++i) sx[Q & 1][i] = *reinterpret_cast<const int*>(p + (1 + i) * 256);
+    }
+    // chunk c of half u of fragment i (w's, then x's) of stage Q
+    template <int Q>
+    __device__ __forceinline__ i32x4 read(int u, int i, int c) const
+    {
+        return *reinterpret_cast<const i32x4*>(lds + Q * Tile::kStage + i % W * 32 * kFp8Block + get[i < W][2 * u + c]);
+    }
+    template <int U>
+    __device__ __forceinline__ i32x8 fragment(int i) const
+    {
+        return __builtin_shufflevector(f[U][i][0], f[U][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
     }
     // piece i (w's, then x's) of quarter q of half U in BF16, scaled
     template <int U, int P>
@@ -458,9 +502,17 @@ struct Fp8Run {
     {
         const bool w = i < W;
         const int t = w ? i : i - W;
-        const uint32_t s = w ? (uint32_t)sw[P] >> (8 * t) : MODE == kGather ? (uint32_t)sx[P][MODE == kGather ? t : 0]
-                                                                            : (uint32_t)sx[P][0] >> (8 * t);
-        wide[q & 1][i] = fp8_to_bf16(w ? fw[U][t] : fx[U][t], q, fp8_scale(s));
+        const uint32_t s = w ? (uint32_t)sw[P & 1] >> (8 * t) : MODE == kGather ? (uint32_t)sx[P & 1][MODE == kGather ? t : 0]
+                                                                                : (uint32_t)sx[P & 1][0] >> (8 * t);
+        wide[q & 1][i] = fp8_to_bf16(fragment<U>(i), q, fp8_scale(s));
+    }
+    // the same piece of the quarter after q
+    template <int U, int P>
+    __device__ __forceinline__ void widen_next(int q, int piece)
+    {
+        if (q < 3) widen_piece<U, P>(q + 1, piece);
+        else if (U == 0) widen_piece<1, P>(0, piece);
+        else widen_piece<0, (P + 1) % NS>(0, piece);
     }
     // MFMA M of half U of a step on stage P
     template <int U, int P, int M>
@@ -470,30 +522,24 @@ struct Fp8Run {
         if constexpr (EXACT) {
             constexpr int q = M / kMf, piece = M % kMf;
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wide[q & 1][j], wide[q & 1][W + i], acc[i][j], 0, 0, 0);
-            if constexpr (kMf >= 2 * W) {
-                if constexpr (piece < 2 * W) widen_next<U, P>(q, piece);
-            } else {
-                widen_next<U, P>(q, piece);
-            }
+            if constexpr (piece < 2 * W) widen_next<U, P>(q, piece);
         } else if constexpr (MODE == kGather)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[U][j], fx[U][i], acc[i][j], 0, 0, j, sw[P], 0,
-                                                                         sx[P][i]);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fragment<U>(j), fragment<U>(W + i), acc[i][j], 0, 0, j,
+                                                                         sw[P & 1], 0, sx[P & 1][i]);
         else
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[U][j], fx[U][i], acc[i][j], 0, 0, j, sw[P], i,
-                                                                         sx[P][0]);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fragment<U>(j), fragment<U>(W + i), acc[i][j], 0, 0, j,
+                                                                         sw[P & 1], i, sx[P & 1][0]);
     }
-    // the same piece of the quarter after q
-    template <int U, int P>
-    __device__ __forceinline__ void widen_next(int q, int piece)
+    // This wave's LDS reads have ended, and its memory instructions but the last LEFT; the wait is a builtin: the compiler
+    // then knows.
+    template <int LEFT>
+    static __device__ __forceinline__ void wait()
     {
-        if (q < 3) widen_piece<U, P>(q + 1, piece);
-        else if (U == 0) widen_piece<1, P>(0, piece);
-        else widen_piece<0, P ^ 1>(0, piece);
+        constexpr int n = LEFT < 63 ? LEFT : 63;
+        __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 7 << 4);
     }
-    // this wave's LDS reads and loads have ended, then everybody's
     static __device__ __forceinline__ void barrier()
     {
-        __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0), as a builtin: the compiler then knows
         __asm__ __volatile__("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     }
@@ -505,161 +551,241 @@ struct Fp8Run {
 #pragma unroll
         for (int c = 0; c < 4; ++c) __asm__ __volatile__("" : "+v"(get[0][c]), "+v"(get[1][c]));
     }
-    template <int P>
-    __device__ __forceinline__ void step(int s)
+    // Step s on stage P.  STORES: those that may still be on their way, issued behind the loads of the step after it.
+    template <int P, int STORES>
+    __device__ __forceinline__ void step(int s, bool stores)
     {
-        constexpr int kAll = EXACT ? 4 * kMf : kMf, kPer = 4 * W / kMf;  // loads beside an MFMA
+        constexpr int kAll = EXACT ? 4 * kMf : kMf, kReads = 4 * W, kPer = 2;  // reads beside an MFMA
         hide();
         each<kAll>([&](auto m) {
             constexpr int M = decltype(m)::value;
             multiply<0, P, M>();
-            if constexpr (M < W) fw[1][M] = read<P>(1, M, true);
-            else if constexpr (M < 2 * W) fx[1][M - W] = read<P>(1, M - W, false);
+#pragma unroll
+            for (int i = kPer * M; i < kPer * (M + 1) && i < kReads; ++i) f[1][i / 2][i % 2] = read<P>(1, i / 2, i % 2);
             __builtin_amdgcn_sched_barrier(0);
         });
+        if (STORES > 0 && stores) wait<(NS - 2) * kStep + STORES>();
+        else wait<(NS - 2) * kStep>();
         barrier();
+        read_scales<(P + 1) % NS>();
+        const uint32_t skip = past(s + NS);
+        const int at = (s + NS) * kFp8Block;
         each<kAll>([&](auto m) {
             constexpr int M = decltype(m)::value;
             multiply<1, P, M>();
 #pragma unroll
-            for (int j = kPer * M; j < kPer * (M + 1) && j < 4 * W; ++j) load<P>(j, s + 2);
-            if constexpr (M < W) fw[0][M] = read<P ^ 1>(0, M, true);
-            else if constexpr (M < 2 * W) fx[0][M - W] = read<P ^ 1>(0, M - W, false);
+            for (int i = M * 2 * kLoads / kMf; i < (M + 1) * 2 * kLoads / kMf && i < 2 * kLoads; ++i) load<P>(i, at, skip);
+#pragma unroll
+            for (int i = kPer * M; i < kPer * (M + 1) && i < kReads; ++i) f[0][i / 2][i % 2] = read<(P + 1) % NS>(0, i / 2, i % 2);
             __builtin_amdgcn_sched_barrier(0);
         });
-        load_scales<P>(s + 2);
+        load_scales<P>(s + NS);
     }
-    __device__ __forceinline__ void run()
+    // The first NS stages, in the order that the waits count.
+    __device__ __forceinline__ void fill()
     {
+        each<NS>([&](auto q) {
+            constexpr int Q = decltype(q)::value;
+            const int at = (step0 + Q) * kFp8Block;
+            const uint32_t skip = past(step0 + Q);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < 2 * kLoads; ++j) load<0>(j, step0);
-        load_scales<0>(step0);
-#pragma unroll
-        for (int j = 0; j < 2 * kLoads; ++j) load<1>(j, step0 + 1);
-        load_scales<1>(step0 + 1);
+            for (int j = 0; j < 2 * kLoads; ++j) load<Q>(j, at, skip);
+            __builtin_amdgcn_sched_barrier(0);
+            load_scales<Q>(step0 + Q);
+        });
+    }
+    // All steps, behind fill(); stores: STORES stores have been issued since.
+    template <int STORES>
+    __device__ __forceinline__ void run(bool stores)
+    {
+        if (STORES > 0 && stores) wait<(NS - 1) * kStep + STORES>();
+        else wait<(NS - 1) * kStep>();
         barrier();
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            fw[0][i] = read<0>(0, i, true);
-            fx[0][i] = read<0>(0, i, false);
-        }
+        for (int i = 0; i < 4 * W; ++i) f[0][i / 2][i % 2] = read<0>(0, i / 2, i % 2);
+        read_scales<0>();
         if constexpr (EXACT)
 #pragma unroll
             for (int i = 0; i < 2 * W; ++i) widen_piece<0, 0>(0, i);
         // in twos: a step past the last multiplies the zeros its loads gave
-        for (int s = step0; s < step1; s += 2) {
-            step<0>(s);
-            step<1>(s + 1);
+        for (int s = step0; s < step1; s += NS) {
+            step<0, STORES>(s, stores && s == step0);
+            step<1, 0>(s + 1, false);
+            if constexpr (NS == 4) {
+                if (s + 2 >= step1) break;
+                step<2, 0>(s + 2, false);
+                step<3, 0>(s + 3, false);
+            }
         }
+        wait<0>();
         barrier();
     }
 };
 
-// The results of a wave leave through LDS, so that whole lines are stored: 32 rows at a time, 16-byte chunk c of a row at
-// chunk c ^ r.  A lane has 4 W neighbouring columns of a row for each g.  Direct stores of those, 16 bytes in each of 64
-// lines an instruction, took 25 us of a tile's 55.
-// area: the wave's own 32 rows; m0, n0: the wave's first row and column.
-template <int W, class T>
-__device__ __forceinline__ void fp8_store_tile(const Fp8Args& a, char* area, int64_t shift, int64_t m0, int64_t m1, int n0,
-                                               const f32x16 (&acc)[W][W])
+// The results of a wave leave through LDS, so that whole lines are stored: 128 bytes of 32 rows at a time, 16-byte chunk c of
+// a row at chunk c ^ r.  A lane has 4 W neighbouring columns of a row for each g.  Direct stores of those, 16 bytes in
+// each of 64 lines an instruction, took 8 us more for each tile of 256 x 256.
+// Stored past the caches, which hold x and w for the tiles to come: 32768 x 8192 x 3584 803 us without, 767 with; the
+// gradients of 64 experts' weights, 738 MB in FP32, 429 and 341.
+// area: the wave's own 4 KB; m0, n0: the wave's first row and column.  FULL: no row or column past the end, so that every
+// wave has the same number of stores.
+// Accumulators stay where they are, in AGPRs and in one piece: the compiler otherwise takes them apart on the way from the
+// loop to the stores, and keeps parts of them in scratch memory.
+template <int W>
+__device__ __forceinline__ void fp8_hold(f32x16 (&acc)[W])
 {
-    constexpr int kPer = 16 / sizeof(T);         // elements of a chunk
-    constexpr int kChunks = 32 * W / kPer;       // chunks of a row
-    constexpr int kRows = 64 / kChunks;          // rows of an instruction
-    typedef T chunk_t __attribute__((ext_vector_type(kPer)));
-    typedef T out_t __attribute__((ext_vector_type(kPer), aligned(sizeof(T))));
-    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5, c = lane % kChunks, n = n0 + c * kPer;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        __asm__ __volatile__("" ::: "memory");  // the LDS operations of a wave complete in order
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int p = 0; p < 4 * W; p += kPer) {
-                chunk_t v;
-#pragma unroll
-                for (int q = 0; q < kPer; ++q) v[q] = (T)acc[i][(p + q) % W][4 * g + (p + q) / W];
-                const int at = (W * (8 * g + 4 * h) + p) / kPer;
-                *reinterpret_cast<chunk_t*>(area + (r * kChunks + (at ^ (r & (kChunks - 1)))) * 16) = v;
-            }
-        __asm__ __volatile__("" ::: "memory");
-#pragma unroll 4
-        for (int k = 0; k < 32 / kRows; ++k) {
-            const int row = k * kRows + lane / kChunks;
-            const int64_t m = m0 + W * row + i;
-            out_t v = *reinterpret_cast<const chunk_t*>(area + (row * kChunks + (c ^ (row & (kChunks - 1)))) * 16);
-            if (m >= m1 || n >= a.N) continue;
-            T* out = static_cast<T*>(a.out) + shift + m * a.out_stride + n;
-            if (n + kPer <= a.N) {
-                if constexpr (fp8_exact<T>)
-                    if (a.add) v += *reinterpret_cast<const out_t*>(a.add + shift + m * a.add_stride + n);
-                *reinterpret_cast<out_t*>(out) = v;
-            } else {
-#pragma unroll
-                for (int q = 0; q < kPer - 1; ++q)
-                    if (n + q < a.N) {
-                        if constexpr (fp8_exact<T>)
-                            if (a.add) v[q] += a.add[shift + m * a.add_stride + n + q];
-                        out[q] = v[q];
-                    }
-            }
-        }
-    }
-    __asm__ __volatile__("" ::: "memory");
+    for (int j = 0; j < W; ++j) __asm__ __volatile__("" : "+a"(acc[j]));
 }
 
-// Where tile `id` of tiles_m x tiles_n is: groups of eight tile rows, column by column, so that the 32 tiles an XCD works on
-// at a time share rows of x and of w.
+template <int W, class T>
+struct Fp8Store {
+    static constexpr int kPer = 16 / sizeof(T);    // elements of a chunk
+    static constexpr int kCols = 128 / sizeof(T);  // columns at a time
+    static constexpr int kChunks = 8;              // of a row
+    static constexpr int kRows = 64 / kChunks;     // rows of an instruction
+    static constexpr int kStores = W * (32 * W / kCols) * (32 / kRows);
+    typedef T chunk_t __attribute__((ext_vector_type(kPer)));
+    typedef T out_t __attribute__((ext_vector_type(kPer), aligned(sizeof(T))));
+
+    template <bool FULL>
+    static __device__ __forceinline__ void run(const Fp8Args& a, char* area, int64_t shift, int64_t m0, int64_t m1, int n0,
+                                               f32x16 (&acc)[W][W])
+    {
+        int lane = threadIdx.x & 63;
+        __asm__ __volatile__("" : "+v"(lane));  // keeps the addresses from being held in registers over all tiles
+        const int r = lane & 31, h = lane >> 5, c = lane % kChunks;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (W == 4) fp8_hold<W>(acc[i]);
+#pragma unroll
+            for (int c0 = 0; c0 < 32 * W; c0 += kCols) {
+                __asm__ __volatile__("" ::: "memory");  // the LDS operations of a wave complete in order
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int g = c0 / (8 * W); g < (c0 + kCols) / (8 * W); ++g)
+#pragma unroll
+                    for (int p = 0; p < 4 * W; p += kPer) {
+                        chunk_t v;
+#pragma unroll
+                        for (int q = 0; q < kPer; ++q) v[q] = (T)acc[i][(p + q) % W][4 * g + (p + q) / W];
+                        const int at = (W * (8 * g + 4 * h) - c0 + p) / kPer;
+                        *reinterpret_cast<chunk_t*>(area + (r * kChunks + (at ^ (r & (kChunks - 1)))) * 16) = v;
+                    }
+                __asm__ __volatile__("" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+                const int n = n0 + c0 + c * kPer;
+#pragma unroll
+                for (int k = 0; k < 32 / kRows; ++k) {
+                    const int row = k * kRows + lane / kChunks;
+                    const int64_t m = m0 + W * row + i;
+                    out_t v = *reinterpret_cast<const chunk_t*>(area + (row * kChunks + (c ^ (row & (kChunks - 1)))) * 16);
+                    if (!FULL && (m >= m1 || n >= a.N)) continue;
+                    T* out = static_cast<T*>(a.out) + shift + m * a.out_stride + n;
+                    if (FULL || n + kPer <= a.N) {
+                        if constexpr (fp8_exact<T>)
+                            if (a.add) v += *reinterpret_cast<const out_t*>(a.add + shift + m * a.add_stride + n);
+                        __builtin_nontemporal_store(v, reinterpret_cast<out_t*>(out));
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < kPer - 1; ++q)
+                            if (n + q < a.N) {
+                                if constexpr (fp8_exact<T>)
+                                    if (a.add) v[q] += a.add[shift + m * a.add_stride + n + q];
+                                out[q] = v[q];
+                            }
+                    }
+                }
+            }
+        }
+        __asm__ __volatile__("" ::: "memory");
+    }
+};
+
+// Where tile `id` of tiles_m x tiles_n is: groups of four tile rows, column by column, so that the 32 tiles an XCD works on
+// at a time share rows of x and of w, and the group's rows of x (3.7 MB at 3584 inputs) stay in its L2 while the columns go
+// by: 32768 x 8192 x 3584 takes 816 / 798 / 870 us with groups of 3 / 4 / 8, 8192^3 402 / 391 / 391.
 __device__ __forceinline__ void fp8_place(int id, int tiles_m, int tiles_n, int& tm, int& tn)
 {
-    const int per = 8 * tiles_n, g = id / per, left = tiles_m - 8 * g, rows = left < 8 ? left : 8, r = id - g * per;
-    tm = 8 * g + r % rows;
+    const int per = 4 * tiles_n, g = id / per, left = tiles_m - 4 * g, rows = left < 4 ? left : 4, r = id - g * per;
+    tm = 4 * g + r % rows;
     tn = r / rows;
 }
 
 // EXACT: quarters of the fragments are turned to BF16, which holds every scaled value, beside the MFMAs of the quarter before.
-template <int W, int MODE, class T>
-__global__ __launch_bounds__(256, W == 4 ? 1 : 2) void fp8_kernel(const Fp8Args a)
+template <int W, int NS, int MODE, class T>
+__global__ __launch_bounds__(256, W == 4 || NS == 4 ? 1 : 2) void fp8_kernel(const Fp8Args a)
 {
-    typedef Fp8Tile<W> Tile;
+    typedef Fp8Tile<W, NS, MODE> Tile;
+    typedef Fp8Store<W, T> Store;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
-    const int wave = uni(threadIdx.x >> 6);
-    int e = 0, n0, s0 = 0, s1 = a.steps;
-    int64_t m0, m1 = a.M;
     constexpr bool kGrouped = MODE == kByExpert || MODE == kGather;
+    const int wave = uni(threadIdx.x >> 6);
     const int tiles_m = kGrouped ? tiles_before(a.offsets, a.E, a.M, Tile::kRows, a.E) : a.tiles_m;
     // workgroups are dealt to the 8 XCDs in turn: those of one XCD take neighbouring tiles
-    const int all = tiles_m * a.tiles_n * (MODE == kSums ? a.E : 1), per = (all + 7) / 8;
-    int id = (int)blockIdx.x % 8 * per + (int)blockIdx.x / 8;
-    if ((int)blockIdx.x / 8 >= per || id >= all) return;  // the grid is a bound
-    if constexpr (MODE == kSums) {
-        e = id / (tiles_m * a.tiles_n);
-        id %= tiles_m * a.tiles_n;
-        s0 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, e);
-        s1 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, e + 1);
-    }
-    int tm, tn;
-    fp8_place(id, tiles_m, a.tiles_n, tm, tn);
-    n0 = tn * Tile::kRows;
-    if constexpr (kGrouped) {
-        RowTile t;
-        if (!find_tile(a.offsets, a.E, a.M, Tile::kRows, tm, t)) return;
-        e = t.e;
-        m0 = t.m0;
-        m1 = t.m1;
-    } else
-        m0 = (int64_t)tm * Tile::kRows;
+    const int all = tiles_m * a.tiles_n * (MODE == kSums ? a.E : 1), per = (all + 7) / 8, mine = (int)gridDim.x / 8;
+    const int first = (int)blockIdx.x % 8 * per;
+    auto place = [&](int i, Fp8Place& p) {
+        int id = first + i;
+        if (i >= per || id >= all) return false;
+        p.s0 = 0;
+        p.s1 = a.steps;
+        p.e = 0;
+        if constexpr (MODE == kSums) {
+            p.e = id / (tiles_m * a.tiles_n);
+            id %= tiles_m * a.tiles_n;
+            p.s0 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, p.e);
+            p.s1 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, p.e + 1);
+        }
+        int tm, tn;
+        fp8_place(id, tiles_m, a.tiles_n, tm, tn);
+        p.n0 = tn * Tile::kRows;
+        p.m0 = (int64_t)tm * Tile::kRows;
+        p.m1 = a.M;
+        if constexpr (kGrouped) {
+            RowTile t;
+            if (!find_tile(a.offsets, a.E, a.M, Tile::kRows, tm, t)) return false;
+            p.e = t.e;
+            p.m0 = t.m0;
+            p.m1 = t.m1;
+        }
+        return true;
+    };
+    int i = (int)blockIdx.x / 8;
+    Fp8Place p;
+    if (!place(i, p)) return;
     f32x16 acc[W][W];
+    Fp8Run<W, NS, MODE, fp8_exact<T>> run(a, lds, acc);
+    run.setup(p);
+    run.fill();
+    bool full = false;
+    for (;;) {
 #pragma unroll
-    for (int i = 0; i < W; ++i)
+        for (int u = 0; u < W; ++u)
 #pragma unroll
-        for (int j = 0; j < W; ++j) acc[i][j] = f32x16{};
-    Fp8Run<W, MODE, fp8_exact<T>>(a, lds, acc, MODE == kSums ? 0 : e, m0, m1, n0, s0, s1).run();
-    const int64_t shift = MODE == kSums ? e * a.out_expert : 0;
-    char* area = lds + wave * (32 * 32 * W * 4);
-    m0 += (wave >> 1) * 32 * W;
-    n0 += (wave & 1) * 32 * W;
-    fp8_store_tile<W, T>(a, area, shift, m0, m1, n0, acc);
+            for (int v = 0; v < W; ++v) acc[u][v] = f32x16{};
+        run.template run<Tile::kKeeps ? Store::kStores : 0>(full);
+        if constexpr (W == 4)
+#pragma unroll
+            for (int u = 0; u < W; ++u) fp8_hold<W>(acc[u]);
+        const int64_t shift = MODE == kSums ? p.e * a.out_expert : 0, m0 = p.m0 + (wave >> 1) * 32 * W, m1 = p.m1;
+        const int n0 = p.n0 + (wave & 1) * 32 * W;
+        bool more = false;
+        if constexpr (Tile::kKeeps) {
+            i += mine;
+            more = place(i, p);
+            if (more) {
+                run.setup(p);
+                run.fill();
+            }
+        }
+        char* area = lds + Tile::kOut + wave * Tile::kArea;
+        full = m0 + 32 * W <= m1 && n0 + 32 * W <= a.N;
+        if (full) Store::template run<true>(a, area, shift, m0, m1, n0, acc);
+        else Store::template run<false>(a, area, shift, m0, m1, n0, acc);
+        if (!more) break;
+    }
 }
 
 // Few rows: a workgroup computes 16 columns for up to 16 MF rows, its waves split the blocks of
