@@ -98,7 +98,7 @@ int tile_launch(Fp8Args& a, int64_t tiles_m, int device, void* stream)
     if (rc != GEMM_RS_OK) return rc;
     a.tiles_n = (int)ceil_div(a.N, kRows);
     a.tiles_m = (int)tiles_m;
-    int64_t grid = ceil_div(tiles_m * a.tiles_n * (MODE == kSums ? a.E : 1), 8) * 8;
+    int64_t grid = ceil_div(tiles_m * a.tiles_n, 8) * 8 * (MODE == kSums ? a.E : 1);
     if (grid >= int64_t(1) << 31) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;  // tiles are counted in 32 bits
     if (Tile::kKeeps && grid > kCus) grid = kCus;
     if (grid * 256 > kMaxThreads) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
@@ -118,6 +118,24 @@ int few_launch(const Fp8Args& a, void* stream)
                   stream, "fp8_few_kernel");
 }
 
+// 0: tiles of 256 x 256, 1: of 128 x 128 with two workgroups per CU, 2: with one: by the time of their rounds of tiles over
+// the CUs, which is so much for each step and for the rest.  In tenths of a us; measured, us, BF16 results, 2 / 8 / 28 / 64
+// steps: 128 tiles of 256 x 256 10 / 16 / 40 / 80, 256 of them 12 / 20 / 50 / 103; 128 x 128, two per CU: 256 tiles 6 / 8 / 24
+// / 45, 512 7 / 11 / 30 / 63, 1024 11 / 21 / 58 / 124; one per CU: 256 tiles 6 / 9 / 20 / 39, 512 10 / 14 / 35 / 73.  FP32
+// results: 256 tiles of 256 x 256 21 / 38 / 95 / 197; 128 x 128, two per CU: 256 tiles 8 / 11 / 29 / 60, 512 10 / 18 / 51 /
+// 110; one per CU, 256 tiles: 8 / 12 / 30 / 63, which is never taken.  It takes the fastest of the three, or one within 7%,
+// for 1024 x 4096 .. 8192 x 8192 with 8 steps or more; at two steps the second is up to 20% faster than the first, which
+// is taken from 256 tiles on.
+int tile_choice(bool exact, int64_t big, int64_t small, int64_t steps)
+{
+    const int64_t whole = exact ? 16 * steps + 70 : 9 * steps + 55, rest = small % (2 * kCus);
+    const int64_t cost[3] = {ceil_div(big, kCus) * (exact ? 29 * steps + 100 : 14 * steps + 80),
+                             small / (2 * kCus) * whole + (rest > kCus ? whole : rest == 0 ? 0 : exact ? 9 * steps + 60 : (13 * steps + 90) / 2),
+                             ceil_div(small, kCus) * (exact ? 9 * steps + 60 : (11 * steps + 110) / 2)};
+    if (cost[0] <= cost[1] && cost[0] <= cost[2]) return 0;
+    return cost[1] < cost[2] ? 1 : 2;
+}
+
 template <int MODE, class T>
 int product(Fp8Args& a, int device, void* stream)
 {
@@ -125,16 +143,21 @@ int product(Fp8Args& a, int device, void* stream)
         const int64_t rows = MODE == kDense ? a.M : ceil_div(a.M, a.E);  // of an expert, if all have as many
         if (rows <= 16) return few_launch<1, MODE, T>(a, stream);
         if (rows <= 32) return few_launch<2, MODE, T>(a, stream);
-        if (rows <= 64) return few_launch<4, MODE, T>(a, stream);
     }
-    // rows of tiles: exact, or at most one ragged tile an expert
-    auto rows_of = [&](int64_t edge) {
-        return MODE == kByExpert || MODE == kGather ? a.M / edge + (a.E < a.M ? a.E : a.M) : ceil_div(a.M, edge);
+    // rows of tiles: exact, or a bound, and what to expect
+    constexpr bool kGrouped = MODE == kByExpert || MODE == kGather;
+    const int64_t experts = a.E < a.M ? a.E : a.M;  // that can have a row
+    auto rows_of = [&](int64_t edge) { return kGrouped ? a.M / edge + experts : ceil_div(a.M, edge); };
+    auto tiles = [&](int64_t edge) {
+        return (kGrouped ? a.M / edge + (experts + 1) / 2 : rows_of(edge)) * ceil_div(a.N, edge) * (MODE == kSums ? a.E : 1);
     };
-    auto tiles = [&](int64_t edge) { return rows_of(edge) * ceil_div(a.N, edge) * (MODE == kSums ? a.E : 1); };
-    if (tiles(256) >= kCus) return tile_launch<4, 2, MODE, T>(a, rows_of(256), device, stream);
-    return tiles(128) > kCus ? tile_launch<2, 2, MODE, T>(a, rows_of(128), device, stream)
-                             : tile_launch<2, 4, MODE, T>(a, rows_of(128), device, stream);
+    switch (tile_choice(fp8_exact<T>, tiles(256), tiles(128), MODE == kSums ? a.rows / a.E / kFp8Block + 1 : a.steps)) {
+    case 0: return tile_launch<4, 2, MODE, T>(a, rows_of(256), device, stream);
+    case 1: return tile_launch<2, 2, MODE, T>(a, rows_of(128), device, stream);
+    default:
+        if constexpr (fp8_exact<T>) return tile_launch<2, 2, MODE, T>(a, rows_of(128), device, stream);
+        else return tile_launch<2, 4, MODE, T>(a, rows_of(128), device, stream);
+    }
 }
 
 template <int MODE>

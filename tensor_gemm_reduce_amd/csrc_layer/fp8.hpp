@@ -723,18 +723,21 @@ __global__ __launch_bounds__(256, W == 4 || NS == 4 ? 1 : 2) void fp8_kernel(con
     constexpr bool kGrouped = MODE == kByExpert || MODE == kGather;
     const int wave = uni(threadIdx.x >> 6);
     const int tiles_m = kGrouped ? tiles_before(a.offsets, a.E, a.M, Tile::kRows, a.E) : a.tiles_m;
-    // workgroups are dealt to the 8 XCDs in turn: those of one XCD take neighbouring tiles
-    const int all = tiles_m * a.tiles_n * (MODE == kSums ? a.E : 1), per = (all + 7) / 8, mine = (int)gridDim.x / 8;
+    // Workgroups are dealt to the 8 XCDs in turn: those of one XCD take neighbouring tiles, an eighth of all, or of each
+    // expert's where those differ in their steps.
+    const int all = tiles_m * a.tiles_n, per = (all + 7) / 8, mine = (int)gridDim.x / 8;
     const int first = (int)blockIdx.x % 8 * per;
-    auto place = [&](int i, Fp8Place& p) {
-        int id = first + i;
-        if (i >= per || id >= all) return false;
+    auto place = [&](int& i, Fp8Place& p) {
+        p.e = 0;
+        if constexpr (MODE == kSums)
+            while (i / per < a.E && first + i % per >= all) i += mine;  // an XCD's eighth may be short
+        if (MODE == kSums ? i / per >= a.E : i >= per) return false;
+        int id = first + i % per;
+        if (id >= all) return false;
         p.s0 = 0;
         p.s1 = a.steps;
-        p.e = 0;
         if constexpr (MODE == kSums) {
-            p.e = id / (tiles_m * a.tiles_n);
-            id %= tiles_m * a.tiles_n;
+            p.e = i / per;
             p.s0 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, p.e);
             p.s1 = tiles_before(a.offsets, a.E, a.rows, kFp8Block, p.e + 1);
         }

@@ -9,16 +9,21 @@ using namespace gemm_rs_layer;
 
 namespace {
 
-int route_tokens(int k, int threads)
+// Tokens per workgroup: all of a few, for which one launch is faster than three; else one for each of its waves, or up to
+// kRouteTokens while two workgroups for every CU are left.  At most as many as its threads have choices for.
+constexpr int kRouteAlone = 64;
+int route_tokens(int64_t T, int k, int threads)
 {
-    const int n = threads / k;
-    return n < kRouteTokens ? n : kRouteTokens;
+    int64_t n = T <= kRouteAlone ? kRouteAlone : threads / 64;
+    while (n < kRouteTokens && T > n * 2 * kCus) n *= 2;
+    const int most = threads / k;
+    return n < most ? (int)n : most;
 }
 
 int route_values(int E) { return E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16; }
 
 // Choices per workgroup of the router's call; of gemm_rs_expert_plan's, at least as many.
-int route_chunk(int E, int k) { return route_tokens(k, route_threads(route_values(E))) * k; }
+int route_chunk(int64_t T, int E, int k) { return route_tokens(T, k, route_threads(route_values(E))) * k; }
 
 size_t plan_bytes(int64_t ids, int E, int chunk)
 {
@@ -67,8 +72,10 @@ void plan_check(Checker& c, int64_t T, const gemm_rs_expert_plan_args* p, const 
 // What follows the counts of more than one workgroup.
 int plan_rest(const PlanArgs& a, void* stream)
 {
-    const int rc = launch(plan_scan_kernel, dim3((unsigned)ceil_div(a.E, 8)), 256, a, stream, "gemm_rs_expert_plan");
-    return rc != GEMM_RS_OK ? rc : launch(plan_place_kernel, dim3((unsigned)a.chunks), kPlanIds, a, stream, "gemm_rs_expert_plan");
+    const int rc = launch(plan_scan_kernel, dim3((unsigned)a.E), kScanThreads, a, stream, "plan_scan_kernel");
+    return rc != GEMM_RS_OK ? rc
+                            : launch(plan_place_kernel, dim3((unsigned)a.chunks), (int)ceil_div(a.chunk, 64) * 64, a, stream,
+                                     "plan_place_kernel");
 }
 
 template <int SEG, int NV>
@@ -125,7 +132,7 @@ int gemm_rs_route_validate(const gemm_rs_route_config* c)
 
 size_t gemm_rs_expert_plan_workspace(int64_t T, int32_t E, int32_t k)
 {
-    return plan_sizes(T, E, k) && T * k < kMaxRows ? plan_bytes(T * k, E, route_chunk(E, k)) : 0;
+    return plan_sizes(T, E, k) && T * k < kMaxRows ? plan_bytes(T * k, E, route_chunk(T, E, k)) : 0;
 }
 
 int gemm_rs_route(const gemm_rs_route_config* c, int64_t T, const void* logits, int64_t logits_stride, const float* bias,
@@ -161,7 +168,7 @@ int gemm_rs_route(const gemm_rs_route_config* c, int64_t T, const void* logits, 
     a.groups = c->groups;
     a.keep = c->keep_groups;
     a.scale = c->scale;
-    a.tokens = route_chunk(c->E, c->k) / c->k;
+    a.tokens = route_chunk(T, c->E, c->k) / c->k;
     a.plan = plan_args(T, c->E, c->k, a.tokens * c->k, experts, *plan, workspace);
     if (T == 0)  // offsets of nothing
         return launch(plan_count_kernel, dim3(1), kPlanIds, [&] { a.plan.chunks = 1; return a.plan; }(), stream, "gemm_rs_route");

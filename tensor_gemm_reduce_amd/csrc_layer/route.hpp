@@ -363,32 +363,38 @@ __global__ __launch_bounds__(kPlanIds) void plan_count_kernel(const PlanArgs a)
     for (int i = threadIdx.x; i < a.E; i += blockDim.x) a.hist[(int64_t)blockIdx.x * a.E + i] = s.before[i];
 }
 
-// hist[c][e] becomes the sum over the workgroups before c: 8 experts x 32 workgroups at a time.
-__global__ __launch_bounds__(256) void plan_scan_kernel(const PlanArgs a)
+// hist[c][e] becomes the sum over the workgroups before c.  A workgroup takes an expert, a lane a workgroup's count: the
+// loads have a line each, but they are few, and only their latency counts.
+constexpr int kScanThreads = 256;
+
+__global__ __launch_bounds__(kScanThreads) void plan_scan_kernel(const PlanArgs a)
 {
-    __shared__ int part[8][33];
-    const int col = threadIdx.x & 7, row = threadIdx.x >> 3, e = blockIdx.x * 8 + col;
+    __shared__ int part[2][kScanThreads / 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.x;
     int carry = 0;
-    for (int c0 = 0; c0 < a.chunks; c0 += 32) {
-        const int c = c0 + row;
-        const bool in = c < a.chunks && e < a.E;
-        const int own = in ? a.hist[(int64_t)c * a.E + e] : 0;
-        part[col][row] = own;
-        __syncthreads();
-        int before = 0, all = 0;
+    for (int c0 = 0, turn = 0; c0 < a.chunks; c0 += kScanThreads, turn ^= 1) {
+        const int c = c0 + threadIdx.x;
+        const int own = c < a.chunks ? a.hist[(int64_t)c * a.E + e] : 0;
+        int s = own;
 #pragma unroll
-        for (int r = 0; r < 32; ++r) {
-            const int v = part[col][r];
-            before += r < row ? v : 0;
-            all += v;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(s, d);
+            if (lane >= d) s += o;
         }
-        if (in) a.hist[(int64_t)c * a.E + e] = carry + before;
-        carry += all;
-        __syncthreads();
+        if (lane == 63) part[turn][wave] = s;
+        __syncthreads();  // one for each turn: the next one writes the other half
+        int before = carry;
+#pragma unroll
+        for (int w = 0; w < kScanThreads / 64; ++w) {
+            before += w < wave ? part[turn][w] : 0;
+            carry += part[turn][w];
+        }
+        if (c < a.chunks) a.hist[(int64_t)c * a.E + e] = before + s - own;
     }
-    if (row == 0 && e < a.E) a.totals[e] = carry;
+    if (threadIdx.x == 0) a.totals[e] = carry;
 }
 
+// One thread for each choice of the workgroup's.
 __global__ __launch_bounds__(kPlanIds) void plan_place_kernel(const PlanArgs a)
 {
     __shared__ PlanLds s;

@@ -70,9 +70,11 @@ def test_route_validate(kw, code):
 
 def test_plan_workspace():
     size = ex.lib().gemm_rs_expert_plan_workspace
-    assert size(0, 8, 2) == 0 and size(128, 8, 2) == 0   # one workgroup's choices
-    assert size(129, 8, 2) == 3 * 8 * 4                  # two workgroups' counts, and their sum
-    assert size(1024 * 8, 256, 8) == (64 + 1) * 256 * 4
+    assert size(0, 8, 2) == 0 and size(64, 8, 2) == 0    # one workgroup's choices
+    assert size(65, 8, 2) == (5 + 1) * 8 * 4             # workgroups of 16 tokens: their counts, and the sums
+    assert size(32768, 256, 8) == (512 + 1) * 256 * 4    # of 64 tokens
+    assert size(1 << 20, 8, 2) == (8192 + 1) * 8 * 4     # of 128
+    assert size(30, 64, 64) == (2 + 1) * 64 * 4          # of 16, whose threads have no room for more choices
     assert size(-1, 8, 2) == 0 and size(10, 1025, 2) == 0 and size(10, 8, 65) == 0
     assert size(1 << 40, 8, 2) == 0
 
