@@ -10,6 +10,7 @@ using namespace gemm_rs_layer;
 namespace {
 
 constexpr int64_t kMaxWidth = 1 << 22;
+constexpr int64_t kFewRows = 16;  // of the kernel for few rows, which has a form for twice as many
 constexpr int64_t kMaxResource = (int64_t(1) << 31) - 1;  // bytes of a buffer resource below kOob
 
 int64_t blocks_of(int64_t n) { return ceil_div(n, kFp8Block); }
@@ -108,13 +109,13 @@ int tile_launch(Fp8Args& a, int64_t tiles_m, int device, void* stream)
     return e == hipSuccess ? GEMM_RS_OK : hip_fail(e, "fp8_kernel");
 }
 
-template <int MF, int MODE, class T>
+template <int MF, int MODE, class X, class T>
 int few_launch(const Fp8Args& a, void* stream)
 {
     constexpr int kWaves = 8;
     int64_t tiles = ceil_div(a.M, 16 * MF);
     if (MODE != kDense) tiles = a.M / (16 * MF) + (a.E < a.M ? a.E : a.M);
-    return launch(fp8_few_kernel<kWaves, MF, MODE, T>, dim3((unsigned)ceil_div(a.N, kFewTile), (unsigned)tiles), 64 * kWaves, a,
+    return launch(fp8_few_kernel<kWaves, MF, MODE, X, T>, dim3((unsigned)ceil_div(a.N, kFewTile), (unsigned)tiles), 64 * kWaves, a,
                   stream, "fp8_few_kernel");
 }
 
@@ -141,8 +142,8 @@ int product(Fp8Args& a, int device, void* stream)
 {
     if constexpr (MODE != kSums) {
         const int64_t rows = MODE == kDense ? a.M : ceil_div(a.M, a.E);  // of an expert, if all have as many
-        if (rows <= 16) return few_launch<1, MODE, T>(a, stream);
-        if (rows <= 32) return few_launch<2, MODE, T>(a, stream);
+        if (rows <= kFewRows) return few_launch<1, MODE, Fp8Few, T>(a, stream);
+        if (rows <= 2 * kFewRows) return few_launch<2, MODE, Fp8Few, T>(a, stream);
     }
     // rows of tiles: exact, or a bound, and what to expect
     constexpr bool kGrouped = MODE == kByExpert || MODE == kGather;
@@ -160,6 +161,18 @@ int product(Fp8Args& a, int device, void* stream)
     }
 }
 
+// The product of a few rows that are quantised on the way: x and x_pitch are the matrix itself.
+template <int MODE>
+int few_of(int x_dtype, int out_dtype, const Fp8Args& a, void* stream)
+{
+    if (x_dtype == GEMM_RS_DTYPE_F32) return few_launch<1, MODE, float, float>(a, stream);
+    if (x_dtype == GEMM_RS_DTYPE_F16)
+        return out_dtype == GEMM_RS_DTYPE_F32 ? few_launch<1, MODE, _Float16, float>(a, stream)
+                                              : few_launch<1, MODE, _Float16, _Float16>(a, stream);
+    return out_dtype == GEMM_RS_DTYPE_F32 ? few_launch<1, MODE, __bf16, float>(a, stream)
+                                          : few_launch<1, MODE, __bf16, __bf16>(a, stream);
+}
+
 template <int MODE>
 int product_of(int out_dtype, Fp8Args& a, int device, void* stream)
 {
@@ -172,6 +185,21 @@ bool fp8_args_ok(const gemm_rs_fp8_args* g)
 {
     return g && (is_float(g->x_dtype) || g->x_dtype == GEMM_RS_DTYPE_FP8) && is_float(g->out_dtype) && g->M >= 0 && g->N >= 1 &&
            g->K >= 1 && g->x_rows >= 0 && g->E >= 0;
+}
+
+// Rows of an expert, if all have as many; of a dense product.
+int64_t rows_each(const gemm_rs_fp8_args& g) { return g.E > 0 ? ceil_div(g.M, g.E) : g.M; }
+
+// x is quantised by the product's own kernel: few rows, not too many bytes of them for every 16 columns to read again, and of
+// few blocks, since a wave's conversions stand in the way of its weights' loads.  us so, and with a kernel before it: 1 x 1024 x
+// 1024 3.2 / 5.1, 1 x 8192 x 1024 5.1 / 5.7, 16 x 8192 x 1024 6.3 / 7.1, 8 x 2048 x 4096 7.9 / 7.9, 1 x 7168 x 8192 20.5 / 15.8.
+constexpr int64_t kFewBytes = 17 << 20, kFewInputs = 4096;
+
+bool few_raw(const gemm_rs_fp8_args& g)
+{
+    return g.x_dtype != GEMM_RS_DTYPE_FP8 && (g.out_dtype == g.x_dtype || g.out_dtype == GEMM_RS_DTYPE_F32) &&
+           rows_each(g) <= kFewRows && g.K <= kFewInputs &&
+           ceil_div(g.N, kFewTile) * g.M <= kFewBytes / (g.K * elem_bytes(g.x_dtype));
 }
 
 // q and scales of x in the workspace
@@ -217,7 +245,8 @@ int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t
     Fp8Args a = {};
     a.x = static_cast<const uint8_t*>(g->x);
     a.xs = static_cast<const uint8_t*>(g->x_scales);
-    if (raw) {
+    const bool few = few_raw(*g);
+    if (raw && !few) {
         rc = quant_check(g->x_dtype, g->x_rows, g->K, g->x, g->x_stride, workspace, workspace);
         if (rc != GEMM_RS_OK) return rc;
         uint8_t* q = static_cast<uint8_t*>(workspace);
@@ -235,7 +264,8 @@ int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t
     a.out = g->out;
     a.M = g->M;
     a.x_rows = g->x_rows;
-    a.x_pitch = a.w_pitch = pitch;
+    a.x_pitch = few ? g->x_stride * elem_bytes(g->x_dtype) : pitch;
+    a.w_pitch = pitch;
     a.w_expert = g->N * pitch;
     a.ws_expert = scale_bytes(g->N, g->K);
     a.add_stride = g->add_stride;
@@ -243,10 +273,15 @@ int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t
     a.xs_bytes = scale_bytes(g->x_rows, g->K);
     a.ws_bytes = a.ws_expert;
     a.N = (int)g->N;
+    a.K = (int)g->K;
     a.E = (int)g->E;
     a.steps = (int)blocks;
     a.xs_pitch = (int)pitch_of(g->x_rows);
     a.ws_pitch = (int)pitch_of(g->N);
+    if (few)
+        return !experts    ? few_of<kDense>(g->x_dtype, g->out_dtype, a, stream)
+               : g->tokens ? few_of<kGather>(g->x_dtype, g->out_dtype, a, stream)
+                           : few_of<kByExpert>(g->x_dtype, g->out_dtype, a, stream);
     if (!experts) return product_of<kDense>(g->out_dtype, a, device, stream);
     return g->tokens ? product_of<kGather>(g->out_dtype, a, device, stream) : product_of<kByExpert>(g->out_dtype, a, device, stream);
 }
@@ -322,7 +357,8 @@ int gemm_rs_fp8_pack(int32_t dtype, int64_t E, int64_t N, int64_t K, int32_t tra
 
 size_t gemm_rs_fp8_workspace(const gemm_rs_fp8_args* g)
 {
-    if (!fp8_args_ok(g) || g->M == 0 || g->x_dtype == GEMM_RS_DTYPE_FP8 || g->x_rows >= kMaxRows || g->K > kMaxWidth) return 0;
+    if (!fp8_args_ok(g) || g->M == 0 || g->x_dtype == GEMM_RS_DTYPE_FP8 || g->x_rows >= kMaxRows || g->K > kMaxWidth || few_raw(*g))
+        return 0;
     return quant_bytes(g->x_rows, g->K);
 }
 

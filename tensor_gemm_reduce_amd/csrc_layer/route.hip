@@ -9,9 +9,10 @@ using namespace gemm_rs_layer;
 
 namespace {
 
-// Tokens per workgroup: all of a few, for which one launch is faster than three; else one for each of its waves, or up to
+// Tokens per workgroup: all of a few, for which one launch is faster than three (256 experts in groups, 16 / 64 tokens: 16 / 35 us
+// so, 1024 in three launches 24); else one for each of its waves, or up to
 // kRouteTokens while two workgroups for every CU are left.  At most as many as its threads have choices for.
-constexpr int kRouteAlone = 64;
+constexpr int kRouteAlone = 32;
 int route_tokens(int64_t T, int k, int threads)
 {
     int64_t n = T <= kRouteAlone ? kRouteAlone : threads / 64;

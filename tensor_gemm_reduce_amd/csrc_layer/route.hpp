@@ -3,11 +3,11 @@
 // back into one.
 //
 // A wave takes a token (or 64 / SEG tokens where the experts fit SEG lanes): lane l
-// holds experts l, l + 64, ..  Choices have to come out as the formula says, not as
+// holds experts NV l .. NV l + NV - 1.  Choices have to come out as the formula says, not as
 // FP32 rounds it: without a bias and groups scores order as the logits do, which are
-// compared as they are; else in 64 bits.  Either way as unsigned keys that order like
-// the values, so that a maximum over the lanes and the lowest lane that has it are the
-// choice.  Bytes are few (8192 x 256 logits in FP32: 8 MB, 1.7 us); the k maxima over
+// compared as they are; else in 64 bits, where FP32 does not tell.  Either way as unsigned
+// keys that order like the values, so that a maximum over the lanes and the lowest lane
+// that has it are the choice.  Bytes are few (8192 x 256 logits in FP32: 8 MB, 1.7 us); the k maxima over
 // the lanes, six exchanges each, are what takes time.
 #pragma once
 
@@ -46,36 +46,57 @@ __device__ __forceinline__ uint64_t route_key(double v)
     return b >> 63 ? ~b : b | (uint64_t(1) << 63);
 }
 
-template <int SEG>
-__device__ __forceinline__ uint32_t seg_max(uint32_t v)
+// v of another lane of the 16: by the ALU's own exchanges (a shuffle takes the LDS pipe, which the router would be bound by:
+// 35 us for 8192 x 256).
+template <int CTRL, class V>
+__device__ __forceinline__ V row_other(V v)
 {
-#pragma unroll
-    for (int d = SEG / 2; d > 0; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+    if constexpr (sizeof(V) == 8) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+        return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+    } else
+        return __builtin_bit_cast(V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+// v of lane `at`, the same for all lanes
+template <class V>
+__device__ __forceinline__ V lane_value(V v, int at)
+{
+    if constexpr (sizeof(V) == 8) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, at);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), at);
+        return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+    } else
+        return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), at));
+}
+// op over the SEG lanes, in every lane
+template <int SEG, class V, class OP>
+__device__ __forceinline__ V seg_all(V v, OP op)
+{
+    v = op(v, row_other<0xB1>(v));   // lane ^ 1
+    v = op(v, row_other<0x4E>(v));   // lane ^ 2
+    v = op(v, row_other<0x141>(v));  // 7 - lane: the other four, which agree
+    if constexpr (SEG >= 16) v = op(v, row_other<0x140>(v));  // 15 - lane
+    if constexpr (SEG == 32) v = op(v, __shfl_xor(v, 16));
+    if constexpr (SEG == 64) v = op(op(lane_value(v, 0), lane_value(v, 16)), op(lane_value(v, 32), lane_value(v, 48)));
     return v;
 }
-template <int SEG>
-__device__ __forceinline__ uint64_t seg_max(uint64_t v)
+template <int SEG, class V>
+__device__ __forceinline__ V seg_max(V v)
 {
-#pragma unroll
-    for (int d = SEG / 2; d > 0; d >>= 1) {
-        const uint64_t o = (uint64_t)__shfl_xor((long long)v, d);
-        v = o > v ? o : v;
-    }
-    return v;
+    return seg_all<SEG>(v, [](V a, V b) { return a > b ? a : b; });
 }
 template <int SEG>
 __device__ __forceinline__ float seg_max(float v)
 {
-#pragma unroll
-    for (int d = SEG / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    return seg_all<SEG>(v, [](float a, float b) { return fmaxf(a, b); });
 }
-template <int SEG, class F>
-__device__ __forceinline__ F seg_sum(F v)
+template <int SEG, class V>
+__device__ __forceinline__ V seg_sum(V v)
 {
-#pragma unroll
-    for (int d = SEG / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+    return seg_all<SEG>(v, [](V a, V b) { return a + b; });
 }
 
 __device__ __forceinline__ float route_exp(float v) { return expf(v); }
@@ -119,11 +140,23 @@ struct RouteArgs {
     PlanArgs plan;
 };
 
-__device__ __forceinline__ float route_load(const void* p, int dtype, int64_t at)
+// A lane's logits of token t: experts first, first + step, ..; -inf for those that are not there.  All loads are on their way
+// before one is waited for: a token's are a chain of latencies otherwise (8 of them were 20 us of 8192 x 256's 31).
+template <int NV>
+__device__ __forceinline__ void route_load(const void* logits, int dtype, int64_t row, int E, int first, int step, bool live,
+                                           float (&l)[NV])
 {
-    if (dtype == 0) return (float)static_cast<const __bf16*>(p)[at];
-    if (dtype == 1) return (float)static_cast<const _Float16*>(p)[at];
-    return static_cast<const float*>(p)[at];
+    auto load = [&](auto* p) {
+        p += row;
+        typename std::remove_cv<typename std::remove_reference<decltype(*p)>::type>::type v[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = p[min(first + i * step, E - 1)];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) l[i] = live && first + i * step < E ? (float)v[i] : -INFINITY;
+    };
+    if (dtype == 0) load(static_cast<const __bf16*>(logits));
+    else if (dtype == 1) load(static_cast<const _Float16*>(logits));
+    else load(static_cast<const float*>(logits));
 }
 
 // Where the choices of a workgroup go: thread i has choice i of the workgroup's (its expert,
@@ -131,7 +164,7 @@ __device__ __forceinline__ float route_load(const void* p, int dtype, int64_t at
 // rank among the same expert's in the wave by comparing indices bit by bit, and the waves'
 // counts stand in LDS.  before[e]: the expert's first row of this workgroup.  count:
 // [waves][E + 1] 16-bit, and room for E + 1 more words behind it.
-__device__ __forceinline__ int plan_rank(int e, bool in, int E, uint16_t* count, int& wave_rank)
+__device__ __forceinline__ int plan_rank(int e, bool in, int E, uint16_t* count)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     uint32_t* words = reinterpret_cast<uint32_t*>(count);
@@ -145,7 +178,6 @@ __device__ __forceinline__ int plan_rank(int e, bool in, int E, uint16_t* count,
     }
     const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
     if (in && rank == 0) count[wave * pitch + e] = (uint16_t)__popcll(same);
-    wave_rank = rank;
     __syncthreads();
     int r = rank;
     if (in)
@@ -202,8 +234,7 @@ __device__ __forceinline__ void plan_store(const PlanArgs& a, int64_t id, bool i
 __device__ __forceinline__ void plan_alone(const PlanArgs& a, PlanLds& s, int e, bool in)
 {
     for (int i = threadIdx.x; i < a.E; i += blockDim.x) s.before[i] = 0;
-    int wave_rank;
-    const int r = plan_rank(e, in, a.E, s.count, wave_rank);
+    const int r = plan_rank(e, in, a.E, s.count);
     // the last wave that has an expert knows its number of rows, so each raises the count to its own last rank
     if (in) atomicMax(&s.before[e], r + 1);
     __syncthreads();
@@ -212,127 +243,214 @@ __device__ __forceinline__ void plan_alone(const PlanArgs& a, PlanLds& s, int e,
     plan_store(a, threadIdx.x, in, in ? s.before[e] + r : 0, s.before[a.E]);
 }
 
-// Threads of the router's workgroups, and so choices that one may make: the scores of WIDE take LDS.
+// Threads of the router's workgroups, and so choices that one may make: the scores of groups take LDS.
 constexpr int route_threads(int nv) { return nv > 4 ? 256 : kPlanIds; }
 
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
+
+// What a token's lanes hold after the choice: lane j choice j and its score; the scores' sum; the least distance between a
+// choice and the next best expert.
+struct Choice {
+    int expert;
+    float score, sum, gap;
+};
+
+// The k largest keys, largest first; the key after the last counts for the distance.  A lane's keys (experts NV lane and on)
+// are put in order first, equal ones as they were; then each choice is the largest of the lanes' first keys, the lowest
+// lane's of equal ones, which moves up by one.
+template <int SEG, int NV, class K>
+__device__ __forceinline__ Choice route_choose(K (&key)[NV], const float (&p)[NV], int k)
+{
+    constexpr bool kGaps = std::is_same<K, uint32_t>::value;
+    const int lane = threadIdx.x & 63, sub = lane & (SEG - 1), part = lane / SEG;
+    int id[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) id[i] = sub * NV + i;
+#pragma unroll
+    for (int n = NV; n > 1; --n)
+#pragma unroll
+        for (int i = 0; i + 1 < n; ++i) {
+            const bool swap = key[i + 1] > key[i];
+            const K a = swap ? key[i + 1] : key[i], b = swap ? key[i] : key[i + 1];
+            const int c = swap ? id[i + 1] : id[i], d = swap ? id[i] : id[i + 1];
+            key[i] = a;
+            key[i + 1] = b;
+            id[i] = c;
+            id[i + 1] = d;
+        }
+    Choice c = {-1, 0.f, 0.f, INFINITY};
+    float last = INFINITY;
+    for (int j = 0; j < k + (kGaps ? 1 : 0); ++j) {
+        const K top = seg_max<SEG>(key[0]);
+        if constexpr (kGaps) {
+            const float v = key_value(top);
+            if (top != 0 && last - v < c.gap) c.gap = last - v;  // NaN's keys are the lowest and have no distance
+            last = v;
+            if (j == k) break;
+        }
+        uint64_t m = __ballot(key[0] == top);
+        if constexpr (SEG < 64) m = m >> (part * SEG) & ((uint64_t(1) << SEG) - 1);
+        const int at = __ffsll((unsigned long long)m) - 1;
+        const int e = SEG == 64 ? lane_value(id[0], uni(at)) : __shfl(id[0], part * SEG + at);
+        if (sub == j % SEG) c.expert = top != 0 ? e : -1;
+        if (sub == at) {
+#pragma unroll
+            for (int i = 0; i + 1 < NV; ++i) {
+                key[i] = key[i + 1];
+                id[i] = id[i + 1];
+            }
+            key[NV - 1] = 0;
+        }
+    }
+    const int from = part * SEG + (c.expert < 0 ? 0 : c.expert / NV);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const float v = __shfl(p[i], from);
+        if (c.expert >= 0 && c.expert % NV == i) c.score = v;
+    }
+    c.sum = seg_sum<SEG>(c.score);
+    return c;
+}
+
+// Which groups stay, as a mask of lanes: group g's are from g `per` on.  mine: the wave's part of LDS.  gap: the distance of
+// the last group that stays from the first that does not.
+template <int NV, class F>
+__device__ __forceinline__ uint64_t route_groups(const F (&c)[NV], const float (&l)[NV], F* mine, int E, int groups, int keep,
+                                                 int& per, F& gap)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) mine[lane * NV + i] = l[i] == -INFINITY ? (F)-INFINITY : c[i] != c[i] ? (F)-1e30 : c[i];
+    __asm__ __volatile__("" ::: "memory");  // the LDS operations of a wave complete in order
+    const int size = E / groups;
+    per = 64;  // lanes of a group
+    while (per * groups > 64) per >>= 1;
+    const int group = lane / per;
+    F hi = -INFINITY, lo = -INFINITY;
+    if (group < groups)
+        for (int i = lane % per; i < size; i += per) {
+            const F v = mine[group * size + i];
+            if (v > hi) {
+                lo = hi;
+                hi = v;
+            } else if (v > lo)
+                lo = v;
+        }
+    for (int d = per / 2; d > 0; d >>= 1) {
+        const F oh = __shfl_xor(hi, d), ol = __shfl_xor(lo, d);
+        const F third = hi < oh ? hi : oh;  // the smaller of the two largest
+        lo = lo > ol ? lo : ol;
+        if (third > lo) lo = third;
+        if (oh > hi) hi = oh;
+    }
+    const F total = lo == -INFINITY ? hi : hi + lo;
+    int rank = 0;  // how many groups come before this one
+    for (int o = 0; o < groups; ++o) {
+        const F v = lane_value(total, o * per);
+        rank += v > total || (v == total && o < group) ? 1 : 0;
+    }
+    const bool stays = group < groups && rank < keep;
+    const F in = seg_all<64>(stays ? total : (F)INFINITY, [](F a, F b) { return a < b ? a : b; });
+    const F out = seg_all<64>(stays || group >= groups ? (F)-INFINITY : total, [](F a, F b) { return a > b ? a : b; });
+    // groups that are off are last whatever the others' rounding
+    gap = out == -INFINITY ? (F)INFINITY : in - out;
+    __asm__ __volatile__("" ::: "memory");
+    return __ballot(stays);
+}
+
+// WIDE: a bias or groups.  The choice is first made in FP32, and stands where all distances in it are more than twice what
+// FP32 can be off by: a few roundings of a score (of exp's argument, exp, the sum over the experts, the quotient: some 30 2^-24, so less than
+// 2^-18, of the largest) and that of the sum with the bias.  Else, for about a token in a thousand and for equal scores, it is made
+// again in 64 bits.
 template <int SEG, int NV, bool WIDE>
 __global__ __launch_bounds__(route_threads(NV)) void route_kernel(const RouteArgs a)
 {
-    typedef typename std::conditional<WIDE, uint64_t, uint32_t>::type key_t;
     constexpr int kPer = 64 / SEG;  // tokens of a wave at a time
     constexpr int kThreads = route_threads(NV);
+    constexpr bool kGroups = WIDE && SEG == 64;
     __shared__ union {
         PlanLds plan;
-        double c[WIDE && SEG == 64 ? kThreads / 64 : 1][WIDE && SEG == 64 ? 64 * NV : 1];
+        double c[kGroups ? kThreads / 64 : 1][kGroups ? 64 * NV : 1];
     } lds;
     __shared__ int32_t ids[kThreads], hist[kMaxExperts];
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), waves = kThreads / 64;
     const int sub = lane & (SEG - 1), part = lane / SEG;
     const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+    float bias[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) bias[i] = WIDE && a.bias ? a.bias[min(sub * NV + i, a.E - 1)] : 0.f;
     ids[threadIdx.x] = -1;
     for (int i = threadIdx.x; i < a.E; i += kThreads) hist[i] = 0;
     __syncthreads();
     for (int g = wave * kPer; g < a.tokens; g += waves * kPer) {
+        if (t0 + g >= a.T) break;
         const int64_t t = t0 + g + part;
         const bool live = g + part < a.tokens && t < a.T;
         float l[NV], p[NV];
-        key_t key[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = i * 64 + sub;
-            l[i] = live && e < a.E ? route_load(a.logits, a.dtype, t * a.stride + e) : -INFINITY;
-        }
+        route_load<NV>(a.logits, a.dtype, (live ? t : a.T - 1) * a.stride, a.E, sub * NV, 1, live, l);
         route_scores<float, SEG, NV>(l, a.sigmoid, p);
+        uint32_t key[NV];
+        Choice c;
         if constexpr (WIDE) {
-            double c[NV];
-            route_scores<double, SEG, NV>(l, a.sigmoid, c);
+            float f[NV], most = 0.f, score = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int e = i * 64 + sub;
-                if (a.bias && e < a.E) c[i] += (double)a.bias[e];
-                key[i] = l[i] == -INFINITY ? 0 : route_key(c[i]);
+                f[i] = p[i] + bias[i];
+                key[i] = l[i] == -INFINITY ? 0 : route_key(f[i]);
+                most = l[i] == -INFINITY ? most : fmaxf(most, fabsf(f[i]));
+                score = fmaxf(score, p[i]);
             }
-            if constexpr (SEG == 64) if (a.groups > 1) {
-                // the lanes of the wave share the groups; each group's two largest
-                double* mine = lds.c[wave];
-#pragma unroll
-                for (int i = 0; i < NV; ++i) mine[i * 64 + lane] = l[i] == -INFINITY ? -INFINITY : c[i] != c[i] ? -1e300 : c[i];
-                __asm__ __volatile__("" ::: "memory");  // the LDS operations of a wave complete in order
+            most = seg_max<SEG>(most);
+            score = seg_max<SEG>(score);
+            float gap = INFINITY;
+            if constexpr (kGroups) if (a.groups > 1) {
+                int per;
+                const uint64_t kept = route_groups<NV, float>(f, l, reinterpret_cast<float*>(lds.c[wave]), a.E, a.groups, a.keep, per, gap);
                 const int size = a.E / a.groups;
-                int per = 64;  // lanes of a group
-                while (per * a.groups > 64) per >>= 1;
-                const int group = lane / per;
-                double hi = -INFINITY, lo = -INFINITY;
-                if (group < a.groups)
-                    for (int i = lane % per; i < size; i += per) {
-                        const double v = mine[group * size + i];
-                        if (v > hi) {
-                            lo = hi;
-                            hi = v;
-                        } else if (v > lo)
-                            lo = v;
-                    }
-                for (int d = per / 2; d > 0; d >>= 1) {
-                    const double oh = __shfl_xor(hi, d), ol = __shfl_xor(lo, d);
-                    const double third = hi < oh ? hi : oh;  // the smaller of the two largest
-                    lo = lo > ol ? lo : ol;
-                    if (third > lo) lo = third;
-                    if (oh > hi) hi = oh;
-                }
-                const double total = lo == -INFINITY ? hi : hi + lo;
-                // how many groups come before this one
-                int rank = 0;
-                for (int o = 0; o < a.groups; ++o) {
-                    const double v = __shfl(total, o * per);
-                    rank += v > total || (v == total && o < group) ? 1 : 0;
-                }
-                const uint64_t kept = __ballot(group < a.groups && rank < a.keep);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int e = i * 64 + lane;
+                    const int e = lane * NV + i;
                     if (e < a.E && !(kept >> (e / size * per) & 1)) key[i] = 0;
                 }
-                __asm__ __volatile__("" ::: "memory");
+                gap *= 0.5f;  // of sums of two
+            }
+            c = route_choose<SEG, NV>(key, p, a.k);
+            gap = fminf(gap, c.gap);
+            const float off = score * 0x1p-18f + most * 0x1p-23f;
+            if (__any(live && !(gap > 2.f * off))) {
+                double d[NV];
+                uint64_t wide[NV];
+                route_scores<double, SEG, NV>(l, a.sigmoid, d);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    d[i] += (double)bias[i];
+                    wide[i] = l[i] == -INFINITY ? 0 : route_key(d[i]);
+                }
+                if constexpr (kGroups) if (a.groups > 1) {
+                    int per;
+                    double unused;
+                    const uint64_t kept = route_groups<NV, double>(d, l, lds.c[wave], a.E, a.groups, a.keep, per, unused);
+                    const int size = a.E / a.groups;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int e = lane * NV + i;
+                        if (e < a.E && !(kept >> (e / size * per) & 1)) wide[i] = 0;
+                    }
+                }
+                c = route_choose<SEG, NV>(wide, p, a.k);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i) key[i] = l[i] == -INFINITY ? 0 : route_key(l[i]);
-        }
-        int chosen = -1;
-        float score = 0.f, sum = 0.f;
-        for (int j = 0; j < a.k; ++j) {
-            key_t top = key[0];
-#pragma unroll
-            for (int i = 1; i < NV; ++i) top = key[i] > top ? key[i] : top;
-            top = seg_max<SEG>(top);
-            int e = -1;
-            float v = 0.f;
-#pragma unroll
-            for (int i = NV - 1; i >= 0; --i) {
-                uint64_t m = __ballot(top != 0 && key[i] == top);
-                if constexpr (SEG < 64) m = m >> (part * SEG) & ((uint64_t(1) << SEG) - 1);
-                if (m) {
-                    const int at = __ffsll((unsigned long long)m) - 1;
-                    e = i * 64 + at;
-                    v = __shfl(p[i], part * SEG + at);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (e == i * 64 + sub) key[i] = 0;
-            sum += v;
-            if (sub == j % SEG) {
-                chosen = e;
-                score = v;
-            }
+            c = route_choose<SEG, NV>(key, p, a.k);
         }
         // lane j of the token has choice j (k <= SEG)
         if (live && sub < a.k) {
-            const float w = a.renormalise ? score / (sum + 1e-20f) : score;
+            const float w = a.renormalise ? c.score / (c.sum + 1e-20f) : c.score;
             a.weights[t * a.k + sub] = a.scale * w;
-            a.experts[t * a.k + sub] = chosen;
-            ids[(g + part) * a.k + sub] = chosen;
-            if (a.plan.chunks > 1 && chosen >= 0) atomicAdd(&hist[chosen], 1);
+            a.experts[t * a.k + sub] = c.expert;
+            ids[(g + part) * a.k + sub] = c.expert;
+            if (a.plan.chunks > 1 && c.expert >= 0) atomicAdd(&hist[c.expert], 1);
         }
     }
     __syncthreads();
@@ -408,8 +526,7 @@ __global__ __launch_bounds__(kPlanIds) void plan_place_kernel(const PlanArgs a)
     int e = mine ? a.experts[id] : -1;
     if (e >= a.E) e = -1;
     const bool in = e >= 0;
-    int wave_rank;
-    const int r = plan_rank(e, in, a.E, s.count, wave_rank);
+    const int r = plan_rank(e, in, a.E, s.count);
     if (mine) plan_store(a, id, in, in ? s.before[e] + a.hist[(int64_t)blockIdx.x * a.E + e] + r : 0, s.before[a.E]);
 }
 
@@ -433,12 +550,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
     const int64_t t = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * kPer + part;
     const bool live = t < a.T;
     float l[NV], p[NV], ds[NV];
+    route_load<NV>(a.logits, a.dtype, (live ? t : a.T - 1) * a.stride, a.E, sub, 64, live, l);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = i * 64 + sub;
-        l[i] = live && e < a.E ? route_load(a.logits, a.dtype, t * a.stride + e) : -INFINITY;
-        ds[i] = 0.f;
-    }
+    for (int i = 0; i < NV; ++i) ds[i] = 0.f;
     int e = -1;
     float dw = 0.f;
     if (live && sub < a.k) {

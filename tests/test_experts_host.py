@@ -70,8 +70,8 @@ def test_route_validate(kw, code):
 
 def test_plan_workspace():
     size = ex.lib().gemm_rs_expert_plan_workspace
-    assert size(0, 8, 2) == 0 and size(64, 8, 2) == 0    # one workgroup's choices
-    assert size(65, 8, 2) == (5 + 1) * 8 * 4             # workgroups of 16 tokens: their counts, and the sums
+    assert size(0, 8, 2) == 0 and size(32, 8, 2) == 0    # one workgroup's choices
+    assert size(33, 8, 2) == (3 + 1) * 8 * 4             # workgroups of 16 tokens: their counts, and the sums
     assert size(32768, 256, 8) == (512 + 1) * 256 * 4    # of 64 tokens
     assert size(1 << 20, 8, 2) == (8192 + 1) * 8 * 4     # of 128
     assert size(30, 64, 64) == (2 + 1) * 64 * 4          # of 16, whose threads have no room for more choices
@@ -88,9 +88,11 @@ def fp8(**kw):
 
 def test_fp8_workspace():
     size = lambda **kw: ex.lib().gemm_rs_fp8_workspace(ctypes.byref(fp8(**kw)))  # noqa: E731
-    assert size() == 4 * 256 + 16           # q, and two blocks' scales of 4 + 3 rows, rounded up to 8
+    assert size(M=17, x_rows=17) == 17 * 256 + 2 * 20 + 8      # q, and two blocks' scales of 17 + 3 rows, to 16 bytes
     assert size(x_dtype=ex.DTYPE_FP8) == 0
-    assert size(x_rows=100) == 100 * 256 + 2 * 104
+    assert size(x_rows=100, M=100) == 100 * 256 + 2 * 104
+    assert size() == 0                                         # a few rows are quantised by the product's kernel
+    assert size(out_dtype=1) > 0 and size(K=5000) > 0 and size(K=4096, N=1 << 20) > 0  # unless it has no such form
     assert size(M=0) == 0 and size(K=0) == 0
 
 
@@ -112,7 +114,7 @@ def test_fp8_workspace():
     (dict(out_stride=15), gr.ERR_INVALID_ARG),
     (dict(add=512, add_stride=16), gr.ERR_INVALID_ARG),       # needs an FP32 result
     (dict(add=256, add_stride=17, out_dtype=2), gr.ERR_INVALID_ARG),  # in place, of another stride
-    (dict(), gr.ERR_SCRATCH),
+    (dict(M=17, x_rows=17), gr.ERR_SCRATCH),
 ])
 def test_fp8_linear_refuses(kw, code):
     assert ex.lib().gemm_rs_fp8_linear(ctypes.byref(fp8(**kw)), None, 0, None) == code
@@ -125,7 +127,7 @@ def test_fp8_linear_refuses(kw, code):
     (dict(E=2, offsets=256, tokens=256, x_rows=1 << 24), gr.ERR_UNSUPPORTED_SHAPE),  # gathered from 4 GiB
     (dict(E=2, offsets=258), gr.ERR_MISALIGNED),
     (dict(E=2, offsets=256, M=0, x_rows=0), gr.OK),
-    (dict(E=2, offsets=256), gr.ERR_SCRATCH),
+    (dict(E=2, offsets=256, M=100, x_rows=100), gr.ERR_SCRATCH),
 ])
 def test_experts_linear_refuses(kw, code):
     assert ex.lib().gemm_rs_experts_linear(ctypes.byref(fp8(**kw)), None, 0, None) == code

@@ -741,3 +741,22 @@ def test_plans_out_of_range_read_and_write_nothing_outside():
     assert (dweights == 0).all()
     ex.experts_wgrad(torch.ones((T * k, N), dtype=BF16, device="cuda"), x, plan)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (4, 2)])
+def test_route_of_scores_closer_than_fp32(score, groups, keep):
+    """Biases that bring the sums next to one another: within FP32's rounding of a score, where 64 bits decide."""
+    g = gen(21)
+    T, E, k = 300, 64, 6
+    logits = torch.randn((1, E), generator=g).repeat(T, 1)
+    s = torch.from_numpy(ref.scores(logits[:1], score))[0]
+    bias = (1.0 - s).float()                       # all sums near one, as far apart as the biases' rounding
+    logits += 2.0 ** -18 * torch.randn((T, E), generator=g)
+    want = ref.route(logits, k, score, bias, groups, keep, True, 1.0)[1]
+    r = ex.route(logits.cuda(), k, score=score, bias=bias.cuda(), groups=groups, keep_groups=keep)
+    assert torch.equal(r.experts.cpu(), want)
+    # FP32 alone would not do: many of the order of its sums are others
+    f = (torch.softmax(logits, 1) if score == "softmax" else torch.sigmoid(logits)) + bias
+    if groups == 1:
+        assert (f.sort(dim=1, descending=True, stable=True)[1][:, :k] != want).any()
