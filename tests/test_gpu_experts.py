@@ -760,3 +760,20 @@ def test_route_of_scores_closer_than_fp32(score, groups, keep):
     f = (torch.softmax(logits, 1) if score == "softmax" else torch.sigmoid(logits)) + bias
     if groups == 1:
         assert (f.sort(dim=1, descending=True, stable=True)[1][:, :k] != want).any()
+
+
+@pytest.mark.parametrize("tokens,decode", [(200, 1), (37, 16), (1, 3)])
+def test_example(tokens, decode):
+    """The example's step against plain FP32: each value rounded to e4m3 on the way is off by at most 2^-4 of it, so a result
+    in the 2-norm by 2^-4 for each rounding that it passes (four products of two operands, forward and back)."""
+    import sys
+
+    from conftest import ROOT
+
+    if ROOT + "/examples" not in sys.path:
+        sys.path.insert(0, ROOT + "/examples")
+    import experts_block
+
+    found = experts_block.run(experts_block.SHAPES["tiny"], tokens, decode, verbose=False)
+    for k, roundings in {"partial": 4, "h": 4, "z": 4, "decode partial": 4, "dz": 8, "dW1": 8, "dW2": 6, "d router": 8}.items():
+        assert found[k] <= roundings * 2.0 ** -4, (k, found[k])
