@@ -34,7 +34,8 @@ extern "C" {
 /* A matrix [rows][cols] in e4m3 with scales 2^e (E8M0 bytes, e + 127):
  *   q       [rows][Kp], Kp = cols rounded up to 128; the columns past cols are 0
  *   scales  [Kp / 128][Rp], Rp = rows rounded up to 4: byte [b][r] is the scale of
- *           columns 128 b .. 128 b + 127 of row r; bytes past rows are not used
+ *           columns 128 b .. 128 b + 127 of row r; bytes past rows are not used,
+ *           the others 1 .. 254
  * both contiguous and 16-byte aligned.  A block holds
  *   e = the smallest integer >= -126 with max |x| <= 448 2^e,  q = e4m3(x 2^-e)
  * rounded to nearest even, and stands for q 2^e (2^128, past FP32's range, from
@@ -57,10 +58,16 @@ int gemm_rs_fp8_pack(int32_t dtype, int64_t E, int64_t N, int64_t K, int32_t tra
 /* ---- the products ----------------------------------------------------------- */
 
 /* out[m][n] = add[m][n] + sum_k x^[m][k] w^[n][k], FP32 accumulation, one rounding.
+ * Before it, an F32 result is within (K + 2) 2^-24 sum |x^| |w^|.  For BF16 and F16
+ * results the products of eight neighbouring inputs are lined up with the largest of
+ * them, and what lies below 2^-13 of that is dropped from each: to the bound comes
+ * 2^-10 of the largest product of every eight inputs, summed over K.
  * gemm_rs_fp8_linear: E, offsets and tokens are 0 and x_rows is M.
  * gemm_rs_experts_linear: rows offsets[e] .. offsets[e + 1] - 1 take the weights of
  * expert e; row m's input is row m of x, or row tokens[m] where tokens are given.
- * Rows of out from offsets[E] on stay as they were.  M bounds offsets[E]. */
+ * Rows of out from offsets[E] on stay as they were.  M bounds offsets[E].
+ * Sizes: N and K up to 2^22, E up to GEMM_RS_ROUTE_MAX_EXPERTS, scales of an operand
+ * and x's q where it is gathered less than 2 GiB. */
 typedef struct gemm_rs_fp8_args {
     int32_t x_dtype;         /* BF16, F16, F32: quantised by the call in blocks of a row; FP8 */
     int32_t out_dtype;       /* BF16, F16 or F32                                     */

@@ -211,9 +211,9 @@ int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t
     if (experts ? g->E < 1 || !g->offsets : g->E != 0 || g->offsets || g->tokens) return GEMM_RS_ERR_INVALID_ARG;
     if (!g->tokens && g->x_rows != g->M) return GEMM_RS_ERR_INVALID_ARG;
     const int64_t blocks = blocks_of(g->K), pitch = blocks * kFp8Block;
-    if (g->M >= kMaxRows || g->x_rows >= kMaxRows || g->N > kMaxWidth || g->K > kMaxWidth || g->E > (1 << 20) ||
+    if (g->M >= kMaxRows || g->x_rows >= kMaxRows || g->N > kMaxWidth || g->K > kMaxWidth || g->E > GEMM_RS_ROUTE_MAX_EXPERTS ||
         scale_bytes(g->x_rows, g->K) > kMaxResource || scale_bytes(g->N, g->K) > kMaxResource ||
-        (g->tokens && g->x_rows * pitch > kMaxResource) || g->M / 16 + g->E > 65535 * 16)
+        (g->tokens && g->x_rows * pitch > kMaxResource))
         return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     if (g->M == 0) return GEMM_RS_OK;
     const bool raw = g->x_dtype != GEMM_RS_DTYPE_FP8;
@@ -297,7 +297,7 @@ int64_t wgrad_blocks(const gemm_rs_experts_wgrad_args& g) { return g.M / kFp8Blo
 
 bool wgrad_fits(const gemm_rs_experts_wgrad_args& g)
 {
-    return g.M < kMaxRows && g.x_rows < kMaxRows && g.N <= kMaxWidth && g.K <= kMaxWidth && g.E <= (1 << 20) &&
+    return g.M < kMaxRows && g.x_rows < kMaxRows && g.N <= kMaxWidth && g.K <= kMaxWidth && g.E <= GEMM_RS_ROUTE_MAX_EXPERTS &&
            wgrad_blocks(g) * kFp8Block <= kMaxResource / 256 && pitch_of(g.N) * wgrad_blocks(g) <= kMaxResource &&
            pitch_of(g.K) * wgrad_blocks(g) <= kMaxResource && ceil_div(g.N, 64) <= 65535 && ceil_div(g.K, 64) <= 65535;
 }
@@ -321,7 +321,7 @@ int gemm_rs_fp8_quant_transposed(int32_t dtype, int64_t M, int64_t K, const void
 {
     int rc = quant_check(dtype, M, K, x, x_stride, q, scales);
     if (rc != GEMM_RS_OK || M == 0) return rc;
-    if (ceil_div(K, 64) > 65535) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (ceil_div(K, 64) > 65535 || blocks_of(M) * 256 > kMaxThreads) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     if ((rc = check_device()) != GEMM_RS_OK) return rc;
     return quant_columns(dtype, M, K, M, x, x_stride, nullptr, nullptr, 0, blocks_of(M), q, scales, stream);
 }

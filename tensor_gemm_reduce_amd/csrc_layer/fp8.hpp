@@ -299,9 +299,10 @@ struct Fp8Args {
     int tiles_m, tiles_n;
 };
 
-// Results in FP32 take every product whole: the scaled MFMA lines the products of e4m3 up with the largest of a group and
-// drops what lies below its 2^-13 (the sums with the accumulator are FP32's).  That is within BF16's and F16's rounding
-// of a result, not within FP32's, so there the operands are multiplied in BF16, at half the rate.
+// Results in FP32 take every product whole: the scaled MFMA lines the products of eight neighbouring inputs up with the
+// largest of them and drops from each what lies below its 2^-13 (measured; the sums with the accumulator are FP32's).  That
+// is little beside BF16's and F16's rounding of a result (2-norm over random operands: 2^-13 of it), not beside FP32's, so
+// there the operands are multiplied in BF16, at half the rate.
 template <class T>
 constexpr bool fp8_exact = std::is_same<T, float>::value;
 
@@ -340,13 +341,16 @@ __device__ __forceinline__ void each(F f)
 //   - A step has two halves of 64 inputs.  While the first is multiplied, the second's fragments are read; then the next
 //     step's stage has to have come, and a barrier frees this one; while the second is multiplied, this stage is filled
 //     for step s + NS and the next step's first fragments are read.
-// W = 4, NS = 2: one workgroup per CU, whose waves have 256 accumulators each.  What bounds it is the matrix instructions
-//   at the clock that the power limit leaves (79% of the cycles at 1.8 GHz in 8192^3).  Half steps in four stages, with
-//   more time for a load to arrive, but half lines a request, are 6% slower (8192^3: 393 / 417 us).  It keeps its
-//   workgroups for all tiles: the next tile's first stages are on their way before a tile's results are stored.
+// W = 4, NS = 2: one workgroup per CU, whose waves have 256 accumulators each.  In 8192^3 (390 .. 415 us, 2.65 .. 2.8
+//   PFLOP/s) the matrix instructions are busy for 79% of the cycles, at the 1.8 GHz that the power limit leaves; in 32768 x
+//   8192 x 3584 (767 .. 840 us) for 55%: a third of the cycles are waits for loads, of which those that miss the L2 (22%)
+//   take longer than the step between.  One load beside each MFMA: two or four at a time cost 3% and 8%.  Half steps in
+//   four stages, with more time for a load to arrive, but half lines a request, are 6% slower (8192^3: 393 / 417 us).
+//   It keeps its workgroups for all tiles: the next tile's first stages are on their way before a tile's results are
+//   stored (8192 x 8192 x 1024: 72 us, 79 without).
 // W = 2, NS = 2: two workgroups per CU.  LDS bounds it (96 KB a step against 256 cycles of MFMAs).
 // W = 2, NS = 4: for products of no more tiles than CUs, where a workgroup has the CU to itself and its loads' latency
-//   would bound it (501 x 7168 x 8192: 48 us with two stages).
+//   would bound it (501 x 7168 x 8192: 34 us, 48 with two stages).
 template <int W, int NS, int MODE>
 struct Fp8Tile {
     static constexpr int kRows = 64 * W;
@@ -450,16 +454,18 @@ struct Fp8Run {
         lds_void_t* to = (lds_void_t*)(put + Q * Tile::kStage + (w ? Tile::kOperand : 0) + i * 4096);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(w ? rw : rx, to, 16, off, k, 0, 0);
     }
-    // an offset past every resource for steps past the last, which then read zeros: a mask, no select that might
-    // become one per lane
-    __device__ __forceinline__ uint32_t past(int s) const { return ~(uint32_t)uni((s - step1) >> 31) & kOob; }
+    // Steps past the last read zeros, from an offset past every resource (and not from where their inputs would be): masks,
+    // no selects that might become one per lane.
+    __device__ __forceinline__ int live(int s) const { return uni((s - step1) >> 31); }
+    __device__ __forceinline__ uint32_t past(int s) const { return ~(uint32_t)live(s) & kOob; }
+    __device__ __forceinline__ int inputs(int s) const { return (s & live(s)) * kFp8Block; }
     // The scales go through LDS too, a dword for each lane: in registers, the compiler would wait for them, and so for
     // everything before them, by its own count.
     template <int Q>
     __device__ __forceinline__ void load_scales(int s) const
     {
         const uint32_t skip = past(s);
-        const int kw = s * a.ws_pitch, kx = s * a.xs_pitch;
+        const int in = s & live(s), kw = in * a.ws_pitch, kx = in * a.xs_pitch;
         auto load = [&](const __amdgpu_buffer_rsrc_t& r, uint32_t off, int k, int slot) {
             lds_void_t* to = (lds_void_t*)(put_scales + Q * Tile::kScaleStage + slot * 256);
             if constexpr (W == 4) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 4, off, k, 0, 0);
@@ -569,7 +575,7 @@ struct Fp8Run {
         barrier();
         read_scales<(P + 1) % NS>();
         const uint32_t skip = past(s + NS);
-        const int at = (s + NS) * kFp8Block;
+        const int at = inputs(s + NS);
         each<kAll>([&](auto m) {
             constexpr int M = decltype(m)::value;
             multiply<1, P, M>();
@@ -586,7 +592,7 @@ struct Fp8Run {
     {
         each<NS>([&](auto q) {
             constexpr int Q = decltype(q)::value;
-            const int at = (step0 + Q) * kFp8Block;
+            const int at = inputs(step0 + Q);
             const uint32_t skip = past(step0 + Q);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

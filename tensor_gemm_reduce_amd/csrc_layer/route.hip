@@ -143,7 +143,9 @@ int gemm_rs_route(const gemm_rs_route_config* c, int64_t T, const void* logits, 
     int rc = gemm_rs_route_validate(c);
     if (rc != GEMM_RS_OK) return rc;
     if (T < 0) return GEMM_RS_ERR_INVALID_ARG;
-    if (T * c->k >= kMaxRows || T >= kMaxRows) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (T >= kMaxRows || T * c->k >= kMaxRows) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    const int tokens = route_chunk(T, c->E, c->k) / c->k;  // of a workgroup
+    if (ceil_div(T, tokens) * route_threads(route_values(c->E)) > kMaxThreads) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     Checker k;
     plan_check(k, T, plan, experts, gemm_rs_expert_plan_workspace(T, c->E, c->k), workspace, workspace_bytes);
     if (T > 0) {
@@ -169,7 +171,7 @@ int gemm_rs_route(const gemm_rs_route_config* c, int64_t T, const void* logits, 
     a.groups = c->groups;
     a.keep = c->keep_groups;
     a.scale = c->scale;
-    a.tokens = route_chunk(T, c->E, c->k) / c->k;
+    a.tokens = tokens;
     a.plan = plan_args(T, c->E, c->k, a.tokens * c->k, experts, *plan, workspace);
     if (T == 0)  // offsets of nothing
         return launch(plan_count_kernel, dim3(1), kPlanIds, [&] { a.plan.chunks = 1; return a.plan; }(), stream, "gemm_rs_route");

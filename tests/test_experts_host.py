@@ -126,6 +126,7 @@ def test_fp8_linear_refuses(kw, code):
     (dict(E=2, offsets=256, x_rows=3), gr.ERR_INVALID_ARG),   # rows without tokens are x's own
     (dict(E=2, offsets=256, tokens=256, x_rows=1 << 24), gr.ERR_UNSUPPORTED_SHAPE),  # gathered from 4 GiB
     (dict(E=2, offsets=258), gr.ERR_MISALIGNED),
+    (dict(E=1025, offsets=256), gr.ERR_UNSUPPORTED_SHAPE),
     (dict(E=2, offsets=256, M=0, x_rows=0), gr.OK),
     (dict(E=2, offsets=256, M=100, x_rows=100), gr.ERR_SCRATCH),
 ])
@@ -156,6 +157,8 @@ def test_wgrad_workspace():
     (dict(dy_stride=15), gr.ERR_INVALID_ARG),
     (dict(out_dtype=0, add=256), gr.ERR_INVALID_ARG),
     (dict(N=1 << 23), gr.ERR_UNSUPPORTED_SHAPE),
+    (dict(E=1025), gr.ERR_UNSUPPORTED_SHAPE),
+    (dict(M=1 << 26, x_rows=1 << 26), gr.ERR_UNSUPPORTED_SHAPE),
     (dict(), gr.ERR_SCRATCH),
 ])
 def test_experts_wgrad_refuses(kw, code):
@@ -178,6 +181,14 @@ def test_quant_and_combine_refuse():
     assert L.gemm_rs_expert_plan(1 << 30, 8, 4, 256, ctypes.byref(plan), None, 0, None) == gr.ERR_UNSUPPORTED_SHAPE
     assert L.gemm_rs_expert_plan(2000, 8, 4, 256, ctypes.byref(plan), None, 0, None) == gr.ERR_SCRATCH
     assert L.gemm_rs_expert_plan(1, 8, 4, 256, None, None, 0, None) == gr.ERR_INVALID_ARG
+
+
+def test_route_refuses_more_threads_than_a_launch_has():
+    plan = ex.gemm_rs_expert_plan_args(256, 256, 256)
+    call = lambda T: ex.lib().gemm_rs_route(ctypes.byref(route(k=1)), T, 256, 8, None, 256, 256, ctypes.byref(plan), None, 0, None)  # noqa: E731
+    assert call(1 << 30) == gr.ERR_UNSUPPORTED_SHAPE and call(1 << 31) == gr.ERR_UNSUPPORTED_SHAPE
+    assert call(1 << 20) == gr.ERR_SCRATCH
+    assert call(-1) == gr.ERR_INVALID_ARG
 
 
 def test_binding_refuses_before_a_device_is_needed():

@@ -3,9 +3,9 @@
 Products of small integers have to be exact: their sums are exact in FP32, whatever the order, so the result is the one
 rounding of the 64-bit one.  Random operands have derived bounds:
   FP32 results    K products summed in FP32 in some order: (K + 2) 2^-24 sum |x| |w|
-  16-bit results  the matrix instruction also drops what lies below 2^-13 of the largest product of a group of at most 64,
-                  from each product at most that: 64 2^-13 of the largest, summed over the groups, and half a step of
-                  rounding
+  16-bit results  the matrix instruction also drops what lies below 2^-13 of the largest product of eight neighbouring
+                  inputs, from each product at most that: 8 2^-13 of the largest, summed over the eights, and half a step
+                  of rounding
 """
 import math
 
@@ -151,7 +151,7 @@ def test_linear_of_random_operands(dtype, M, N, K):
     sums = (K + 2) * U32 * mag
     close(ex.fp8_linear(x.cuda(), weight, dtype=F32), want, sums)
     if dtype is not F32:
-        drop = 64 * 2.0 ** -13 * top
+        drop = 8 * 2.0 ** -13 * top
         close(ex.fp8_linear(x.cuda(), weight), want, UNIT[dtype] * (want.abs() + drop + sums) + drop + sums)
         # what is dropped is nothing against the result's own size
         y = f64(ex.fp8_linear(x.cuda(), weight))
@@ -419,6 +419,59 @@ def test_experts_linear(T, E, k, N, K, dead, dtype):
     out.fill_(77.0)
     ex.experts_linear(ex.fp8_quant(x.cuda()), weight, plan, out=out)
     assert torch.equal(out.cpu(), want)
+
+
+def test_no_tokens():
+    """An empty batch through every call."""
+    E, k, N, K = 3, 2, 20, 130
+    empty = lambda *s, dtype=BF16: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+    r = ex.route(empty(0, E), k, bias=torch.zeros(E).cuda())
+    assert r.offsets.tolist() == [0] * (E + 1) and r.tokens.numel() == 0 and r.weights.shape == (0, k)
+    assert ex.route_backward(empty(0, k, dtype=F32), empty(0, E), r.experts).shape == (0, E)
+    weight = ex.fp8_pack(torch.ones((E, N, K), dtype=BF16, device="cuda"))
+    assert ex.experts_linear(empty(0, K), weight, r).shape == (0, N)
+    assert ex.experts_linear(empty(0, K), weight, r, rows=True).shape == (0, N)
+    assert (ex.experts_wgrad(empty(0, N), empty(0, K), r) == 0).all()
+    main = torch.full((E, N, K), 3.0, device="cuda")
+    ex.experts_wgrad(empty(0, N), empty(0, K), r, add=main, out=main)
+    assert (main == 3).all()
+    assert ex.combine(empty(0, N), r, r.weights).shape == (0, N)
+    dy, dw = ex.combine_backward(empty(0, N), empty(0, N), r, r.weights)
+    assert dy.shape == (0, N) and dw.shape == (0, k)
+    assert ex.fp8_quant(empty(0, K)).q.shape == (0, 256)
+
+
+def test_every_token_dropped():
+    T, k, E, N, K = 9, 2, 3, 20, 130
+    r = ex.route(torch.full((T, E), -math.inf, device="cuda"), k)
+    assert (r.experts == -1).all() and r.offsets.tolist() == [0] * (E + 1) and (r.slots == -1).all() and (r.tokens == -1).all()
+    one = lambda *s: torch.ones(s, dtype=BF16, device="cuda")  # noqa: E731
+    out = torch.full((T * k, N), 5.0, dtype=BF16, device="cuda")
+    for rows in (False, True):
+        ex.experts_linear(one(T * k if rows else T, K), ex.fp8_pack(one(E, N, K)), r, rows=rows, out=out)
+    assert (out == 5).all()
+    assert (ex.experts_wgrad(one(T * k, N), one(T, K), r) == 0).all()
+    assert (ex.combine(out, r, r.weights) == 0).all()
+    dy, dw = ex.combine_backward(one(T, N), out, r, r.weights)
+    assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("N,K", [(200, 130), (384, 1100)])
+def test_experts_of_very_different_sizes(N, K):
+    """One expert has nearly all rows, others one or none, in the order of the plan's worst case for the grid."""
+    g = gen(N)
+    E, T = 40, 1500
+    experts = torch.full((T, 1), 17, dtype=torch.int32)
+    experts[:E, 0] = torch.arange(E, dtype=torch.int32)   # one row each
+    plan = ex.plan(experts.cuda(), E)
+    offsets, tokens, _ = ref.plan(experts, E)
+    x, w, dy = integers(g, T, K, low=-3, high=3), integers(g, E, N, K, low=-3, high=3), integers(g, T, N, low=-3, high=3)
+    y = ex.experts_linear(x.to(BF16).cuda(), ex.fp8_pack(w.to(BF16).cuda()), plan, dtype=F32)
+    dw = ex.experts_wgrad(dy.to(BF16).cuda(), x.to(BF16).cuda(), plan)
+    for e in range(E):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        assert torch.equal(f64(y[r]), f64(x)[tokens[r].long()] @ f64(w[e]).t())
+        assert torch.equal(f64(dw[e]), f64(dy[r]).t() @ f64(x)[tokens[r].long()])
 
 
 def test_experts_linear_adds():
