@@ -109,6 +109,15 @@ int tile_launch(Fp8Args& a, int64_t tiles_m, int device, void* stream)
     return e == hipSuccess ? GEMM_RS_OK : hip_fail(e, "fp8_kernel");
 }
 
+// The kernel for few rows: a dense product's up to twice its tile, and experts' while their tiles of 128 x 128 would leave
+// more than half of the CUs idle.  us so, and with tiles: dense, 7168 x 8192, 16 rows 17 / 28, 32 26 / 28; 2 of 8 experts of
+// 4096 x 6144 for 1 token 12 / 26, 8 tokens 34 / 29, 64 62 / 30; 6 of 64 of 1408 x 2048, 4 tokens 14 / 13, 32 41 / 34.
+bool takes_few(int64_t M, int64_t N, int64_t E)
+{
+    if (E == 0) return M <= 2 * kFewRows;
+    return ceil_div(M, E) <= kFewRows && (E < M ? E : M) * ceil_div(N, 128) < kCus / 2;
+}
+
 template <int MF, int MODE, class X, class T>
 int few_launch(const Fp8Args& a, void* stream)
 {
@@ -141,9 +150,10 @@ template <int MODE, class T>
 int product(Fp8Args& a, int device, void* stream)
 {
     if constexpr (MODE != kSums) {
-        const int64_t rows = MODE == kDense ? a.M : ceil_div(a.M, a.E);  // of an expert, if all have as many
-        if (rows <= kFewRows) return few_launch<1, MODE, Fp8Few, T>(a, stream);
-        if (rows <= 2 * kFewRows) return few_launch<2, MODE, Fp8Few, T>(a, stream);
+        if (takes_few(a.M, a.N, a.E)) {
+            if (MODE != kDense || a.M <= kFewRows) return few_launch<1, MODE, Fp8Few, T>(a, stream);
+            if constexpr (MODE == kDense) return few_launch<2, MODE, Fp8Few, T>(a, stream);
+        }
     }
     // rows of tiles: exact, or a bound, and what to expect
     constexpr bool kGrouped = MODE == kByExpert || MODE == kGather;
@@ -187,9 +197,6 @@ bool fp8_args_ok(const gemm_rs_fp8_args* g)
            g->K >= 1 && g->x_rows >= 0 && g->E >= 0;
 }
 
-// Rows of an expert, if all have as many; of a dense product.
-int64_t rows_each(const gemm_rs_fp8_args& g) { return g.E > 0 ? ceil_div(g.M, g.E) : g.M; }
-
 // x is quantised by the product's own kernel: few rows, not too many bytes of them for every 16 columns to read again, and of
 // few blocks, since a wave's conversions stand in the way of its weights' loads.  us so, and with a kernel before it: 1 x 1024 x
 // 1024 3.2 / 5.1, 1 x 8192 x 1024 5.1 / 5.7, 16 x 8192 x 1024 6.3 / 7.1, 8 x 2048 x 4096 7.9 / 7.9, 1 x 7168 x 8192 20.5 / 15.8.
@@ -198,7 +205,7 @@ constexpr int64_t kFewBytes = 17 << 20, kFewInputs = 4096;
 bool few_raw(const gemm_rs_fp8_args& g)
 {
     return g.x_dtype != GEMM_RS_DTYPE_FP8 && (g.out_dtype == g.x_dtype || g.out_dtype == GEMM_RS_DTYPE_F32) &&
-           rows_each(g) <= kFewRows && g.K <= kFewInputs &&
+           takes_few(g.M, g.N, g.E) && (g.E > 0 || g.M <= kFewRows) && g.K <= kFewInputs &&
            ceil_div(g.N, kFewTile) * g.M <= kFewBytes / (g.K * elem_bytes(g.x_dtype));
 }
 

@@ -128,7 +128,7 @@ def test_fp8_linear_refuses(kw, code):
     (dict(E=2, offsets=258), gr.ERR_MISALIGNED),
     (dict(E=1025, offsets=256), gr.ERR_UNSUPPORTED_SHAPE),
     (dict(E=2, offsets=256, M=0, x_rows=0), gr.OK),
-    (dict(E=2, offsets=256, M=100, x_rows=100), gr.ERR_SCRATCH),
+    (dict(E=2, offsets=256, M=100, x_rows=100, N=16), gr.ERR_SCRATCH),
 ])
 def test_experts_linear_refuses(kw, code):
     assert ex.lib().gemm_rs_experts_linear(ctypes.byref(fp8(**kw)), None, 0, None) == code
