@@ -300,9 +300,9 @@ struct Fp8Args {
 };
 
 // Results in FP32 take every product whole: the scaled MFMA lines the products of eight neighbouring inputs up with the
-// largest of them and drops from each what lies below its 2^-13 (measured; the sums with the accumulator are FP32's).  That
-// is little beside BF16's and F16's rounding of a result (2-norm over random operands: 2^-13 of it), not beside FP32's, so
-// there the operands are multiplied in BF16, at half the rate.
+// largest of them and drops from each what lies below its 2^-13 (measured; the sums with the accumulator are FP32's).  F16's
+// half step is 2^-11 and BF16's 2^-8, so that it matters to them only where a sum cancels; FP32's is 2^-24, so there the
+// operands are multiplied in BF16, at half the rate.
 template <class T>
 constexpr bool fp8_exact = std::is_same<T, float>::value;
 
@@ -343,12 +343,12 @@ __device__ __forceinline__ void each(F f)
 //     for step s + NS and the next step's first fragments are read.
 // W = 4, NS = 2: one workgroup per CU, whose waves have 256 accumulators each.  In 8192^3 (390 .. 415 us, 2.65 .. 2.8
 //   PFLOP/s) the matrix instructions are busy for 79% of the cycles, at the 1.8 GHz that the power limit leaves; in 32768 x
-//   8192 x 3584 (767 .. 840 us) for 55%: a third of the cycles are waits for loads, of which those that miss the L2 (22%)
-//   take longer than the step between.  One load beside each MFMA: two or four at a time cost 3% and 8%.  Half steps in
+//   8192 x 3584 (784 .. 919 us at 2.0 .. 1.6 GHz) for 63%: a quarter of the cycles are waits, and 23% of the requests miss
+//   the L2.  One load beside each MFMA: two or four at a time cost 3% and 8%.  Half steps in
 //   four stages, with more time for a load to arrive, but half lines a request, are 6% slower (8192^3: 393 / 417 us).
 //   It keeps its workgroups for all tiles: the next tile's first stages are on their way before a tile's results are
 //   stored (8192 x 8192 x 1024: 72 us, 79 without).
-// W = 2, NS = 2: two workgroups per CU.  LDS bounds it (96 KB a step against 256 cycles of MFMAs).
+// W = 2, NS = 2: two workgroups per CU.  LDS bounds it: 96 KB a step are 768 cycles at 128 bytes each, the MFMAs 512.
 // W = 2, NS = 4: for products of no more tiles than CUs, where a workgroup has the CU to itself and its loads' latency
 //   would bound it (501 x 7168 x 8192: 34 us, 48 with two stages).
 template <int W, int NS, int MODE>
@@ -631,7 +631,8 @@ struct Fp8Run {
 
 // The results of a wave leave through LDS, so that whole lines are stored: 128 bytes of 32 rows at a time, 16-byte chunk c of
 // a row at chunk c ^ r.  A lane has 4 W neighbouring columns of a row for each g.  Direct stores of those, 16 bytes in
-// each of 64 lines an instruction, took 8 us more for each tile of 256 x 256.
+// each of 64 lines an instruction, were slower: 2048 x 3584 x 8192 66 us instead of 60, 4096^3 64 instead of 56, 8192 x
+// 3584 x 2048 in FP32 128 instead of 106.
 // Stored past the caches, which hold x and w for the tiles to come: 32768 x 8192 x 3584 803 us without, 767 with; the
 // gradients of 64 experts' weights, 738 MB in FP32, 429 and 341.
 // area: the wave's own 4 KB; m0, n0: the wave's first row and column.  FULL: no row or column past the end, so that every
@@ -802,7 +803,7 @@ __global__ __launch_bounds__(256, W == 4 || NS == 4 ? 1 : 2) void fp8_kernel(con
 // keeps kAhead blocks of them in flight, straight into the MFMA's registers (16 rows x 64
 // bytes an instruction).  X is the type of x: e4m3 as it is, or what a lane turns to its part of
 // a fragment by itself: 32 values of a row, whose block's scale it shares with three lanes.
-// 1 x 8192 x 1024 from BF16 takes 4.1 us so, and 2.5 + 3.8 with a kernel before it.
+// 1 x 8192 x 1024 from BF16 takes 5.1 us so and 5.7 with a kernel before it, calls in a row.
 constexpr int kFewTile = 16;
 
 struct Fp8Few;  // as X: e4m3
