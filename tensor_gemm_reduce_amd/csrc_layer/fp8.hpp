@@ -633,8 +633,11 @@ struct Fp8Run {
 // a row at chunk c ^ r.  A lane has 4 W neighbouring columns of a row for each g.  Direct stores of those, 16 bytes in
 // each of 64 lines an instruction, were slower: 2048 x 3584 x 8192 66 us instead of 60, 4096^3 64 instead of 56, 8192 x
 // 3584 x 2048 in FP32 128 instead of 106.
-// Stored past the caches, which hold x and w for the tiles to come: 32768 x 8192 x 3584 803 us without, 767 with; the
-// gradients of 64 experts' weights, 738 MB in FP32, 429 and 341.
+// Rows that start at whole lines of 128 bytes are stored past the caches, which hold x and w for the tiles to come: 32768 x
+// 8192 x 3584 803 us without, 767 with; the gradients of 64 experts' weights, 738 MB in FP32, 360 .. 379 and 321 .. 347.
+// Others go through the caches, which join the parts of a line: the same gradients with rows of 2045 instead of 2048 575 us
+// past them and 444 so, 8192 x 8185 x 1024 124 and 79, 8192 x 3581 x 2048 in FP32 154 and 107.  Rows at 64 bytes, which
+// go with the others, gain or lose (8192 x 8160 x 1024 94 and 78, 32768 x 8160 x 3584 794 and 838).
 // area: the wave's own 4 KB; m0, n0: the wave's first row and column.  FULL: no row or column past the end, so that every
 // wave has the same number of stores.
 // Accumulators stay where they are, in AGPRs and in one piece: the compiler otherwise takes them apart on the way from the
@@ -663,6 +666,7 @@ struct Fp8Store {
         int lane = threadIdx.x & 63;
         __asm__ __volatile__("" : "+v"(lane));  // keeps the addresses from being held in registers over all tiles
         const int r = lane & 31, h = lane >> 5, c = lane % kChunks;
+        const bool lines = ((reinterpret_cast<uint64_t>(a.out) | (uint64_t)shift * sizeof(T) | (uint64_t)a.out_stride * sizeof(T)) & 127) == 0;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             if constexpr (W == 4) fp8_hold<W>(acc[i]);
@@ -693,7 +697,12 @@ struct Fp8Store {
                     if (FULL || n + kPer <= a.N) {
                         if constexpr (fp8_exact<T>)
                             if (a.add) v += *reinterpret_cast<const out_t*>(a.add + shift + m * a.add_stride + n);
-                        __builtin_nontemporal_store(v, reinterpret_cast<out_t*>(out));
+                        if (lines) {  // the empty statements keep the compiler from making one store of the two, through the caches
+                            __asm__ __volatile__("" ::: "memory");
+                            __builtin_nontemporal_store(v, reinterpret_cast<out_t*>(out));
+                            __asm__ __volatile__("" ::: "memory");
+                        } else
+                            *reinterpret_cast<out_t*>(out) = v;
                     } else {
 #pragma unroll
                         for (int q = 0; q < kPer - 1; ++q)

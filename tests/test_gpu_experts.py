@@ -188,6 +188,22 @@ def test_linear_strides_add_and_out(M, N, K):
     assert (base[:, 0] == 99).all() and (base[:, N + 1:] == 99).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("extra,offset", [(0, 0), (64, 0), (64, 1), (32, 32), (8, 8), (1, 0)])
+def test_linear_rows_of_results_at_any_address(dtype, extra, offset):
+    """Rows at whole lines and elsewhere are stored in two ways; large tiles, some of them past the end."""
+    g = gen(13)
+    M, N, K = 4100, 4096, 128
+    x, w = integers(g, M, K, low=-3, high=3), integers(g, N, K, low=-3, high=3)
+    pitch = N + extra
+    buf = torch.full((offset + (M + 1) * pitch,), 99.0, dtype=dtype, device="cuda")
+    out = buf[offset:offset + M * pitch].view(M, pitch)[:, :N]
+    ex.fp8_linear(x.to(BF16).cuda(), ex.fp8_pack(w.cuda()), out=out)
+    assert torch.equal(out.cpu(), (x @ w.t()).to(dtype))  # integers of at most 1152: exact in FP32, rounded once
+    out.fill_(99.0)
+    assert (buf == 99).all()   # nothing beside the rows
+
+
 def test_linear_of_no_rows():
     weight = ex.fp8_pack(torch.ones((8, 16), dtype=BF16, device="cuda"))
     assert ex.fp8_linear(torch.ones((0, 16), dtype=BF16, device="cuda"), weight).shape == (0, 8)
