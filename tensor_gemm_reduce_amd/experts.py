@@ -22,8 +22,8 @@ import torch
 
 from . import layer as _layer
 from .gemm_rs import ERR_UNSUPPORTED_SHAPE
-from .layer import (_CODES, GemmRSLayerError, _check, _device, _elsewhere, _flat, _grad_mode, _lost_gradient, _on_stream, _ptr,
-                    _raw_stream, _rows, _two)
+from .layer import (_CODES, GemmRSLayerError, _check, _device, _elsewhere, _flat, _on_stream, _ptr, _raw_stream,
+                    _rows, _two)
 
 # ---- constants mirrored from include/gemm_rs_experts.h -------------------------
 FP8_BLOCK = 128
