@@ -32,16 +32,24 @@ extern "C" {
 /* ---- matrices in 8 bits ---------------------------------------------------- */
 
 /* A matrix [rows][cols] in e4m3 with scales 2^e (E8M0 bytes, e + 127):
- *   q       [rows][Kp], Kp = cols rounded up to 128; the columns past cols are 0
- *   scales  [Kp / 128][Rp], Rp = rows rounded up to 4: byte [b][r] is the scale of
- *           columns 128 b .. 128 b + 127 of row r; bytes past rows are not used,
- *           the others 1 .. 254
- * both contiguous and 16-byte aligned.  A block holds
+ *   q       [rows][Kp], Kp = cols rounded up to 128; the columns past cols are 0 (NaN in
+ *           a block that stands for NaN)
+ *   scales  [Kp / 128][Rp], Rp = rows + 3 rounded up to 4: byte [b][r] is the scale of
+ *           columns 128 b .. 128 b + 127 of row r, 1 .. 254; the Rp - rows bytes behind
+ *           a block's last row are not used, but the products read them: they take the
+ *           scales of four neighbouring rows as a word, from any row on
+ * both contiguous and 16-byte aligned; of E matrices, E times GEMM_RS_FP8_Q_BYTES and
+ * E times GEMM_RS_FP8_SCALE_BYTES, one after the other.  A block holds
  *   e = the smallest integer >= -126 with max |x| <= 448 2^e,  q = e4m3(x 2^-e)
  * rounded to nearest even, and stands for q 2^e (2^128, past FP32's range, from
- * |x| = 1.9375 2^127 on); a block with an infinity or a NaN stands for NaN.  The calls below make blocks of one row (activations, gradients)
- * or of 128 rows that share a scale (weights, which may then be transposed). */
+ * |x| = 1.9375 2^127 on); a block with an infinity or a NaN stands for NaN.  The calls
+ * below make blocks of one row (activations, gradients) or of 128 rows that share a
+ * scale (weights, which may then be transposed). */
 #define GEMM_RS_FP8_BLOCK 128
+#define GEMM_RS_FP8_BLOCKS(cols) (((int64_t)(cols) + 127) / 128)              /* Kp / 128 */
+#define GEMM_RS_FP8_SCALE_ROWS(rows) (((int64_t)(rows) + 6) / 4 * 4)          /* Rp       */
+#define GEMM_RS_FP8_Q_BYTES(rows, cols) ((int64_t)(rows) * GEMM_RS_FP8_BLOCKS(cols) * 128)
+#define GEMM_RS_FP8_SCALE_BYTES(rows, cols) (GEMM_RS_FP8_SCALE_ROWS(rows) * GEMM_RS_FP8_BLOCKS(cols))
 #define GEMM_RS_DTYPE_FP8 3 /* of an operand of gemm_rs_fp8_linear given so */
 
 /* x [M][K] (BF16, F16 or F32) in blocks of one row. */

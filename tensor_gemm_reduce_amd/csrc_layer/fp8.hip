@@ -13,9 +13,9 @@ constexpr int64_t kMaxWidth = 1 << 22;
 constexpr int64_t kFewRows = 16;  // of the kernel for few rows, which has a form for twice as many
 constexpr int64_t kMaxResource = (int64_t(1) << 31) - 1;  // bytes of a buffer resource below kOob
 
-int64_t blocks_of(int64_t n) { return ceil_div(n, kFp8Block); }
-int64_t pitch_of(int64_t rows) { return ceil_div(rows + 3, 4) * 4; }  // bytes from a block's scales to the next one's
-int64_t scale_bytes(int64_t rows, int64_t cols) { return pitch_of(rows) * blocks_of(cols); }
+int64_t blocks_of(int64_t n) { return GEMM_RS_FP8_BLOCKS(n); }
+int64_t pitch_of(int64_t rows) { return GEMM_RS_FP8_SCALE_ROWS(rows); }  // bytes from a block's scales to the next one's
+int64_t scale_bytes(int64_t rows, int64_t cols) { return GEMM_RS_FP8_SCALE_BYTES(rows, cols); }
 int64_t up16(int64_t n) { return ceil_div(n, 16) * 16; }
 bool is_float(int dtype) { return dtype >= GEMM_RS_DTYPE_BF16 && dtype <= GEMM_RS_DTYPE_F32; }
 
@@ -210,7 +210,7 @@ bool few_raw(const gemm_rs_fp8_args& g)
 }
 
 // q and scales of x in the workspace
-size_t quant_bytes(int64_t rows, int64_t K) { return (size_t)(up16(rows * blocks_of(K) * kFp8Block) + up16(scale_bytes(rows, K))); }
+size_t quant_bytes(int64_t rows, int64_t K) { return (size_t)(up16(GEMM_RS_FP8_Q_BYTES(rows, K)) + up16(scale_bytes(rows, K))); }
 
 int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t workspace_bytes, void* stream)
 {
