@@ -40,7 +40,8 @@ extern "C" {
  *           scales of four neighbouring rows as a word, from any row on
  * both contiguous and 16-byte aligned; of E matrices, E times GEMM_RS_FP8_Q_BYTES and
  * E times GEMM_RS_FP8_SCALE_BYTES, one after the other.  A block holds
- *   e = the smallest integer >= -126 with max |x| <= 448 2^e,  q = e4m3(x 2^-e)
+ *   e = the smallest integer >= -126 with max |x| <= 448 2^e (0 where all are zeros or one
+ *   is no number),  q = e4m3(x 2^-e)
  * rounded to nearest even, and stands for q 2^e (2^128, past FP32's range, from
  * |x| = 1.9375 2^127 on); a block with an infinity or a NaN stands for NaN.  The calls
  * below make blocks of one row (activations, gradients) or of 128 rows that share a

@@ -29,6 +29,9 @@ __device__ __forceinline__ int fp8_exponent(uint32_t top)
     const int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
     return e > kFp8MinExp ? e : kFp8MinExp;
 }
+// A block of zeros has the scale one, and so has a block of NaN: what they hold needs no other, and the lowest costs FP32
+// products a second pass.
+__device__ __forceinline__ int fp8_block_exponent(uint32_t top) { return top == 0 || top >= 0x7F800000u ? 0 : fp8_exponent(top); }
 
 // Four values times 2^-e as e4m3 bytes; all NaN in a block with an infinity or a NaN.
 __device__ __forceinline__ uint32_t fp8_word(float a, float b, float c, float d)
@@ -79,7 +82,7 @@ __global__ __launch_bounds__(256) void fp8_quant_kernel(const Fp8QuantArgs a)
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
         const bool bad = top >= 0x7F800000u;
-        const int e = bad ? 0 : fp8_exponent(top);
+        const int e = fp8_block_exponent(top);
         const float inv = fp8_inverse(e);
         u32x2 w = {fp8_word(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
                    fp8_word(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
@@ -193,15 +196,14 @@ __global__ __launch_bounds__(256) void fp8_quant_t_kernel(const Fp8QuantArgs a)
     for (int j = 0; j < 8; ++j) {
         const uint32_t m = top[cg * 8 + j];
         const bool bad = m >= 0x7F800000u;
-        const float inv = fp8_inverse(bad ? 0 : fp8_exponent(m));
+        const float inv = fp8_inverse(fp8_block_exponent(m));
         const uint32_t w = fp8_word((float)v[0][j] * inv, (float)v[1][j] * inv, (float)v[2][j] * inv, (float)v[3][j] * inv);
         *reinterpret_cast<uint32_t*>(out + (cg * 8 + j) * kPitch + rg * 4) = bad ? kFp8Nan4 : w;
     }
     __syncthreads();
     const int64_t kb = blockIdx.x;
     if (tid < kCols && c0 + tid < a.K) {
-        const uint32_t m = top[tid];
-        a.s[kb * a.pitch + c0 + tid] = (uint8_t)((m >= 0x7F800000u ? 0 : fp8_exponent(m)) + 127);
+        a.s[kb * a.pitch + c0 + tid] = (uint8_t)(fp8_block_exponent(top[tid]) + 127);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -249,7 +251,7 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const Fp8PackArgs a)
     __syncthreads();
     m = top;
     const bool bad = m >= 0x7F800000u;
-    const int e = bad ? 0 : fp8_exponent(m);
+    const int e = fp8_block_exponent(m);
     const float inv = fp8_inverse(e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -302,9 +304,18 @@ struct Fp8Args {
 // Results in FP32 take every product whole: the scaled MFMA lines the products of eight neighbouring inputs up with the
 // largest of them and drops from each what lies below its 2^-13 (measured; the sums with the accumulator are FP32's).  F16's
 // half step is 2^-11 and BF16's 2^-8, so that it matters to them only where a sum cancels; FP32's is 2^-24, so there the
-// operands are multiplied in BF16, at half the rate.
+// operands are multiplied in BF16, at half the rate, and block by block where their scales are past BF16's.
 template <class T>
 constexpr bool fp8_exact = std::is_same<T, float>::value;
+
+// Which of four scales may have values q 2^e that are no normal BF16 numbers: below 2^-117 the smallest are not, 2^-9 2^e, above
+// 2^119 the largest, 448 2^e.  The highest bit of each byte is 0 where the byte's upper four bits are all alike, 2^-127 ..
+// 2^-112 and 2^113 and above, which takes the fewest instructions.
+__device__ __forceinline__ uint32_t fp8_near(uint32_t s)
+{
+    const uint32_t d = s ^ (s << 1);
+    return d | (d << 1) | (d << 2);
+}
 
 __device__ __forceinline__ float fp8_scale(uint32_t byte) { return __uint_as_float((byte & 255u) << 23); }
 
@@ -383,6 +394,7 @@ struct Fp8Run {
     i32x4 f[2][2 * W][2];  // fragments of w, then of x, in two chunks
     bf16x8 wide[2][EXACT ? 2 * W : 1];  // a quarter of a half step: w's, then x's
     int sx[2][MODE == kGather ? W : 1], sw[2];  // scales of an even and an odd step
+    uint32_t far_x = 0, far_w = 0;  // EXACT: the scales' bytes that were not fp8_near (W = 2: w's in the upper half of far_x)
     uint32_t xo[MODE == kGather ? kLoads : 1], wo;  // a thread's chunk of a stage, first or of each load
     uint32_t sxo[MODE == kGather ? W : 1], swo;
     uint32_t get[2][4];  // LDS offsets of the lane's chunks of the first stage: operand, chunk
@@ -483,6 +495,31 @@ struct Fp8Run {
             load(rsx, sxo[0] | skip, kx, 1);
         __builtin_amdgcn_sched_barrier(0);  // the waits count them
     }
+    // Counts the scales of a step in.
+    template <int P>
+    __device__ __forceinline__ void see_scales(int s)
+    {
+        uint32_t x = (uint32_t)sx[P & 1][0], w = (uint32_t)sw[P & 1];
+        if constexpr (MODE == kGather) {
+            x = __builtin_amdgcn_perm((uint32_t)sx[P & 1][1], x, 0x0C0C0400);  // the lowest bytes, side by side
+            if constexpr (W == 4)
+                x |= __builtin_amdgcn_perm((uint32_t)sx[P & 1][3], (uint32_t)sx[P & 1][2], 0x04000C0C);
+        }
+        const uint32_t on = P == 0 ? ~0u : (uint32_t)live(s);  // an even step is there
+        if constexpr (W == 2) far_x |= on & ~fp8_near((x & 0xFFFFu) | w << 16);
+        else {
+            far_x |= on & ~fp8_near(x);
+            far_w |= on & ~fp8_near(w);
+        }
+    }
+    // Whether one of the wave's rows of x or w has a block of such a scale.
+    __device__ __forceinline__ bool far(const Fp8Place& p) const
+    {
+        const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), row = W * (lane & 31);
+        auto bytes = [&](int64_t left) { return (left <= 0 ? 0u : left >= W ? ~0u >> (32 - 8 * W) : (1u << (8 * (int)left)) - 1) & 0x80808080u; };
+        const uint32_t x = bytes(p.m1 - p.m0 - (wave >> 1) * 32 * W - row), w = bytes(a.N - p.n0 - (wave & 1) * 32 * W - row);
+        return W == 2 ? __any(far_x & (x | w << 16)) : __any((far_x & x) | (far_w & w));
+    }
     template <int Q>
     __device__ __forceinline__ void read_scales()
     {
@@ -570,6 +607,7 @@ struct Fp8Run {
             for (int i = kPer * M; i < kPer * (M + 1) && i < kReads; ++i) f[1][i / 2][i % 2] = read<P>(1, i / 2, i % 2);
             __builtin_amdgcn_sched_barrier(0);
         });
+        if constexpr (EXACT) see_scales<P>(s);
         if (STORES > 0 && stores) wait<(NS - 2) * kStep + STORES>();
         else wait<(NS - 2) * kStep>();
         barrier();
@@ -611,6 +649,7 @@ struct Fp8Run {
 #pragma unroll
         for (int i = 0; i < 4 * W; ++i) f[0][i / 2][i % 2] = read<0>(0, i / 2, i % 2);
         read_scales<0>();
+        far_x = far_w = 0;
         if constexpr (EXACT)
 #pragma unroll
             for (int i = 0; i < 2 * W; ++i) widen_piece<0, 0>(0, i);
@@ -719,6 +758,63 @@ struct Fp8Store {
     }
 };
 
+// The results of a wave with scales that take its values out of BF16, computed and stored again: the products of a block are
+// summed as they are, in FP32, and the sum is scaled by both scales at once.  A tile of 32 x 32 at a time, straight from
+// memory: for values below 2^-103 and above 2^120, which programs seldom have: with one such row in
+// every tile 4096 x 4096 x 384 takes 127 us instead of 27, 8192 x 8192 x 1024 890 instead of 140.  Looking for them costs 1 to 3%
+// (501 x 7168 x 8192 59 / 61 us, 8192 x 8192 x 1024 134 / 135).
+template <int W, int MODE>
+__device__ __forceinline__ void fp8_scaled_apart(const Fp8Args& a, const Fp8Place& p, int64_t shift, int64_t m0, int n0)
+{
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5, e = MODE == kSums ? 0 : p.e;
+#pragma unroll 1
+    for (int ij = 0; ij < W * W; ++ij) {
+        const int i = ij / W, j = ij % W, n = min(n0 + W * r + j, a.N - 1);  // rows past the last are read again, and not stored
+        const int64_t m = m0 + W * r + i;
+        int64_t row = m < p.m1 ? m : p.m1 - 1;
+        bool none = false;
+        if constexpr (MODE == kGather) {
+            row = a.tokens[row];
+            none = row < 0 || row >= a.x_rows;
+            if (none) row = 0;
+        }
+        const uint8_t *x = a.x + row * a.x_pitch + 64 * h, *xs = a.xs + row;
+        const uint8_t *w = a.w + e * a.w_expert + n * a.w_pitch + 64 * h, *ws = a.ws + e * a.ws_expert + n;
+        f32x16 sum = {};
+#pragma unroll 1
+        for (int64_t s = p.s0; s < p.s1; ++s) {
+            const int ex = xs[s * a.xs_pitch], ew = ws[s * a.ws_pitch];
+            f32x16 part = {};
+#pragma unroll
+            for (int c = 0; c < 4; c += 2) {
+                i32x4 fx[2], fw[2];
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    fx[d] = none ? i32x4{} : *reinterpret_cast<const i32x4*>(x + s * kFp8Block + (c + d) * 16);
+                    fw[d] = *reinterpret_cast<const i32x4*>(w + s * kFp8Block + (c + d) * 16);
+                }
+                const i32x8 qx = __builtin_shufflevector(fx[0], fx[1], 0, 1, 2, 3, 4, 5, 6, 7);
+                const i32x8 qw = __builtin_shufflevector(fw[0], fw[1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp8_to_bf16(qw, q, 1.f), fp8_to_bf16(qx, q, 1.f), part, 0, 0, 0);
+            }
+#pragma unroll
+            for (int g = 0; g < 16; ++g) sum[g] += ldexpf(part[g], ex + __shfl(ew, 8 * (g / 4) + 4 * h + g % 4) - 254);
+        }
+        if (m < p.m1) {
+#pragma unroll
+            for (int g = 0; g < 16; ++g) {
+                const int at = n0 + W * (8 * (g / 4) + 4 * h + g % 4) + j;
+                if (at >= a.N) continue;
+                float v = sum[g];
+                if (a.add) v += a.add[shift + m * a.add_stride + at];
+                static_cast<float*>(a.out)[shift + m * a.out_stride + at] = v;
+            }
+        }
+    }
+}
+
 // Where tile `id` of tiles_m x tiles_n is: groups of four tile rows, column by column, so that the 32 tiles an XCD works on
 // at a time share rows of x and of w, and the group's rows of x (3.7 MB at 3584 inputs) stay in its L2 while the columns go
 // by: 32768 x 8192 x 3584 takes 816 / 798 / 870 us with groups of 3 / 4 / 8, 8192^3 402 / 391 / 391.
@@ -729,7 +825,8 @@ __device__ __forceinline__ void fp8_place(int id, int tiles_m, int tiles_n, int&
     tn = r / rows;
 }
 
-// EXACT: quarters of the fragments are turned to BF16, which holds every scaled value, beside the MFMAs of the quarter before.
+// EXACT: quarters of the fragments are turned to BF16, scaled, beside the MFMAs of the quarter before.  BF16 holds every value
+// q 2^e with e = -117 .. 119 as a normal number; a wave that has met a scale past fp8_near's computes its results again.
 template <int W, int NS, int MODE, class T>
 __global__ __launch_bounds__(256, W == 4 || NS == 4 ? 1 : 2) void fp8_kernel(const Fp8Args a)
 {
@@ -790,6 +887,8 @@ __global__ __launch_bounds__(256, W == 4 || NS == 4 ? 1 : 2) void fp8_kernel(con
             for (int u = 0; u < W; ++u) fp8_hold<W>(acc[u]);
         const int64_t shift = MODE == kSums ? p.e * a.out_expert : 0, m0 = p.m0 + (wave >> 1) * 32 * W, m1 = p.m1;
         const int n0 = p.n0 + (wave & 1) * 32 * W;
+        const bool far = fp8_exact<T> && run.far(p);
+        const Fp8Place at = p;
         bool more = false;
         if constexpr (Tile::kKeeps) {
             i += mine;
@@ -800,8 +899,10 @@ __global__ __launch_bounds__(256, W == 4 || NS == 4 ? 1 : 2) void fp8_kernel(con
             }
         }
         char* area = lds + Tile::kOut + wave * Tile::kArea;
-        full = m0 + 32 * W <= m1 && n0 + 32 * W <= a.N;
-        if (full) Store::template run<true>(a, area, shift, m0, m1, n0, acc);
+        full = m0 + 32 * W <= m1 && n0 + 32 * W <= a.N && !far;
+        if (far) {
+            if constexpr (fp8_exact<T>) fp8_scaled_apart<W, MODE>(a, at, shift, m0, n0);
+        } else if (full) Store::template run<true>(a, area, shift, m0, m1, n0, acc);
         else Store::template run<false>(a, area, shift, m0, m1, n0, acc);
         if (!more) break;
     }
@@ -850,7 +951,7 @@ struct FewInput {
         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
         const bool bad = top >= 0x7F800000u;
-        const int e = bad ? 0 : fp8_exponent(top);
+        const int e = fp8_block_exponent(top);
         const float inv = fp8_inverse(e);
         scale = e + 127;
         i32x8 w;
@@ -937,17 +1038,37 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_few_kernel(const Fp8Args a)
             const int at = kb + i * WAVES;
             if (at >= a.steps) break;
             const i32x8 fw = __builtin_shufflevector(b[i].w[0], b[i].w[1], 0, 1, 2, 3, 4, 5, 6, 7);
+            i32x8 fx[MF];
+            int scale[MF];
 #pragma unroll
-            for (int f = 0; f < MF; ++f) {
-                int scale;
-                const i32x8 fx = b[i].x.fragment(f, scale);
-                if constexpr (fp8_exact<T>) {
+            for (int f = 0; f < MF; ++f) fx[f] = b[i].x.fragment(f, scale[f]);
+            bool far = false;
+            if constexpr (fp8_exact<T>) {
+                static_assert(MF <= 2, "a word has room for three scales");
+                const uint32_t all = (uint32_t)b[i].ws << 24 | (uint32_t)scale[MF - 1] << 16 | (uint32_t)scale[0] << 8;
+                far = __any((~fp8_near(all) & 0x80808000u) != 0);
+            }
+            if (far) {  // a scale that may take values out of BF16: the block's sum is scaled
+#pragma unroll
+                for (int f = 0; f < MF; ++f) {
+                    f32x4 sum = {};
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
-                        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_to_bf16(fw, p, fp8_scale(b[i].ws)),
-                                                                         fp8_to_bf16(fx, p, fp8_scale(scale)), acc[f], 0, 0, 0);
-                } else
-                    acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fx, acc[f], 0, 0, 0, b[i].ws, 0, scale);
+                        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_to_bf16(fw, p, 1.f), fp8_to_bf16(fx[f], p, 1.f), sum, 0, 0, 0);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[f][c] += ldexpf(sum[c], scale[f] + __shfl(b[i].ws, 4 * q + c) - 254);
+                }
+            } else {
+#pragma unroll
+                for (int f = 0; f < MF; ++f) {
+                    if constexpr (fp8_exact<T>) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_to_bf16(fw, p, fp8_scale(b[i].ws)),
+                                                                             fp8_to_bf16(fx[f], p, fp8_scale(scale[f])), acc[f], 0, 0, 0);
+                    } else
+                        acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fx[f], acc[f], 0, 0, 0, b[i].ws, 0, scale[f]);
+                }
             }
             if (at + kAhead * WAVES < a.steps) load(b[i], at + kAhead * WAVES);
         }

@@ -1,9 +1,11 @@
-"""GPU tests of the experts' operators at the ends of their ranges: buffers of exactly the stated sizes."""
+"""GPU tests of the experts' operators at the ends of their ranges: buffers of exactly the stated sizes, and
+FP32 results of blocks whose scales are the lowest and highest."""
 import pytest
 import torch
 
+import experts_ref as ref
 from tensor_gemm_reduce_amd import experts as ex
-from test_gpu_experts import gen
+from test_gpu_experts import F32, gen, integers
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +45,137 @@ def test_calls_write_the_stated_layout_and_nothing_else(rows, cols):
         m = ex.Fp8(q.view(E, rows, kp).view(torch.float8_e4m3fn), s.view(E, kp // 128, rp), rows, cols)
         # quantised to within half a step of e4m3 of its block's largest value
         assert ((m.values() - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -9 * x.abs().max()).all()
+
+
+# ---- FP32 results at both ends of the scales ------------------------------------------------------------------------
+
+# exponents of blocks: the lowest (where e4m3's values times 2^e are no BF16 numbers), those beside it, and the highest
+ENDS = (-126, -125, -124, -120, -117, -110, 0, 113, 119, 120)
+
+
+def bytes_of(g, rows, K):
+    """Finite e4m3 bytes, subnormal ones and zeros among them; zeros past K."""
+    q = torch.randint(0, 256, (rows, (K + 127) // 128 * 128), generator=g, dtype=torch.int32)
+    q[q % 128 == 127] = 1
+    q[:, K:] = 0
+    return q.to(torch.uint8)
+
+
+def operand(g, e, K):
+    """(an Fp8 [.., rows][K] with block exponents e [.., rows][blocks], what it stands for in 64 bits); random unused bytes."""
+    lead, (rows, blocks) = e.shape[:-2], e.shape[-2:]
+    n = max(1, int(torch.tensor(lead).prod())) if lead else 1
+    q = bytes_of(g, n * rows, K).view(*lead, rows, blocks * 128)
+    s = torch.randint(0, 256, (*lead, blocks, (rows + 6) // 4 * 4), generator=g, dtype=torch.int32).to(torch.uint8)
+    s[..., :rows] = (e + 127).transpose(-1, -2).to(torch.uint8)
+    q = q.cuda().view(torch.float8_e4m3fn)
+    values = q.double() * torch.ldexp(torch.ones((), dtype=torch.float64, device="cuda"), e.cuda().repeat_interleave(128, -1))
+    return ex.Fp8(q, s.cuda(), rows, K), values[..., :K]
+
+
+def exponents(g, rows, blocks, share=1.0):
+    """Exponents of x's blocks: near ENDS in turn for a `share` of the rows, near zero for the others."""
+    e = torch.tensor([ENDS[b % len(ENDS)] for b in range(blocks)]) + torch.randint(-2, 3, (rows, blocks), generator=g)
+    e = torch.where(torch.rand((rows, 1), generator=g) < share, e, torch.randint(-3, 4, (rows, blocks), generator=g))
+    return e.clamp(-126, 120)
+
+
+def partners(g, rows, blocks, share=1.0):
+    """Those of w's: where all of x's rows are at an end, at the other one (products are about one); else part of the way, so
+    that no product leaves FP32."""
+    c = torch.tensor([ENDS[b % len(ENDS)] for b in range(blocks)])
+    e = -c if share == 1 else -20 * c.sign()
+    return (e + torch.randint(-2, 3, (rows, blocks), generator=g)).clamp(-126, 120)
+
+
+def near(got, x, w, add=0.0):
+    """Within (K + 2) 2^-24 sum |x| |w|, the stated bound, the rounding of the sum with add, and the rounding of K products to
+    multiples of 2^-149."""
+    want, mag = x @ w.t().contiguous(), x.abs() @ w.abs().t().contiguous()
+    bound = (x.shape[1] + 2) * 2.0 ** -24 * mag
+    off = (got.double() - (want + add)).abs()
+    ok = off <= bound + 2.0 ** -24 * (want + add).abs() + x.shape[1] * 2.0 ** -149
+    assert ok.all(), (int((~ok).sum()), float((off / (bound + 2.0 ** -149))[~ok].max()))
+
+
+# few rows, both forms; tiles of 128 x 128; of 256 x 256, one and more for a workgroup
+DENSE = [(3, 40, 300), (16, 33, 1300), (20, 40, 600), (130, 150, 1300), (300, 260, 130), (4090, 4096, 384), (8100, 4300, 256)]
+
+
+@pytest.mark.parametrize("M,N,K", DENSE)
+@pytest.mark.parametrize("share", [1.0, 0.003])
+def test_fp32_results_of_blocks_at_both_ends(M, N, K, share):
+    g = gen(M + N)
+    blocks = (K + 127) // 128
+    x, xv = operand(g, exponents(g, M, blocks, share), K)
+    w, wv = operand(g, partners(g, N, blocks, share), K)
+    near(ex.fp8_linear(x, w, dtype=F32), xv, wv)
+    add = integers(g, M, N).cuda()
+    got = add.clone()
+    assert ex.fp8_linear(x, w, add=got, out=got) is got
+    near(got, xv, wv, add.double())
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 40, 200), (17, 40, 200), (200, 130, 384)])
+@pytest.mark.parametrize("top", [2.0 ** -118, 2.0 ** -126, 2.0 ** -133, 1.99 * 2.0 ** 127])
+def test_fp32_results_of_operands_at_both_ends(M, N, K, top):
+    """Matrices whose largest values are at an end of FP32, quantised by the calls, times others that bring them back."""
+    g = gen(N)
+    x = torch.rand((M, K), generator=g) * (2 * torch.randint(0, 2, (M, K), generator=g) - 1) * top
+    w = torch.randn((N, K), generator=g) * (2.0 ** 100 if top < 1 else 2.0 ** -126)
+    near(ex.fp8_linear(x.cuda(), ex.fp8_pack(w.cuda())), ref.quantised(x).cuda(), ref.quantised(w, 128, 128).cuda())
+    near(ex.fp8_linear(w.cuda(), ex.fp8_pack(x.cuda())), ref.quantised(w).cuda(), ref.quantised(x, 128, 128).cuda())
+
+
+# T, E, k, N, K: few rows an expert; tiles of 128; of 256, one and more for a workgroup
+EXPERTS = [(6, 4, 2, 40, 300), (300, 3, 2, 140, 300), (8192, 2, 1, 1700, 384), (9000, 3, 2, 1700, 256)]
+
+
+@pytest.mark.parametrize("T,E,k,N,K", EXPERTS)
+@pytest.mark.parametrize("rows", [False, True])
+@pytest.mark.parametrize("share", [1.0, 0.01])
+def test_experts_fp32_results_of_blocks_at_both_ends(T, E, k, N, K, rows, share):
+    g = gen(T)
+    blocks = (K + 127) // 128
+    plan = ex.plan(torch.rand((T, E), generator=g).argsort(1)[:, :k].to(torch.int32).contiguous().cuda(), E)
+    at, tokens = plan.offsets.tolist(), plan.tokens.long()
+    x, xv = operand(g, exponents(g, T * k if rows else T, blocks, share), K)
+    w, wv = operand(g, torch.stack([partners(g, N, blocks, share) for _ in range(E)]), K)
+    y = ex.experts_linear(x, w, plan, rows=rows, dtype=F32)
+    for e in range(E):
+        r = slice(at[e], at[e + 1])
+        near(y[r], xv[r] if rows else xv[tokens[r]], wv[e])
+
+
+@pytest.mark.parametrize("T,E,N,K", [(300, 3, 70, 130), (700, 2, 2100, 2100), (1000, 4, 2750, 2700)])
+def test_experts_wgrad_of_operands_at_both_ends(T, E, N, K):
+    """Gradients of 2^-128 and inputs of 2^100, in some blocks; FP32 operands."""
+    g = gen(E)
+    plan = ex.plan(torch.randint(0, E, (T, 1), generator=g, dtype=torch.int32).cuda(), E)
+    at, tokens = plan.offsets.tolist(), plan.tokens.long().cpu()
+    dy, x = torch.randn((T, N), generator=g), torch.randn((T, K), generator=g)
+    dy[:, ::7] *= 2.0 ** -128
+    x[:, ::5] *= 2.0 ** 100
+    dw = ex.experts_wgrad(dy.cuda(), x.cuda(), plan)
+    for e in range(E):
+        r = slice(at[e], at[e + 1])
+        near(dw[e], ref.quantised(dy[r], 128, 1).t().contiguous().cuda(), ref.quantised(x[tokens[r]], 128, 1).t().contiguous().cuda())
+
+
+def test_blocks_of_zeros_beside_others():
+    """Zeros at the lowest scale, as a caller's own matrices may have them, change nothing."""
+    g = gen(3)
+    x, xv = operand(g, torch.zeros((300, 3), dtype=torch.int64), 384)
+    w, wv = operand(g, torch.zeros((200, 3), dtype=torch.int64), 384)
+    x.q.view(torch.uint8)[::2, 128:256] = 0
+    x.scales[1, :300:2] = 1
+    xv[::2, 128:256] = 0
+    near(ex.fp8_linear(x, w, dtype=F32), xv, wv)
+
+
+@pytest.mark.parametrize("M,N", [(5, 40), (130, 140)])
+def test_fp32_results_below_the_normal_range(M, N):
+    g = gen(M)
+    x, xv = operand(g, torch.full((M, 2), -90), 256)
+    w, wv = operand(g, torch.full((N, 2), -48), 256)
+    near(ex.fp8_linear(x, w, dtype=F32), xv, wv)
