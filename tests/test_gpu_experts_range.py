@@ -1,9 +1,10 @@
-"""GPU tests of the experts' operators at the ends of their ranges: buffers of exactly the stated sizes, and
-FP32 results of blocks whose scales are the lowest and highest."""
+"""GPU tests of the experts' operators at the ends of their ranges: buffers of exactly the stated sizes,
+FP32 results of blocks whose scales are the lowest and highest, and gradients of saturated scores."""
 import pytest
 import torch
 
 import experts_ref as ref
+from experts_ref import f64
 from tensor_gemm_reduce_amd import experts as ex
 from test_gpu_experts import F32, gen, integers
 
@@ -179,3 +180,37 @@ def test_fp32_results_below_the_normal_range(M, N):
     x, xv = operand(g, torch.full((M, 2), -90), 256)
     w, wv = operand(g, torch.full((N, 2), -48), 256)
     near(ex.fp8_linear(x, w, dtype=F32), xv, wv)
+
+
+# ---- the sigmoid's gradient where it saturates -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("E,k", [(6, 2), (40, 5), (300, 8)])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_sigmoid_gradient_of_saturated_logits(E, k, renormalise):
+    """dl = ds s (1 - s) to a few roundings of each factor, also where s is next to one: 1 - s is 1 / (1 + e^l)."""
+    g = gen(E)
+    T = 50
+    logits = 30 * (2 * torch.rand((T, E), generator=g) - 1)
+    logits[0, :4] = torch.tensor([8.0, 12.0, 17.0, 30.0])
+    r = ex.route(logits.cuda(), k, score="sigmoid", renormalise=renormalise)
+    dw = torch.randn((T, k), generator=g)
+    got = f64(ex.route_backward(dw.cuda(), logits.cuda(), r.experts, score="sigmoid", renormalise=renormalise))
+    l, e = f64(logits), r.experts.cpu().long()
+    s, rest = torch.sigmoid(l), torch.sigmoid(-l)
+    ds = f64(dw)
+    size = ds.abs()   # the sum of the magnitudes that make ds
+    if renormalise:
+        se = s.gather(1, e)
+        D = se.sum(1, keepdim=True) + 1e-20
+        ds, size = (ds - (ds * se).sum(1, keepdim=True) / D) / D, (size + (size * se).sum(1, keepdim=True) / D) / D
+    factor = (s * rest).gather(1, e)
+    want = torch.zeros_like(l).scatter_(1, e, ds * factor)
+    # each of s and 1 - s: exp (2 units), of a logit that is a number; the sum and the quotient: 4; their product, ds: k + 8
+    bound = torch.zeros_like(l).scatter_(1, e, (k + 24) * 2.0 ** -24 * size * factor) + 1e-37
+    bad = (got - want).abs() > bound
+    assert not bad.any(), float(((got - want).abs() / bound).max())
+    # against differences of the score, in 64 bits: h^2 / 6 of it and less, and two scores' roundings of 2^-52 each over 2 h
+    h = 1e-4
+    diff = (torch.sigmoid(l + h) - torch.sigmoid(l - h)) / (2 * h)
+    bad = (diff - s * rest).abs() > h * h / 6 * s * rest + 2 * 2.0 ** -52 / (2 * h)
+    assert not bad.any()
