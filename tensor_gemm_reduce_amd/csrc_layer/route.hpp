@@ -541,8 +541,11 @@ struct RouteGradArgs {
 };
 
 // Scores are computed again.  ds is what the weights pass to the scores that were chosen;
-// softmax: dl = s (ds - sum ds s), sigmoid: dl = ds s (1 - s), where 1 - s is 1 / (1 + e^l): the difference has lost a
-// hundredth of itself at l = 12 and all of it from 17 on.
+// softmax: dl = s (ds - sum ds s), sigmoid: dl = ds s (1 - s).  Where one score is nearly all, what is left are the others'
+// parts, which differences of nearly equal numbers lose (a hundredth of 1 - s at a sigmoid's logit of 12, all of it from 17 on):
+//   sigmoid      1 - s is 1 / (1 + e^l)
+//   softmax      for a score above a half, 1 - s is the sum of the others, and its own term leaves sum ds s
+//   renormalise  (dw_i - sum_j dw_j s_j / D) / D is sum_j s_j (dw_i - dw_j) / D^2, and 1e-20 dw_i / D^2
 template <int SEG, int NV>
 __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs a)
 {
@@ -568,29 +571,43 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
         const float v = __shfl(p[i], part * SEG + (e & (SEG - 1)));
         if (e >= 0 && e / 64 == i) s = v;
     }
+    auto choice = [&](auto v, int j) {  // choice j's
+        if constexpr (SEG == 64) return lane_value(v, j);
+        else return __shfl(v, part * SEG + j);
+    };
     if (a.renormalise) {
         const float inv = 1.f / (seg_sum<SEG>(s) + 1e-20f);
-        dw = (dw - seg_sum<SEG>(dw * s) * inv) * inv;
-        if (e < 0) dw = 0.f;
+        float sum = 1e-20f * dw;
+        for (int j = 0; j < a.k; ++j) sum += choice(s, j) * (dw - choice(dw, j));
+        dw = e < 0 ? 0.f : sum * inv * inv;
     }
-    float dot = 0.f;
     for (int j = 0; j < a.k; ++j) {
-        const int ej = __shfl(e, part * SEG + j);
-        const float dj = __shfl(dw, part * SEG + j);
+        const int ej = choice(e, j);
+        const float dj = choice(dw, j);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (ej == i * 64 + sub) ds[i] += dj;
     }
+    float rest = 0.f, dot = 0.f, all = 0.f;  // sums of s and ds s without a score above a half, of ds s
     if (!a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) dot += ds[i] * p[i];
+        for (int i = 0; i < NV; ++i) {
+            const float d = ds[i] * p[i];
+            rest += p[i] > 0.5f ? 0.f : p[i];
+            dot += p[i] > 0.5f ? 0.f : d;
+            all += p[i] > 0.5f ? d : 0.f;
+        }
+        rest = seg_sum<SEG>(rest);
         dot = seg_sum<SEG>(dot);
+        all = dot + seg_sum<SEG>(all);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int at = i * 64 + sub;
         if (!live || at >= a.E) continue;
-        const float d = a.sigmoid ? ds[i] * (p[i] * (1.f / (1.f + expf(l[i])))) : p[i] * (ds[i] - dot);
+        const float d = a.sigmoid      ? ds[i] * (p[i] * (1.f / (1.f + expf(l[i]))))
+                        : p[i] > 0.5f ? p[i] * (ds[i] * rest - dot)
+                                      : p[i] * (ds[i] - all);
         const int64_t to = t * a.dstride + at;
         if (a.dtype == 0) static_cast<__bf16*>(a.dlogits)[to] = (__bf16)d;
         else if (a.dtype == 1) static_cast<_Float16*>(a.dlogits)[to] = (_Float16)d;

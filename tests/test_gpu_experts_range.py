@@ -214,3 +214,42 @@ def test_sigmoid_gradient_of_saturated_logits(E, k, renormalise):
     diff = (torch.sigmoid(l + h) - torch.sigmoid(l - h)) / (2 * h)
     bad = (diff - s * rest).abs() > h * h / 6 * s * rest + 2 * 2.0 ** -52 / (2 * h)
     assert not bad.any()
+
+
+@pytest.mark.parametrize("E,k", [(2, 1), (2, 2), (6, 2), (40, 5), (300, 8), (1000, 64)])
+@pytest.mark.parametrize("renormalise", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_where_one_score_is_nearly_all(E, k, renormalise, score):
+    """What is left of the others counts: sums of s_j (g_i - g_j), relative to the terms that are there, not to g_i."""
+    g = gen(E + k)
+    T = 60
+    logits = torch.randn((T, E), generator=g)
+    for t in range(T):
+        logits[t, t % E] += t / 2   # ahead of the rest by up to 30
+    r = ex.route(logits.cuda(), k, score=score, renormalise=renormalise, scale=2.0)
+    dw = torch.randn((T, k), generator=g)
+    got = f64(ex.route_backward(dw.cuda(), logits.cuda(), r.experts, score=score, renormalise=renormalise, scale=2.0))
+    l, e = f64(logits), r.experts.cpu().long()
+    s = torch.softmax(l, 1) if score == "softmax" else torch.sigmoid(l)
+    se, ds = s.gather(1, e), 2 * f64(dw)
+    size = ds.abs()
+    if renormalise:
+        D = se.sum(1)[:, None, None] + 1e-20
+        apart = ds[:, :, None] - ds[:, None, :]              # [i][j]
+        sizes = (ds.abs()[:, :, None] + ds.abs()[:, None, :]) * (1 - torch.eye(k))
+        ds, size = (((se[:, None, :] * a).sum(2, keepdim=True) / D / D)[:, :, 0] + 1e-20 * b / D[:, :, 0] ** 2
+                    for a, b in ((apart, ds), (sizes, size)))
+    full, full_size = (torch.zeros_like(l).scatter_(1, e, v) for v in (ds, size))
+    if score == "softmax":
+        others = s.sum(1, keepdim=True) - s                  # 1 - s, by what is not s: the largest's is summed without it
+        top = s.argmax(1, keepdim=True)
+        others.scatter_(1, top, s.scatter(1, top, 0.0).sum(1, keepdim=True))
+        rest = lambda v: torch.stack([(s * v).scatter(1, torch.full((T, 1), i), 0.0).sum(1) for i in range(E)], 1)  # noqa: E731
+        want, mag = s * (full * others - rest(full)), s * (full_size * others + rest(full_size))
+    else:
+        want, mag = full * s * torch.sigmoid(-l), full_size * s * torch.sigmoid(-l)
+    # in units of 2^-24: a score's exp is of a rounded difference of up to 35 (half of it, and 2), its sum has E / 64 + 6 in a row, and
+    # a quotient: 28 + E / 64; a term has up to four of them, two sums over k and one more over E / 64 + 6
+    rel = (4 * (28 + E / 64) + 2 * k + E / 64 + 24) * 2.0 ** -24
+    bad = (got - want).abs() > rel * mag + 1e-37
+    assert not bad.any(), (int(bad.sum()), float(((got - want).abs() / (rel * mag + 1e-37)).max()))
