@@ -73,7 +73,8 @@ int gemm_rs_fp8_pack(int32_t dtype, int64_t E, int64_t N, int64_t K, int32_t tra
  * 2^-10 of the largest product of every eight inputs, summed over K.
  * gemm_rs_fp8_linear: E, offsets and tokens are 0 and x_rows is M.
  * gemm_rs_experts_linear: rows offsets[e] .. offsets[e + 1] - 1 take the weights of
- * expert e; row m's input is row m of x, or row tokens[m] where tokens are given.
+ * expert e; row m's input is row m of x, or row tokens[m] where tokens are given (zeros
+ * for a token outside 0 .. x_rows - 1, as in gemm_rs_experts_wgrad).
  * Rows of out from offsets[E] on stay as they were.  M bounds offsets[E].
  * Sizes: N and K up to 2^22, E up to GEMM_RS_ROUTE_MAX_EXPERTS, scales of an operand
  * and x's q where it is gathered less than 2 GiB. */
@@ -81,7 +82,7 @@ typedef struct gemm_rs_fp8_args {
     int32_t x_dtype;         /* BF16, F16, F32: quantised by the call in blocks of a row; FP8 */
     int32_t out_dtype;       /* BF16, F16 or F32                                     */
     int64_t M, N, K;
-    int64_t x_rows;          /* rows of x                                            */
+    int64_t x_rows;          /* rows of x: 1 or more, but with M = 0                  */
     int64_t E;
     const void *x;           /* [x_rows][K], or q of an FP8 matrix                   */
     int64_t x_stride;        /* not of FP8                                           */

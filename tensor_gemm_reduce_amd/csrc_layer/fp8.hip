@@ -216,7 +216,7 @@ int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t
 {
     if (!fp8_args_ok(g)) return GEMM_RS_ERR_INVALID_ARG;
     if (experts ? g->E < 1 || !g->offsets : g->E != 0 || g->offsets || g->tokens) return GEMM_RS_ERR_INVALID_ARG;
-    if (!g->tokens && g->x_rows != g->M) return GEMM_RS_ERR_INVALID_ARG;
+    if (g->tokens ? g->x_rows == 0 && g->M > 0 : g->x_rows != g->M) return GEMM_RS_ERR_INVALID_ARG;
     const int64_t blocks = blocks_of(g->K), pitch = blocks * kFp8Block;
     if (g->M >= kMaxRows || g->x_rows >= kMaxRows || g->N > kMaxWidth || g->K > kMaxWidth || g->E > GEMM_RS_ROUTE_MAX_EXPERTS ||
         scale_bytes(g->x_rows, g->K) > kMaxResource || scale_bytes(g->N, g->K) > kMaxResource ||
@@ -225,11 +225,9 @@ int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t
     if (g->M == 0) return GEMM_RS_OK;
     const bool raw = g->x_dtype != GEMM_RS_DTYPE_FP8;
     Checker c;
-    if (g->x_rows > 0) {
-        c.need(g->x, raw ? elem_bytes(g->x_dtype) : 16);
-        if (raw) c.stride(g->x_stride, g->K);
-        else c.need(g->x_scales, 16);
-    }
+    c.need(g->x, raw ? elem_bytes(g->x_dtype) : 16);
+    if (raw) c.stride(g->x_stride, g->K);
+    else c.need(g->x_scales, 16);
     c.need(g->w, 16);
     c.need(g->w_scales, 16);
     c.maybe(g->offsets, 4);
@@ -248,7 +246,6 @@ int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t
     if (c.code != GEMM_RS_OK) return c.code;
     int device = 0, rc = check_device(&device);
     if (rc != GEMM_RS_OK) return rc;
-    if (g->x_rows == 0) return GEMM_RS_OK;  // no row can have an input
     Fp8Args a = {};
     a.x = static_cast<const uint8_t*>(g->x);
     a.xs = static_cast<const uint8_t*>(g->x_scales);

@@ -1005,13 +1005,16 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_few_kernel(const Fp8Args a)
     const uint8_t* ws = a.ws + e * a.ws_expert + n;
     const char* x[MF];
     const uint8_t* xs[MF];
+    bool none[MF];  // kGather: the row has no input, as in fp8_kernel
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
+        none[f] = false;
         int64_t m = m0 + 16 * f + r;
         m = m < m1 ? m : m1 - 1;
         if constexpr (MODE == kGather) {
-            const int64_t t = a.tokens[m];
-            m = t < 0 ? 0 : t < a.x_rows ? t : a.x_rows - 1;
+            m = a.tokens[m];
+            none[f] = m < 0 || m >= a.x_rows;
+            if (none[f]) m = 0;
         }
         x[f] = reinterpret_cast<const char*>(a.x) + m * a.x_pitch;
         xs[f] = a.xs + m;
@@ -1041,7 +1044,10 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_few_kernel(const Fp8Args a)
             i32x8 fx[MF];
             int scale[MF];
 #pragma unroll
-            for (int f = 0; f < MF; ++f) fx[f] = b[i].x.fragment(f, scale[f]);
+            for (int f = 0; f < MF; ++f) {
+                fx[f] = b[i].x.fragment(f, scale[f]);
+                if (MODE == kGather && none[f]) fx[f] = i32x8{};
+            }
             bool far = false;
             if constexpr (fp8_exact<T>) {
                 static_assert(MF <= 2, "a word has room for three scales");

@@ -1,0 +1,16 @@
+"""Host-side refusals of the experts' calls at the ends of their sizes (no GPU calls)."""
+import ctypes
+
+import pytest
+
+from test_experts_host import fp8
+
+ex = pytest.importorskip("tensor_gemm_reduce_amd.experts")
+gr = pytest.importorskip("tensor_gemm_reduce_amd.gemm_rs")
+
+
+def test_rows_without_any_input_are_refused():
+    """Results of M rows from an x of none: there is nothing to take them from."""
+    call = lambda **kw: ex.lib().gemm_rs_experts_linear(ctypes.byref(fp8(E=2, offsets=256, tokens=256, **kw)), None, 0, None)  # noqa: E731
+    assert call(x_rows=0, M=4) == gr.ERR_INVALID_ARG
+    assert call(x_rows=0, M=0) == gr.OK

@@ -1,12 +1,13 @@
 """GPU tests of the experts' operators at the ends of their ranges: buffers of exactly the stated sizes,
-FP32 results of blocks whose scales are the lowest and highest, and gradients of saturated scores."""
+FP32 results of blocks whose scales are the lowest and highest, gradients of saturated scores, and
+tokens that no plan makes."""
 import pytest
 import torch
 
 import experts_ref as ref
 from experts_ref import f64
 from tensor_gemm_reduce_amd import experts as ex
-from test_gpu_experts import F32, gen, integers
+from test_gpu_experts import BF16, F32, gen, integers
 
 pytestmark = pytest.mark.gpu
 
@@ -253,3 +254,29 @@ def test_gradient_where_one_score_is_nearly_all(E, k, renormalise, score):
     rel = (4 * (28 + E / 64) + 2 * k + E / 64 + 24) * 2.0 ** -24
     bad = (got - want).abs() > rel * mag + 1e-37
     assert not bad.any(), (int(bad.sum()), float(((got - want).abs() / (rel * mag + 1e-37)).max()))
+
+
+# ---- tokens that no plan makes ----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,E,N,K,wide", [(6, 3, 20, 130, False), (6, 3, 20, 5000, False), (6, 3, 20, 130, True), (300, 2, 140, 130, False),
+                                          (8000, 2, 2100, 130, False)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_token_out_of_range_has_no_input(T, E, N, K, wide, dtype):
+    """Its row is zeros in every kernel: for few rows (quantising on the way, or not), and tiles of both sizes."""
+    g = gen(T)
+    plan = ex.plan((torch.arange(T, dtype=torch.int32) % E)[:, None].contiguous().cuda(), E)
+    bad = torch.tensor([-1, T, 1 << 30, -(1 << 31)], dtype=torch.int32).cuda()
+    plan.tokens[1::2] = bad.repeat((T + 3) // 4)[:plan.tokens[1::2].numel()]
+    x, w = integers(g, T, K, low=-3, high=3).to(dtype), integers(g, E, N, K, low=-3, high=3).to(dtype)
+    given = ex.fp8_quant(x.cuda()) if wide else x.cuda()
+    y = ex.experts_linear(given, ex.fp8_pack(w.cuda()), plan, dtype=dtype)
+    assert (y[1::2] == 0).all()
+    at = plan.offsets.tolist()
+    for e in range(E):
+        r = torch.arange(at[e], at[e + 1], device="cuda")
+        r = r[r % 2 == 0]
+        want = x.cuda().double()[plan.tokens[r].long()] @ w[e].cuda().double().t().contiguous()
+        assert torch.equal(y[r].double(), want.to(dtype).double())
+    if dtype is F32:
+        add = torch.full((T, N), 5.0, device="cuda")
+        assert (ex.experts_linear(given, ex.fp8_pack(w.cuda()), plan, add=add, dtype=F32)[1::2] == 5).all()
