@@ -109,6 +109,12 @@ def _ints(t, name, shape, dev):
     return t.data_ptr()
 
 
+def _plan_rows(routing, rows, dev):
+    """Addresses of a plan's first rows, and of its rows' tokens where x is gathered by them."""
+    return (_ints(routing.offsets, "routing.offsets", (routing.E + 1,), dev),
+            0 if rows else _ints(routing.tokens, "routing.tokens", (routing.rows,), dev))
+
+
 def _workspace(like, size):
     return like.new_empty(size, dtype=torch.uint8) if size else None
 
@@ -227,9 +233,7 @@ def _product(name, x, weight, routing, rows, add, out, dtype, stream):
         want = M if rows else routing.T
         if x_rows != want:
             raise ValueError(f"x: {x_rows} rows, the plan has {want} {'rows' if rows else 'tokens'}")
-        if routing.offsets.get_device() != dev:
-            raise ValueError(f"routing: on {routing.offsets.device}, not on the current device")
-        offsets, tokens = routing.offsets.data_ptr(), 0 if rows else routing.tokens.data_ptr()
+        offsets, tokens = _plan_rows(routing, rows, dev)
     elif weight.E:
         raise ValueError("weight: of several experts; use experts_linear")
     if out is not None:
@@ -277,14 +281,28 @@ class Routing:
     """What route and plan return, for T tokens with k choices of E experts each and R = T k rows:
     weights float32 [T][k] and experts int32 [T][k] (-1: none); offsets int32 [E + 1], the experts' first rows and the
     number of rows; tokens int32 [R], the rows' tokens (-1 behind the last row); slots int32 [T][k], the choices' rows
-    (-1: none).  plan leaves weights at None."""
+    (-1: none).  plan leaves weights at None.  A program's own plan has to have these types and shapes, contiguous and on one
+    device; what its numbers say is its own matter (rows and tokens out of range are not read)."""
 
     __slots__ = ("weights", "experts", "offsets", "tokens", "slots", "T", "k", "E", "rows")
 
     def __init__(self, weights, experts, offsets, tokens, slots, E):
+        T, k = _two(experts, "experts")
+        if E < 1:
+            raise ValueError(f"E: {E}")
+        dev = experts.get_device()
+        for t, name, shape in ((experts, "experts", (T, k)), (offsets, "offsets", (E + 1,)), (tokens, "tokens", (T * k,)),
+                               (slots, "slots", (T, k))):
+            _flat(t, name, shape, torch.int32, dev)
+        if weights is not None:
+            _flat(weights, "weights", (T, k), torch.float32, dev)
+        self._set(weights, experts, offsets, tokens, slots, E)
+
+    def _set(self, weights, experts, offsets, tokens, slots, E):
         self.weights, self.experts, self.offsets, self.tokens, self.slots, self.E = weights, experts, offsets, tokens, slots, E
         self.T, self.k = experts.shape
         self.rows = self.T * self.k
+        return self
 
 
 def _new_plan(like, T, k, E):
@@ -334,7 +352,7 @@ def route(logits, k, *, score="softmax", bias=None, groups=1, keep_groups=None, 
     _check(L.gemm_rs_route(cfg, T, logits.data_ptr(), ls, _ptr(bias), weights.data_ptr(), experts.data_ptr(),
                            _PLAN_ARGS.pack(offsets.data_ptr(), tokens.data_ptr(), slots.data_ptr()), _ptr(ws), size,
                            _raw_stream(dev)), "gemm_rs_route")
-    return Routing(weights, experts, offsets, tokens, slots, E)
+    return Routing.__new__(Routing)._set(weights, experts, offsets, tokens, slots, E)
 
 
 def plan(experts, num_experts, *, stream=None) -> Routing:
@@ -357,7 +375,7 @@ def plan(experts, num_experts, *, stream=None) -> Routing:
     _check(L.gemm_rs_expert_plan(T, num_experts, k, experts.data_ptr(),
                                  _PLAN_ARGS.pack(offsets.data_ptr(), tokens.data_ptr(), slots.data_ptr()), _ptr(ws), size,
                                  _raw_stream(dev)), "gemm_rs_expert_plan")
-    return Routing(None, experts, offsets, tokens, slots, num_experts)
+    return Routing.__new__(Routing)._set(None, experts, offsets, tokens, slots, num_experts)
 
 
 def route_backward(dweights, logits, experts, *, score="softmax", renormalise=True, scale=1.0, stream=None):
@@ -411,8 +429,7 @@ def experts_wgrad(dy, x, routing: Routing, *, rows=False, add=None, out=None, dt
     dev = _device(dy, "dy")
     E = routing.E
     ys, xs = _rows(dy, "dy", routing.rows, N, dy.dtype, dev), _rows(x, "x", routing.rows if rows else routing.T, K, dy.dtype, dev)
-    if routing.offsets.get_device() != dev:
-        raise ValueError(f"routing: on {routing.offsets.device}, not on the current device")
+    offsets, tokens = _plan_rows(routing, rows, dev)
     if out is not None:
         dtype = out.dtype
     if dtype is not torch.float32 and dtype is not dy.dtype:
@@ -432,7 +449,7 @@ def experts_wgrad(dy, x, routing: Routing, *, rows=False, add=None, out=None, dt
     if out is None:
         out = dy.new_empty((E, N, K), dtype=dtype)
     args = _WGRAD_ARGS.pack(code, _CODES[dtype], M, N, K, E, x_rows, dy.data_ptr(), ys, x.data_ptr(), xs,
-                            routing.offsets.data_ptr(), 0 if rows else routing.tokens.data_ptr(), _ptr(add), out.data_ptr())
+                            offsets, tokens, _ptr(add), out.data_ptr())
     L = lib()
     size = L.gemm_rs_experts_wgrad_workspace(args)
     ws = _workspace(dy, size)

@@ -280,3 +280,18 @@ def test_a_token_out_of_range_has_no_input(T, E, N, K, wide, dtype):
     if dtype is F32:
         add = torch.full((T, N), 5.0, device="cuda")
         assert (ex.experts_linear(given, ex.fp8_pack(w.cuda()), plan, add=add, dtype=F32)[1::2] == 5).all()
+
+
+@pytest.mark.parametrize("name", ["offsets", "tokens"])
+def test_a_plan_with_parts_exchanged_is_refused(name):
+    """Parts of other sizes or types, or in host memory, are refused by the calls that read them."""
+    plan = ex.plan(torch.zeros((4, 2), dtype=torch.int32, device="cuda"), 3)
+    x, dy, w = (torch.ones(s, dtype=BF16, device="cuda") for s in ((4, 16), (8, 8), (3, 8, 16)))
+    weight, whole = ex.fp8_pack(w), getattr(plan, name)
+    for part, error in ((whole[:-1], ValueError), (whole.long(), TypeError), (whole.cpu(), ValueError), (whole[:, None], ValueError)):
+        setattr(plan, name, part)
+        for call in (lambda: ex.experts_linear(x, weight, plan), lambda: ex.experts_wgrad(dy, x, plan)):
+            with pytest.raises(error, match=name):
+                call()
+    setattr(plan, name, whole)
+    assert (ex.experts_linear(x, weight, plan) == 16).all()
