@@ -352,8 +352,9 @@ __device__ __forceinline__ uint64_t route_groups(const F (&c)[NV], const float (
     const bool stays = group < groups && rank < keep;
     const F in = seg_all<64>(stays ? total : (F)INFINITY, [](F a, F b) { return a < b ? a : b; });
     const F out = seg_all<64>(stays || group >= groups ? (F)-INFINITY : total, [](F a, F b) { return a > b ? a : b; });
-    // groups that are off are last whatever the others' rounding
-    gap = out == -INFINITY ? (F)INFINITY : in - out;
+    // groups that are off are last whatever the others' rounding; sums of two that FP32 does not hold say nothing
+    const bool past = group < groups && lo != -INFINITY && (total == INFINITY || total == -INFINITY);
+    gap = __any(past) ? (F)0 : out == -INFINITY ? (F)INFINITY : in - out;
     __asm__ __volatile__("" ::: "memory");
     return __ballot(stays);
 }

@@ -1,6 +1,6 @@
 """GPU tests of the experts' operators at the ends of their ranges: buffers of exactly the stated sizes,
-FP32 results of blocks whose scales are the lowest and highest, gradients of saturated scores, and
-tokens that no plan makes."""
+FP32 results of blocks whose scales are the lowest and highest, gradients of saturated scores,
+biases at the types' ends, and tokens that no plan makes."""
 import pytest
 import torch
 
@@ -254,6 +254,32 @@ def test_gradient_where_one_score_is_nearly_all(E, k, renormalise, score):
     rel = (4 * (28 + E / 64) + 2 * k + E / 64 + 24) * 2.0 ** -24
     bad = (got - want).abs() > rel * mag + 1e-37
     assert not bad.any(), (int(bad.sum()), float(((got - want).abs() / (rel * mag + 1e-37)).max()))
+
+
+# ---- groups with biases at the types' ends ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [1, 40])
+def test_groups_whose_sums_leave_fp32(score, T):
+    """Biases of the type's lowest and highest value: sums of two are past FP32, not past 64 bits."""
+    low, high = torch.finfo(F32).min, torch.finfo(F32).max
+    off = -float("inf")
+    l = torch.tensor([0.5, -0.25, 1.0, 0.75, -0.5, 0.25, 2.0, 1.5])
+    cases = [
+        # a group that is off beside one whose experts are on, at the lowest bias: the latter stays
+        ([off, off, 1.0, 0.5, 0.25, 0.75, off, off], [0, 0, 0, 0, low, low, 0, 0], 4, 2),
+        # sums past the lowest value, that differ
+        (l.tolist(), [low, low, 0, 0, low * 0.75, low * 0.8, 0, 0], 4, 3),
+        # and past the highest
+        (l.tolist(), [0.6 * high, 0.7 * high, 0.9 * high, high, 0.8 * high, 0.75 * high, 0, 0], 4, 1),
+        (l.tolist(), [0.6 * high, 0.7 * high, 0.9 * high, high, 0.8 * high, 0.75 * high, 0, 0], 4, 2),
+    ]
+    for logits, bias, groups, keep in cases:
+        logits, bias = torch.tensor([logits]).repeat(T, 1), torch.tensor(bias)
+        for k in (1, 2, 4, 6):
+            want = ref.route(logits, k, score, bias, groups, keep, True, 1.0)[1]
+            r = ex.route(logits.cuda(), k, score=score, bias=bias.cuda(), groups=groups, keep_groups=keep)
+            assert torch.equal(r.experts.cpu(), want), (bias, keep, k, r.experts[0], want[0])
 
 
 # ---- tokens that no plan makes ----------------------------------------------------------------------------------------
