@@ -133,7 +133,7 @@ int gemm_rs_route_validate(const gemm_rs_route_config* c)
 
 size_t gemm_rs_expert_plan_workspace(int64_t T, int32_t E, int32_t k)
 {
-    return plan_sizes(T, E, k) && T * k < kMaxRows ? plan_bytes(T * k, E, route_chunk(T, E, k)) : 0;
+    return plan_sizes(T, E, k) && T < kMaxRows && T * k < kMaxRows ? plan_bytes(T * k, E, route_chunk(T, E, k)) : 0;
 }
 
 int gemm_rs_route(const gemm_rs_route_config* c, int64_t T, const void* logits, int64_t logits_stride, const float* bias,
