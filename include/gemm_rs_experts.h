@@ -97,6 +97,20 @@ typedef struct gemm_rs_fp8_args {
     int64_t out_stride;
 } gemm_rs_fp8_args;
 
+/* How a product of these arguments runs (their sizes, types and whether tokens are given;
+ * host only). */
+typedef struct gemm_rs_fp8_info {
+    int32_t tile;       /* edge of a workgroup's tile of results: 256 or 128; 16 or 32: the
+                           kernel for few rows, of so many by 16 columns (0: M is 0)  */
+    int32_t stages;     /* of inputs in LDS: 2 or 4; 0: few rows                      */
+    int32_t quantises;  /* 1: the product's own kernel quantises x                    */
+    int32_t tiles;      /* of the results; with experts' rows, at most               */
+    int32_t workgroups; /* of the product's kernel; with tiles of 256 at most 256, which
+                           take several where there are more                          */
+} gemm_rs_fp8_info;
+
+int gemm_rs_fp8_plan(const gemm_rs_fp8_args *args, gemm_rs_fp8_info *info);
+
 /* Bytes of workspace (16-byte aligned; its contents need not be set). */
 size_t gemm_rs_fp8_workspace(const gemm_rs_fp8_args *args);
 int gemm_rs_fp8_linear(const gemm_rs_fp8_args *args, void *workspace, size_t workspace_bytes, void *stream);
@@ -121,6 +135,7 @@ typedef struct gemm_rs_experts_wgrad_args {
     void *dw;               /* [E][N][K] contiguous */
 } gemm_rs_experts_wgrad_args;
 
+int gemm_rs_experts_wgrad_plan(const gemm_rs_experts_wgrad_args *args, gemm_rs_fp8_info *info);
 size_t gemm_rs_experts_wgrad_workspace(const gemm_rs_experts_wgrad_args *args);
 int gemm_rs_experts_wgrad(const gemm_rs_experts_wgrad_args *args, void *workspace, size_t workspace_bytes,
                           void *stream);

@@ -65,10 +65,13 @@ int quant_columns(int dtype, int64_t M, int64_t K, int64_t x_rows, const void* x
                   dim3((unsigned)blocks, (unsigned)ceil_div(K, 64)), 256, a, stream, "gemm_rs_fp8_quant_transposed");
 }
 
+// A launch has threads for all of the rows' blocks.
+bool quant_fits(int64_t M, int64_t K) { return ceil_div(M, 16) * blocks_of(K) <= kMaxThreads / 64 - 4; }
+
 int quant_check(int32_t dtype, int64_t M, int64_t K, const void* x, int64_t stride, const void* q, const void* s)
 {
     if (!is_float(dtype) || M < 0 || K < 1) return GEMM_RS_ERR_INVALID_ARG;
-    if (M >= kMaxRows || K > kMaxWidth || ceil_div(M, 16) * blocks_of(K) > kMaxThreads / 64 - 4) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    if (M >= kMaxRows || K > kMaxWidth || !quant_fits(M, K)) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return GEMM_RS_OK;
     Checker c;
     c.need(x, elem_bytes(dtype));
@@ -89,22 +92,23 @@ int allow_lds(K kernel, int bytes, int device, std::atomic<bool>* allowed)
     return GEMM_RS_OK;
 }
 
+// How a product runs: tiles of `tile` x `tile`, or the kernel for few rows, 16 or 32 of them at a time.
+struct Fp8Form {
+    int tile, stages;
+    int64_t tiles_m, tiles_n, tiles, grid;
+};
+
 template <int W, int NS, int MODE, class T>
-int tile_launch(Fp8Args& a, int64_t tiles_m, int device, void* stream)
+int tile_launch(Fp8Args& a, const Fp8Form& f, int device, void* stream)
 {
     typedef Fp8Tile<W, NS, MODE> Tile;
-    constexpr int kRows = Tile::kRows;
     static std::atomic<bool> allowed[kMaxDevices];
     const int rc = allow_lds(fp8_kernel<W, NS, MODE, T>, Tile::kLds, device, allowed);
     if (rc != GEMM_RS_OK) return rc;
-    a.tiles_n = (int)ceil_div(a.N, kRows);
-    a.tiles_m = (int)tiles_m;
-    int64_t grid = ceil_div(tiles_m * a.tiles_n, 8) * 8 * (MODE == kSums ? a.E : 1);
-    if (grid >= int64_t(1) << 31) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;  // tiles are counted in 32 bits
-    if (Tile::kKeeps && grid > kCus) grid = kCus;
-    if (grid * 256 > kMaxThreads) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    a.tiles_n = (int)f.tiles_n;
+    a.tiles_m = (int)f.tiles_m;
     void* p[] = {&a};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fp8_kernel<W, NS, MODE, T>), dim3((unsigned)grid), dim3(256), p,
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fp8_kernel<W, NS, MODE, T>), dim3((unsigned)f.grid), dim3(256), p,
                                          Tile::kLds, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? GEMM_RS_OK : hip_fail(e, "fp8_kernel");
 }
@@ -119,13 +123,11 @@ bool takes_few(int64_t M, int64_t N, int64_t E)
 }
 
 template <int MF, int MODE, class X, class T>
-int few_launch(const Fp8Args& a, void* stream)
+int few_launch(const Fp8Args& a, const Fp8Form& f, void* stream)
 {
     constexpr int kWaves = 8;
-    int64_t tiles = ceil_div(a.M, 16 * MF);
-    if (MODE != kDense) tiles = a.M / (16 * MF) + (a.E < a.M ? a.E : a.M);
-    return launch(fp8_few_kernel<kWaves, MF, MODE, X, T>, dim3((unsigned)ceil_div(a.N, kFewTile), (unsigned)tiles), 64 * kWaves, a,
-                  stream, "fp8_few_kernel");
+    return launch(fp8_few_kernel<kWaves, MF, MODE, X, T>, dim3((unsigned)f.tiles_n, (unsigned)f.tiles_m), 64 * kWaves, a, stream,
+                  "fp8_few_kernel");
 }
 
 // 0: tiles of 256 x 256, 1: of 128 x 128 with two workgroups per CU, 2: with one: by the time of their rounds of tiles over
@@ -146,49 +148,63 @@ int tile_choice(bool exact, int64_t big, int64_t small, int64_t steps)
     return cost[1] < cost[2] ? 1 : 2;
 }
 
-template <int MODE, class T>
-int product(Fp8Args& a, int device, void* stream)
+// rows: of the experts' (kSums), whose steps are not known here, but their number on average
+int form_of(int mode, int out_dtype, int64_t M, int64_t N, int64_t K, int64_t E, int64_t rows, Fp8Form& f)
 {
-    if constexpr (MODE != kSums) {
-        if (takes_few(a.M, a.N, a.E)) {
-            if (MODE != kDense || a.M <= kFewRows) return few_launch<1, MODE, Fp8Few, T>(a, stream);
-            if constexpr (MODE == kDense) return few_launch<2, MODE, Fp8Few, T>(a, stream);
-        }
-    }
+    const bool exact = out_dtype == GEMM_RS_DTYPE_F32, grouped = mode == kByExpert || mode == kGather;
+    const int64_t experts = E < M ? E : M;  // that can have a row
     // rows of tiles: exact, or a bound, and what to expect
-    constexpr bool kGrouped = MODE == kByExpert || MODE == kGather;
-    const int64_t experts = a.E < a.M ? a.E : a.M;  // that can have a row
-    auto rows_of = [&](int64_t edge) { return kGrouped ? a.M / edge + experts : ceil_div(a.M, edge); };
+    auto rows_of = [&](int64_t edge) { return grouped ? M / edge + experts : ceil_div(M, edge); };
     auto tiles = [&](int64_t edge) {
-        return (kGrouped ? a.M / edge + (experts + 1) / 2 : rows_of(edge)) * ceil_div(a.N, edge) * (MODE == kSums ? a.E : 1);
+        return (grouped ? M / edge + (experts + 1) / 2 : rows_of(edge)) * ceil_div(N, edge) * (mode == kSums ? E : 1);
     };
-    switch (tile_choice(fp8_exact<T>, tiles(256), tiles(128), MODE == kSums ? a.rows / a.E / kFp8Block + 1 : a.steps)) {
-    case 0: return tile_launch<4, 2, MODE, T>(a, rows_of(256), device, stream);
-    case 1: return tile_launch<2, 2, MODE, T>(a, rows_of(128), device, stream);
-    default:
-        if constexpr (fp8_exact<T>) return tile_launch<2, 2, MODE, T>(a, rows_of(128), device, stream);
-        else return tile_launch<2, 4, MODE, T>(a, rows_of(128), device, stream);
+    if (mode != kSums && takes_few(M, N, E)) {
+        const int few = mode == kDense && M > kFewRows ? 2 * kFewRows : kFewRows;
+        f = {few, 0, rows_of(few), ceil_div(N, kFewTile)};
+        f.tiles = f.grid = f.tiles_m * f.tiles_n;
+        return GEMM_RS_OK;
     }
+    const int choice = tile_choice(exact, tiles(256), tiles(128), mode == kSums ? rows / E / kFp8Block + 1 : blocks_of(K));
+    const int edge = choice == 0 ? 256 : 128;
+    f = {edge, choice == 2 && !exact ? 4 : 2, rows_of(edge), ceil_div(N, edge)};
+    f.tiles = f.tiles_m * f.tiles_n * (mode == kSums ? E : 1);
+    f.grid = ceil_div(f.tiles_m * f.tiles_n, 8) * 8 * (mode == kSums ? E : 1);
+    if (f.grid >= int64_t(1) << 31) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;  // tiles are counted in 32 bits
+    if (choice == 0 && f.grid > kCus) f.grid = kCus;
+    return f.grid * 256 > kMaxThreads ? GEMM_RS_ERR_UNSUPPORTED_SHAPE : GEMM_RS_OK;
+}
+
+template <int MODE, class T>
+int product(Fp8Args& a, const Fp8Form& f, int device, void* stream)
+{
+    if constexpr (MODE != kSums)
+        if (f.tile == kFewRows) return few_launch<1, MODE, Fp8Few, T>(a, f, stream);
+    if constexpr (MODE == kDense)
+        if (f.tile == 2 * kFewRows) return few_launch<2, MODE, Fp8Few, T>(a, f, stream);
+    if (f.tile == 256) return tile_launch<4, 2, MODE, T>(a, f, device, stream);
+    if constexpr (!fp8_exact<T>)
+        if (f.stages == 4) return tile_launch<2, 4, MODE, T>(a, f, device, stream);
+    return tile_launch<2, 2, MODE, T>(a, f, device, stream);
 }
 
 // The product of a few rows that are quantised on the way: x and x_pitch are the matrix itself.
 template <int MODE>
-int few_of(int x_dtype, int out_dtype, const Fp8Args& a, void* stream)
+int few_of(int x_dtype, int out_dtype, const Fp8Args& a, const Fp8Form& f, void* stream)
 {
-    if (x_dtype == GEMM_RS_DTYPE_F32) return few_launch<1, MODE, float, float>(a, stream);
+    if (x_dtype == GEMM_RS_DTYPE_F32) return few_launch<1, MODE, float, float>(a, f, stream);
     if (x_dtype == GEMM_RS_DTYPE_F16)
-        return out_dtype == GEMM_RS_DTYPE_F32 ? few_launch<1, MODE, _Float16, float>(a, stream)
-                                              : few_launch<1, MODE, _Float16, _Float16>(a, stream);
-    return out_dtype == GEMM_RS_DTYPE_F32 ? few_launch<1, MODE, __bf16, float>(a, stream)
-                                          : few_launch<1, MODE, __bf16, __bf16>(a, stream);
+        return out_dtype == GEMM_RS_DTYPE_F32 ? few_launch<1, MODE, _Float16, float>(a, f, stream)
+                                              : few_launch<1, MODE, _Float16, _Float16>(a, f, stream);
+    return out_dtype == GEMM_RS_DTYPE_F32 ? few_launch<1, MODE, __bf16, float>(a, f, stream)
+                                          : few_launch<1, MODE, __bf16, __bf16>(a, f, stream);
 }
 
 template <int MODE>
-int product_of(int out_dtype, Fp8Args& a, int device, void* stream)
+int product_of(int out_dtype, Fp8Args& a, const Fp8Form& f, int device, void* stream)
 {
-    return out_dtype == GEMM_RS_DTYPE_BF16  ? product<MODE, __bf16>(a, device, stream)
-           : out_dtype == GEMM_RS_DTYPE_F16 ? product<MODE, _Float16>(a, device, stream)
-                                            : product<MODE, float>(a, device, stream);
+    return out_dtype == GEMM_RS_DTYPE_BF16  ? product<MODE, __bf16>(a, f, device, stream)
+           : out_dtype == GEMM_RS_DTYPE_F16 ? product<MODE, _Float16>(a, f, device, stream)
+                                            : product<MODE, float>(a, f, device, stream);
 }
 
 bool fp8_args_ok(const gemm_rs_fp8_args* g)
@@ -212,17 +228,29 @@ bool few_raw(const gemm_rs_fp8_args& g)
 // q and scales of x in the workspace
 size_t quant_bytes(int64_t rows, int64_t K) { return (size_t)(up16(GEMM_RS_FP8_Q_BYTES(rows, K)) + up16(scale_bytes(rows, K))); }
 
-int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t workspace_bytes, void* stream)
+// The sizes and the kind of a product, and how it runs.
+int fp8_form(const gemm_rs_fp8_args* g, Fp8Form& f)
 {
     if (!fp8_args_ok(g)) return GEMM_RS_ERR_INVALID_ARG;
-    if (experts ? g->E < 1 || !g->offsets : g->E != 0 || g->offsets || g->tokens) return GEMM_RS_ERR_INVALID_ARG;
+    if (g->E ? !g->offsets : g->offsets || g->tokens) return GEMM_RS_ERR_INVALID_ARG;
     if (g->tokens ? g->x_rows == 0 && g->M > 0 : g->x_rows != g->M) return GEMM_RS_ERR_INVALID_ARG;
-    const int64_t blocks = blocks_of(g->K), pitch = blocks * kFp8Block;
     if (g->M >= kMaxRows || g->x_rows >= kMaxRows || g->N > kMaxWidth || g->K > kMaxWidth || g->E > GEMM_RS_ROUTE_MAX_EXPERTS ||
         scale_bytes(g->x_rows, g->K) > kMaxResource || scale_bytes(g->N, g->K) > kMaxResource ||
-        (g->tokens && g->x_rows * pitch > kMaxResource))
+        (g->tokens && GEMM_RS_FP8_Q_BYTES(g->x_rows, g->K) > kMaxResource))
         return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    f = {};
     if (g->M == 0) return GEMM_RS_OK;
+    if (g->x_dtype != GEMM_RS_DTYPE_FP8 && !quant_fits(g->x_rows, g->K)) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    return form_of(g->E == 0 ? kDense : g->tokens ? kGather : kByExpert, g->out_dtype, g->M, g->N, g->K, g->E, 0, f);
+}
+
+int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (g && experts != (g->E != 0)) return GEMM_RS_ERR_INVALID_ARG;
+    Fp8Form form;
+    int rc = fp8_form(g, form);
+    if (rc != GEMM_RS_OK || g->M == 0) return rc;
+    const int64_t blocks = blocks_of(g->K), pitch = blocks * kFp8Block;
     const bool raw = g->x_dtype != GEMM_RS_DTYPE_FP8;
     Checker c;
     c.need(g->x, raw ? elem_bytes(g->x_dtype) : 16);
@@ -244,15 +272,13 @@ int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t
         else c.need(workspace, 16);
     }
     if (c.code != GEMM_RS_OK) return c.code;
-    int device = 0, rc = check_device(&device);
-    if (rc != GEMM_RS_OK) return rc;
+    int device = 0;
+    if ((rc = check_device(&device)) != GEMM_RS_OK) return rc;
     Fp8Args a = {};
     a.x = static_cast<const uint8_t*>(g->x);
     a.xs = static_cast<const uint8_t*>(g->x_scales);
     const bool few = few_raw(*g);
     if (raw && !few) {
-        rc = quant_check(g->x_dtype, g->x_rows, g->K, g->x, g->x_stride, workspace, workspace);
-        if (rc != GEMM_RS_OK) return rc;
         uint8_t* q = static_cast<uint8_t*>(workspace);
         uint8_t* s = q + up16(g->x_rows * pitch);
         rc = quant_rows(g->x_dtype, g->x_rows, g->K, g->x, g->x_stride, q, s, stream);
@@ -283,11 +309,12 @@ int fp8_product(const gemm_rs_fp8_args* g, bool experts, void* workspace, size_t
     a.xs_pitch = (int)pitch_of(g->x_rows);
     a.ws_pitch = (int)pitch_of(g->N);
     if (few)
-        return !experts    ? few_of<kDense>(g->x_dtype, g->out_dtype, a, stream)
-               : g->tokens ? few_of<kGather>(g->x_dtype, g->out_dtype, a, stream)
-                           : few_of<kByExpert>(g->x_dtype, g->out_dtype, a, stream);
-    if (!experts) return product_of<kDense>(g->out_dtype, a, device, stream);
-    return g->tokens ? product_of<kGather>(g->out_dtype, a, device, stream) : product_of<kByExpert>(g->out_dtype, a, device, stream);
+        return !experts    ? few_of<kDense>(g->x_dtype, g->out_dtype, a, form, stream)
+               : g->tokens ? few_of<kGather>(g->x_dtype, g->out_dtype, a, form, stream)
+                           : few_of<kByExpert>(g->x_dtype, g->out_dtype, a, form, stream);
+    return !experts    ? product_of<kDense>(g->out_dtype, a, form, device, stream)
+           : g->tokens ? product_of<kGather>(g->out_dtype, a, form, device, stream)
+                       : product_of<kByExpert>(g->out_dtype, a, form, device, stream);
 }
 
 bool wgrad_ok(const gemm_rs_experts_wgrad_args* g)
@@ -304,6 +331,13 @@ bool wgrad_fits(const gemm_rs_experts_wgrad_args& g)
     return g.M < kMaxRows && g.x_rows < kMaxRows && g.N <= kMaxWidth && g.K <= kMaxWidth && g.E <= GEMM_RS_ROUTE_MAX_EXPERTS &&
            wgrad_blocks(g) * kFp8Block <= kMaxResource / 256 && pitch_of(g.N) * wgrad_blocks(g) <= kMaxResource &&
            pitch_of(g.K) * wgrad_blocks(g) <= kMaxResource && ceil_div(g.N, 64) <= 65535 && ceil_div(g.K, 64) <= 65535;
+}
+
+int wgrad_form(const gemm_rs_experts_wgrad_args* g, Fp8Form& f)
+{
+    if (!wgrad_ok(g) || (!g->tokens && g->x_rows != g->M)) return GEMM_RS_ERR_INVALID_ARG;
+    if (!wgrad_fits(*g)) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    return form_of(kSums, g->out_dtype, g->N, g->K, 0, g->E, g->x_rows > 0 ? g->M : 0, f);
 }
 
 int64_t wgrad_operand(int64_t rows, int64_t blocks) { return up16(rows * blocks * kFp8Block) + up16(pitch_of(rows) * blocks); }
@@ -366,6 +400,16 @@ size_t gemm_rs_fp8_workspace(const gemm_rs_fp8_args* g)
     return quant_bytes(g->x_rows, g->K);
 }
 
+int gemm_rs_fp8_plan(const gemm_rs_fp8_args* g, gemm_rs_fp8_info* info)
+{
+    Fp8Form f;
+    const int rc = fp8_form(g, f);
+    if (rc != GEMM_RS_OK) return rc;
+    if (!info) return GEMM_RS_ERR_INVALID_ARG;
+    *info = {f.tile, f.stages, g->M > 0 && few_raw(*g), (int32_t)f.tiles, (int32_t)f.grid};
+    return GEMM_RS_OK;
+}
+
 int gemm_rs_fp8_linear(const gemm_rs_fp8_args* g, void* workspace, size_t workspace_bytes, void* stream)
 {
     return fp8_product(g, false, workspace, workspace_bytes, stream);
@@ -383,10 +427,21 @@ size_t gemm_rs_experts_wgrad_workspace(const gemm_rs_experts_wgrad_args* g)
     return (size_t)(wgrad_operand(g->N, blocks) + wgrad_operand(g->K, blocks));
 }
 
+int gemm_rs_experts_wgrad_plan(const gemm_rs_experts_wgrad_args* g, gemm_rs_fp8_info* info)
+{
+    Fp8Form f;
+    const int rc = wgrad_form(g, f);
+    if (rc != GEMM_RS_OK) return rc;
+    if (!info) return GEMM_RS_ERR_INVALID_ARG;
+    *info = {f.tile, f.stages, 0, (int32_t)f.tiles, (int32_t)f.grid};
+    return GEMM_RS_OK;
+}
+
 int gemm_rs_experts_wgrad(const gemm_rs_experts_wgrad_args* g, void* workspace, size_t workspace_bytes, void* stream)
 {
-    if (!wgrad_ok(g) || (!g->tokens && g->x_rows != g->M)) return GEMM_RS_ERR_INVALID_ARG;
-    if (!wgrad_fits(*g)) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
+    Fp8Form form;
+    int rc = wgrad_form(g, form);
+    if (rc != GEMM_RS_OK) return rc;
     const bool any = g->M > 0 && g->x_rows > 0;
     Checker c;
     c.need(g->offsets, 4);
@@ -406,8 +461,8 @@ int gemm_rs_experts_wgrad(const gemm_rs_experts_wgrad_args* g, void* workspace, 
         else c.need(workspace, 16);
     }
     if (c.code != GEMM_RS_OK) return c.code;
-    int device = 0, rc = check_device(&device);
-    if (rc != GEMM_RS_OK) return rc;
+    int device = 0;
+    if ((rc = check_device(&device)) != GEMM_RS_OK) return rc;
     Fp8Args a = {};
     const int64_t blocks = any ? wgrad_blocks(*g) : 0;
     if (any) {
@@ -439,7 +494,7 @@ int gemm_rs_experts_wgrad(const gemm_rs_experts_wgrad_args* g, void* workspace, 
     a.E = (int)g->E;
     a.xs_pitch = (int)pitch_of(g->N);
     a.ws_pitch = (int)pitch_of(g->K);
-    return product_of<kSums>(g->out_dtype, a, device, stream);
+    return product_of<kSums>(g->out_dtype, a, form, device, stream);
 }
 
 }  // extern "C"

@@ -33,8 +33,9 @@ SCORE_SIGMOID = 1
 ROUTE_MAX_EXPERTS = 1024
 ROUTE_MAX_CHOICES = 64
 
-EXPORTS = ("gemm_rs_fp8_quant", "gemm_rs_fp8_quant_transposed", "gemm_rs_fp8_pack", "gemm_rs_fp8_workspace",
-           "gemm_rs_fp8_linear", "gemm_rs_experts_linear", "gemm_rs_experts_wgrad_workspace", "gemm_rs_experts_wgrad",
+EXPORTS = ("gemm_rs_fp8_quant", "gemm_rs_fp8_quant_transposed", "gemm_rs_fp8_pack", "gemm_rs_fp8_plan", "gemm_rs_fp8_workspace",
+           "gemm_rs_fp8_linear", "gemm_rs_experts_linear", "gemm_rs_experts_wgrad_plan", "gemm_rs_experts_wgrad_workspace",
+           "gemm_rs_experts_wgrad",
            "gemm_rs_route_validate", "gemm_rs_expert_plan_workspace", "gemm_rs_route", "gemm_rs_expert_plan",
            "gemm_rs_route_backward", "gemm_rs_combine", "gemm_rs_combine_backward")
 
@@ -62,6 +63,10 @@ class gemm_rs_expert_plan_args(ctypes.Structure):
     _fields_ = [("offsets", _vp), ("tokens", _vp), ("slots", _vp)]
 
 
+class gemm_rs_fp8_info(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("tile", "stages", "quantises", "tiles", "workgroups")]
+
+
 # The argument blocks as calls pack them.
 _FP8_ARGS = struct.Struct("2i5qQqQQQQQQqQq")
 _WGRAD_ARGS = struct.Struct("2i5qQqQqQQQQ")
@@ -79,9 +84,11 @@ def lib():
         L.gemm_rs_fp8_quant.argtypes = [_i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp]
         L.gemm_rs_fp8_quant_transposed.argtypes = [_i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp]
         L.gemm_rs_fp8_pack.argtypes = [_i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]
+        L.gemm_rs_fp8_plan.argtypes = [a, ctypes.POINTER(gemm_rs_fp8_info)]
         L.gemm_rs_fp8_workspace.argtypes = [a]
         L.gemm_rs_fp8_linear.argtypes = [a, _vp, _size, _vp]
         L.gemm_rs_experts_linear.argtypes = [a, _vp, _size, _vp]
+        L.gemm_rs_experts_wgrad_plan.argtypes = [a, ctypes.POINTER(gemm_rs_fp8_info)]
         L.gemm_rs_experts_wgrad_workspace.argtypes = [a]
         L.gemm_rs_experts_wgrad.argtypes = [a, _vp, _size, _vp]
         L.gemm_rs_route_validate.argtypes = [a]
