@@ -70,7 +70,8 @@ int gemm_rs_fp8_pack(int32_t dtype, int64_t E, int64_t N, int64_t K, int32_t tra
  * Before it, an F32 result is within (K + 2) 2^-24 sum |x^| |w^|.  For BF16 and F16
  * results the products of eight neighbouring inputs are lined up with the largest of
  * them, and what lies below 2^-13 of that is dropped from each: to the bound comes
- * 2^-10 of the largest product of every eight inputs, summed over K.
+ * 2^-10 of the largest product of every eight inputs, summed over K (which is up to two
+ * half steps of F16, or a quarter of BF16's, also where nothing cancels).
  * gemm_rs_fp8_linear: E, offsets and tokens are 0 and x_rows is M.
  * gemm_rs_experts_linear: rows offsets[e] .. offsets[e + 1] - 1 take the weights of
  * expert e; row m's input is row m of x, or row tokens[m] where tokens are given (zeros

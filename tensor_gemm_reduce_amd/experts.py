@@ -274,6 +274,9 @@ def _product(name, x, weight, routing, rows, add, out, dtype, stream):
 def fp8_linear(x, weight: Fp8, *, add=None, out=None, dtype=None, stream=None):
     """out [M][N] = x w^T (+ add), FP32 accumulation, rounded once.
 
+    For bfloat16 and float16 results the products of eight neighbouring inputs lose what lies below 2^-13 of the largest of
+    them, together less than 2^-10 of it: up to two half steps of float16, a quarter of bfloat16's.  dtype=torch.float32 keeps every
+    product whole, at half the rate.
     x: [M][K] bfloat16, float16 or float32, quantised by the call as fp8_quant does, or an Fp8.  weight: an Fp8 [N][K].
     dtype: of out (default: x's; bfloat16 for an Fp8).  add: float32 [M][N] or None, with a float32 out, which may be it.
     The gradients of y = x w^T: fp8_linear(dy, fp8_pack(w, transpose=True)) and
@@ -418,6 +421,7 @@ def experts_linear(x, weight: Fp8, routing: Routing, *, rows=False, add=None, ou
 
     x: [T][K], a token's inputs (gathered by the product), or with rows=True [R][K], in the order of the rows: a tensor
     or an Fp8 as in fp8_linear.  weight: an Fp8 of E experts.
+    Products are fp8_linear's, as are their roundings.
     The gradient of the rows' inputs: experts_linear(dy, fp8_pack(w, transpose=True), routing, rows=True), which
     combine(.., None) adds up over a token's rows.
     """
@@ -427,7 +431,8 @@ def experts_linear(x, weight: Fp8, routing: Routing, *, rows=False, add=None, ou
 def experts_wgrad(dy, x, routing: Routing, *, rows=False, add=None, out=None, dtype=torch.float32, stream=None):
     """The weights' gradients [E][N][K] = dy^T x (+ add) of every expert, both in 8 bits in blocks of 128 of its rows.
 
-    dy: [R][N], x: [T][K] or with rows=True [R][K], of one type.  dtype: float32 or dy's (out's, if given).
+    dy: [R][N], x: [T][K] or with rows=True [R][K], of one type.  dtype: float32, every product whole, or dy's, with fp8_linear's
+    roundings (out's, if given).
     add: float32 [E][N][K], contiguous, or None, with a float32 out, which may be it.
     """
     M, N = _two(dy, "dy")
