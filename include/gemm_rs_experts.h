@@ -154,7 +154,8 @@ int gemm_rs_experts_wgrad(const gemm_rs_experts_wgrad_args *args, void *workspac
  * experts with the largest c, largest first, ties to the lowest index, are chosen:
  *   weights[t][j] = scale s_j  (renormalise: scale s_j / (sum_i s_i + 1e-20))
  * and -1 with weight 0 where fewer than k are on.  c is compared in 64 bits; without
- * a bias and groups the logits are compared.  A NaN counts as the lowest of those on. */
+ * a bias and groups the logits are compared.  A NaN counts as the lowest of those on.
+ * Weights are of scores in FP32, which are 0 where it does not hold them. */
 typedef struct gemm_rs_route_config {
     int32_t dtype;       /* of the logits: BF16, F16 or F32                */
     int32_t E;           /* 1 .. GEMM_RS_ROUTE_MAX_EXPERTS                 */
