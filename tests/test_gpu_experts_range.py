@@ -164,6 +164,19 @@ def test_experts_wgrad_of_operands_at_both_ends(T, E, N, K):
         near(dw[e], ref.quantised(dy[r], 128, 1).t().contiguous().cuda(), ref.quantised(x[tokens[r]], 128, 1).t().contiguous().cuda())
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 40, 300), (20, 33, 1300), (130, 150, 1300), (200, 120, 384)])
+def test_16_bit_results_of_blocks_at_both_ends(M, N, K):
+    """The scales are the matrix instruction's own operands there: every byte from 1 on, and what eights of products drop."""
+    g = gen(K)
+    blocks = (K + 127) // 128
+    x, xv = operand(g, exponents(g, M, blocks), K)
+    w, wv = operand(g, partners(g, N, blocks), K)
+    want, mag, top = (t.cuda() for t in ref.product(xv.cpu(), wv.cpu()))
+    sums, drop = (K + 2) * 2.0 ** -24 * mag, 2.0 ** -10 * top
+    off = (ex.fp8_linear(x, w, dtype=BF16).double() - want).abs()
+    assert not (off > 2.0 ** -8 * (want.abs() + drop + sums) + drop + sums).any()
+
+
 def test_blocks_of_zeros_beside_others():
     """Zeros at the lowest scale, as a caller's own matrices may have them, change nothing."""
     g = gen(3)
