@@ -762,11 +762,11 @@ struct Fp8Store {
     }
 };
 
-// The results of a wave with scales that take its values out of BF16, computed and stored again: the products of a block are
-// summed as they are, in FP32, and the sum is scaled by both scales at once.  A tile of 32 x 32 at a time, straight from
-// memory: for values below 2^-103 and above 2^120, which programs seldom have: with one such row in
-// every tile 4096 x 4096 x 384 takes 127 us instead of 27, 8192 x 8192 x 1024 890 instead of 140.  Looking for them costs 1 to 3%
-// (501 x 7168 x 8192 59 / 61 us, 8192 x 8192 x 1024 134 / 135).
+// The results of a wave with scales that may take its values out of BF16, computed again: the products of a block are summed as
+// they are, in FP32, and the sum is scaled by both scales at once.  A tile of 32 x 32 at a time, straight from memory: for values
+// below 2^-103 and above 2^120, which programs seldom have.  With one such row in every tile 4096 x 4096 x 384 takes 127 us
+// instead of 27, 8192 x 8192 x 1024 890 instead of 140; looking for them costs 1 to 3% (501 x 7168 x 8192 59 / 61 us, 8192 x
+// 8192 x 1024 134 / 135).
 template <int W, int MODE>
 __device__ __forceinline__ void fp8_scaled_apart(const Fp8Args& a, const Fp8Place& p, int64_t shift, int64_t m0, int n0)
 {

@@ -135,8 +135,8 @@ def _up(n, unit):
 class Fp8:
     """A matrix [rows][K], or E of them, in e4m3 with a power-of-two scale for each block of 128 columns of a row:
     q float8_e4m3fn [(E,) rows, K rounded up to 128], zeros past K; scales uint8 [(E,) blocks, rows + 3 rounded up to 4],
-    e + 127 of the scale 2^e of a row's block (bytes past the rows are not used).  A block with an infinity or a NaN
-    stands for NaN."""
+    e + 127 of the scale 2^e of a row's block (bytes past the rows are not used; 127 for a block of zeros).  A block with an
+    infinity or a NaN stands for NaN."""
 
     __slots__ = ("q", "scales", "E", "rows", "K")
 
